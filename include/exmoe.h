@@ -345,6 +345,55 @@ int exmoe_moe_forward_cached(const exmoe_bf16* x, const int32_t* topk_ids, const
                              hipStream_t stream);
 
 /* ------------------------------------------------------------------------------------
+ * Products grouped by expert over ragged segments (device, asynchronous): the matrix
+ * product of an expert layer on plain row-major weights, with its two gradients, for
+ * experts that are not packed (dense bf16 or fp16 experts before exmoe_quantize_pack, and
+ * the training of them). Segment e holds the rows expert_offsets[e] <= s <
+ * expert_offsets[e+1], as exmoe_group_tokens writes them.
+ *   exmoe_grouped_mm        y[s, n]  = sum_k x[src(s), k] w[e, n, k]
+ *   exmoe_grouped_mm_dgrad  dx[s, k] = sum_n dy[s, n] w[e, n, k]; with flat_to_sorted,
+ *                           dx[t, k] = that summed over the k rows of token t, slot order
+ *   exmoe_grouped_mm_wgrad  dw[e, n, k] = sum_{s in segment e} dy[s, n] x[src(s), k]
+ * src(s) = row_index[s] / row_div (with sorted_flat and k: the token of a routed row), or s
+ * when row_index is NULL. Products of 16-bit operands are summed in fp32 and rounded once
+ * (to nearest even) when the output is 16 bits wide.
+ *
+ * Sizes: any rows >= 0, N, K >= 1 (multiples of 8 with 16-byte aligned rows run on wider
+ * loads), 1 <= E <= 256; empty segments are allowed anywhere (exmoe_grouped_mm_wgrad
+ * writes zeros for them). ld* are elements between rows, *_stride elements between
+ * experts; the last axis is contiguous. Pointers need the alignment of their elements only
+ * (workspace: 16 bytes). Operands share `dtype` (bf16 or fp16); out_dtype is that type or
+ * fp32. Outputs must not overlap inputs.
+ * Offsets are read on the device and clamped to [0, rows]. Rows of y and dx outside every
+ * segment are left as they are; with flat_to_sorted every token is written, and an entry
+ * outside the segments (-1 of an ungrouped row) adds nothing. A row_index that leads
+ * outside x's x_rows rows reads as a row of zeros.
+ * The sums of one call are made in a fixed order: equal calls give equal bits.
+ * Workspace: exmoe_grouped_mm_workspace_bytes(op, rows, N, K, E, k) bytes (0: it may be
+ * NULL), needs no initialization, is not kept; k is exmoe_grouped_mm_dgrad's k when it sums
+ * per token, else 0. Calls that overlap in time must not share one.
+ * ---------------------------------------------------------------------------------- */
+enum { EXMOE_DTYPE_BF16 = 0, EXMOE_DTYPE_FP16 = 1, EXMOE_DTYPE_FP32 = 2 };
+enum exmoe_grouped_op { EXMOE_GROUPED_MM = 0, EXMOE_GROUPED_DGRAD = 1, EXMOE_GROUPED_WGRAD = 2 };
+
+size_t exmoe_grouped_mm_workspace_bytes(int op, int rows, int N, int K, int E, int k);
+
+int exmoe_grouped_mm(const void* x, size_t ldx, int x_rows, const int32_t* row_index, int row_div,
+                     const int32_t* expert_offsets, const void* w, size_t ldw, size_t w_stride, int rows, int N, int K,
+                     int E, int dtype, int out_dtype, void* y, size_t ldy, void* workspace, size_t ws_bytes,
+                     hipStream_t stream);
+
+int exmoe_grouped_mm_dgrad(const void* dy, size_t lddy, const int32_t* expert_offsets, const void* w, size_t ldw,
+                           size_t w_stride, const int32_t* flat_to_sorted, int k, int rows, int N, int K, int E,
+                           int dtype, int out_dtype, void* dx, size_t lddx, void* workspace, size_t ws_bytes,
+                           hipStream_t stream);
+
+int exmoe_grouped_mm_wgrad(const void* dy, size_t lddy, const void* x, size_t ldx, int x_rows, const int32_t* row_index,
+                           int row_div, const int32_t* expert_offsets, int rows, int N, int K, int E, int dtype,
+                           int out_dtype, void* dw, size_t lddw, size_t dw_stride, void* workspace, size_t ws_bytes,
+                           hipStream_t stream);
+
+/* ------------------------------------------------------------------------------------
  * Per-kernel timing for benchmarks (not part of the layer's semantics). While enabled,
  * each kernel of the library is launched with a hipEvent pair that stamps that kernel's
  * own start and end on its launch stream (hipExtLaunchKernelGGL; skipped on a stream that

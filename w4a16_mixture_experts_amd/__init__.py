@@ -42,6 +42,8 @@ PATH_AUTO, PATH_DECODE, PATH_PREFILL, PATH_SEQUENTIAL = 0, 1, 2, 3
 WEIGHTS_BF16 = 0x100       # flag: the bank holds dense bf16 experts (bf16_pack)
 DEBUG_COUNTERS = 0x200     # flag: expert kernels count the rows they ran per expert (workspace_rows)
 CACHE_DRY_RUN = 1
+DTYPE_BF16, DTYPE_FP16, DTYPE_FP32 = 0, 1, 2
+GROUPED_MM, GROUPED_DGRAD, GROUPED_WGRAD = 0, 1, 2
 
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
@@ -101,6 +103,13 @@ _SIGS = {
     "exmoe_span_clear": (_i, []),
     "exmoe_span_read": (_i, [ctypes.c_char_p, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_uint64)]),
     "exmoe_device_copy": (_i, [_vp, _vp, _sz, _vp]),
+    "exmoe_grouped_mm_workspace_bytes": (_sz, [_i] * 6),
+    "exmoe_grouped_mm": (_i, [_vp, _sz, _i, _vp, _i, _vp, _vp, _sz, _sz, _i, _i, _i, _i, _i, _i, _vp, _sz, _vp, _sz,
+                              _vp]),
+    "exmoe_grouped_mm_dgrad": (_i, [_vp, _sz, _vp, _vp, _sz, _sz, _vp, _i, _i, _i, _i, _i, _i, _i, _vp, _sz, _vp, _sz,
+                                    _vp]),
+    "exmoe_grouped_mm_wgrad": (_i, [_vp, _sz, _vp, _sz, _i, _vp, _i, _vp, _i, _i, _i, _i, _i, _i, _vp, _sz, _sz, _vp,
+                                    _sz, _vp]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -367,6 +376,146 @@ def moe_layer_noalloc(x, w_router, bank: ExpertBank, I: int, k: int, buffers: La
                                         _ptr(b.offsets), _ptr(b.sorted_flat), _ptr(b.flat_to_sorted), _ptr(b.y),
                                         _stream()))
     return b
+
+
+# ----------------------------------------------------------------------------- grouped products
+def _dtype_code(dtype) -> int:
+    torch = _torch()
+    codes = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_FP16, torch.float32: DTYPE_FP32}
+    if dtype not in codes:
+        raise ValueError(f"unsupported dtype {dtype}: bfloat16, float16 or float32")
+    return codes[dtype]
+
+
+def _rows_ld(name: str, t, ndim: int = 2) -> int:
+    """Elements between the rows of a GPU tensor whose last axis is contiguous."""
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} axes (got shape {tuple(t.shape)})")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last axis must be contiguous")
+    return t.stride(-2) if t.shape[-2] > 1 else max(t.stride(-2), t.shape[-1])
+
+
+def _expert_stride(t, ld: int) -> int:
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * ld)
+
+
+def _int32(name: str, t, like, numel: Optional[int] = None):
+    torch = _torch()
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.device != like.device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor on {like.device}")
+    if numel is not None and t.numel() != numel:
+        raise ValueError(f"{name} must have {numel} entries (got {t.numel()})")
+    return t.data_ptr()
+
+
+def _result(name: str, out, shape, dtype, like):
+    torch = _torch()
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    if tuple(out.shape) != tuple(shape) or out.dtype != dtype or out.device != like.device:
+        raise ValueError(f"{name} must be {tuple(shape)} {dtype} on {like.device}")
+    return out
+
+
+def _scratch(workspace, need: int, like):
+    """(pointer, bytes) of the caller's workspace, or of a new one of the needed size."""
+    if workspace is None:
+        if not need:
+            return None, 0, None
+        workspace = _torch().empty(need, dtype=_torch().uint8, device=like.device)
+    elif workspace.device != like.device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {like.device}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def _run_on(like, fn, *args):
+    """Calls a C entry point on the device of `like`, on that device's current stream."""
+    torch = _torch()
+    if like.device.index == torch.cuda.current_device():
+        _check(fn(*args, torch.cuda.current_stream().cuda_stream))
+    else:
+        with torch.cuda.device(like.device):
+            _check(fn(*args, torch.cuda.current_stream().cuda_stream))
+
+
+def _same(name: str, t, like):
+    if t.dtype != like.dtype or t.device != like.device:
+        raise ValueError(f"{name} must be {like.dtype} on {like.device}")
+
+
+def grouped_mm_workspace_bytes(op: int, rows: int, N: int, K: int, E: int, k: int = 0) -> int:
+    return _lib.exmoe_grouped_mm_workspace_bytes(op, rows, N, K, E, k)
+
+
+def grouped_mm(x, w, offsets, row_index=None, row_div: int = 1, out_dtype=None, y=None, workspace=None):
+    """y[s, :] = w[e] @ x[src(s), :] for the rows s of every expert's segment.
+
+    x [x_rows, K], w [E, N, K] (both bf16 or both fp16, last axis contiguous), offsets int32
+    [E + 1]; row_index int32 [rows] with src(s) = row_index[s] // row_div (sorted_flat and k
+    of a routed batch), or None for src(s) = s. Returns y [rows, N] in out_dtype (x's type
+    or fp32); its rows outside every segment are left as they are."""
+    ldx, ldw = _rows_ld("x", x), _rows_ld("w", w, 3)
+    _same("w", w, x)
+    E, N, K = w.shape
+    if x.shape[1] != K:
+        raise ValueError(f"x has {x.shape[1]} columns, w takes {K}")
+    rows = x.shape[0] if row_index is None else row_index.numel()
+    out_dtype = x.dtype if out_dtype is None else out_dtype
+    y = _result("y", y, (rows, N), out_dtype, x)
+    need = grouped_mm_workspace_bytes(GROUPED_MM, rows, N, K, E) if workspace is None else 0
+    ws, ws_bytes, _keep = _scratch(workspace, need, x)
+    _run_on(x, _lib.exmoe_grouped_mm, x.data_ptr(), ldx, x.shape[0], _int32("row_index", row_index, x), row_div,
+            _int32("offsets", offsets, x, E + 1), w.data_ptr(), ldw, _expert_stride(w, ldw), rows, N, K, E,
+            _dtype_code(x.dtype), _dtype_code(out_dtype), y.data_ptr(), _rows_ld("y", y), ws, ws_bytes)
+    return y
+
+
+def grouped_mm_dgrad(dy, w, offsets, flat_to_sorted=None, k: int = 1, out_dtype=None, dx=None, workspace=None):
+    """Gradient of grouped_mm with respect to x: dx[s, :] = dy[s, :] @ w[e] per row, or, with
+    flat_to_sorted int32 [T * k], summed over the k rows of each token (dx [T, K])."""
+    lddy, ldw = _rows_ld("dy", dy), _rows_ld("w", w, 3)
+    _same("w", w, dy)
+    E, N, K = w.shape
+    rows = dy.shape[0]
+    if dy.shape[1] != N:
+        raise ValueError(f"dy has {dy.shape[1]} columns, w gives {N}")
+    if flat_to_sorted is not None and (k < 1 or rows % k):
+        raise ValueError(f"dy's {rows} rows are no multiple of k = {k}")
+    out_dtype = dy.dtype if out_dtype is None else out_dtype
+    dx = _result("dx", dx, (rows if flat_to_sorted is None else rows // k, K), out_dtype, dy)
+    sum_k = 0 if flat_to_sorted is None else k
+    need = grouped_mm_workspace_bytes(GROUPED_DGRAD, rows, N, K, E, sum_k) if workspace is None else 0
+    ws, ws_bytes, _keep = _scratch(workspace, need, dy)
+    _run_on(dy, _lib.exmoe_grouped_mm_dgrad, dy.data_ptr(), lddy, _int32("offsets", offsets, dy, E + 1), w.data_ptr(),
+            ldw, _expert_stride(w, ldw), _int32("flat_to_sorted", flat_to_sorted, dy, rows), k, rows, N, K, E,
+            _dtype_code(dy.dtype), _dtype_code(out_dtype), dx.data_ptr(), _rows_ld("dx", dx), ws, ws_bytes)
+    return dx
+
+
+def grouped_mm_wgrad(dy, x, offsets, row_index=None, row_div: int = 1, out_dtype=None, dw=None, workspace=None):
+    """Gradient of grouped_mm with respect to w: dw[e] = sum over its rows of dy[s]^T x[src(s)],
+    zeros for an expert without rows. out_dtype defaults to fp32."""
+    torch = _torch()
+    lddy, ldx = _rows_ld("dy", dy), _rows_ld("x", x)
+    _same("x", x, dy)
+    rows, N = dy.shape
+    K, E = x.shape[1], offsets.numel() - 1
+    out_dtype = torch.float32 if out_dtype is None else out_dtype
+    dw = _result("dw", dw, (E, N, K), out_dtype, dy)
+    lddw = _rows_ld("dw", dw, 3)
+    need = grouped_mm_workspace_bytes(GROUPED_WGRAD, rows, N, K, E) if workspace is None else 0
+    ws, ws_bytes, _keep = _scratch(workspace, need, dy)
+    if row_index is None and x.shape[0] < rows:
+        raise ValueError(f"x has {x.shape[0]} rows, dy has {rows}")
+    _run_on(dy, _lib.exmoe_grouped_mm_wgrad, dy.data_ptr(), lddy, x.data_ptr(), ldx, x.shape[0],
+            _int32("row_index", row_index, dy, rows), row_div, _int32("offsets", offsets, dy, E + 1), rows, N, K, E,
+            _dtype_code(dy.dtype), _dtype_code(out_dtype), dw.data_ptr(), lddw, _expert_stride(dw, lddw), ws, ws_bytes)
+    return dw
 
 
 # ----------------------------------------------------------------------------- slot cache

@@ -1,0 +1,201 @@
+// Matrix-product tiles shared by the grouped products (grouped.hip) and the projection
+// with low-rank adapters (lora.hip): 16-bit operands, fp32 accumulation on MFMA.
+//
+// Every product here is D[p, q] = sum_r P(p, r) Q(q, r) with q contiguous in the output.
+// An operand is stored either with the summed axis contiguous ("rows": one row per p or q)
+// or with it outermost ("columns": one row per r, read transposed):
+//   forward          p = routed row (rows), q = output (rows of W),    r = K
+//   gradient of x    p = routed row (rows), q = input (columns of W),  r = N
+//   gradient of W    p = output (columns),  q = input (columns),       r = routed row
+// MFMA takes Q as its A operand and P as its B operand, so that a lane ends with four
+// consecutive q of one p: one 8-byte (16-bit outputs) or 16-byte (fp32) store.
+//
+// Both operands go from memory straight into LDS (global_load_lds, 16 bytes a lane).
+// LDS layout of a 64-deep slice:
+//   rows:    [row][64], the 16-byte chunk c of row i at position c ^ ((i >> 1) & 7): the 16
+//            rows of a fragment read (one chunk each) cover all 64 banks once;
+//   columns: [64][B], the 32-byte unit u of row r at position u ^ col_swz(r): the eight
+//            rows that 32 lanes of a transposing read touch cover all 64 banks once.
+#pragma once
+
+#include <type_traits>
+
+#include "common.h"
+#include "device.h"
+
+namespace exmoe {
+
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// Element types of the operands: bf16 or fp16 bit patterns in memory.
+struct ElemBF16 {
+  static __device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) { return mfma16(a, b, c); }
+  static __device__ __forceinline__ float to_f32(uint16_t v) { return bf16_to_f32(v); }
+  static __device__ __forceinline__ uint16_t from_f32(float v) { return f32_to_bf16(v); }
+  static __device__ __forceinline__ uint32_t pack2(float lo, float hi) { return pack_bf16x2(lo, hi); }
+};
+struct ElemFP16 {
+  static __device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0,
+                                                  0);
+  }
+  static __device__ __forceinline__ float to_f32(uint16_t v) { return (float)__builtin_bit_cast(_Float16, v); }
+  static __device__ __forceinline__ uint16_t from_f32(float v) { return __builtin_bit_cast(uint16_t, (_Float16)v); }
+  static __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    return (uint32_t)from_f32(lo) | ((uint32_t)from_f32(hi) << 16);
+  }
+};
+
+constexpr int kBK = 64;   // depth of one staged slice
+
+// Sixteen zero bytes: what a copy reads in place of elements past the summed axis (device
+// globals start zeroed; never written).
+static __device__ __attribute__((aligned(16))) uint16_t g_zero16[8];
+
+__device__ __forceinline__ void lds_copy16(const void* src, void* dst) {
+  __builtin_amdgcn_global_load_lds(src, (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
+}
+
+__device__ __forceinline__ int col_swz(int r) { return (r & 3) | (((r >> 3) & 1) << 2); }
+
+// Eight elements of a row-major matrix at any alignment: element i is used when i < n (and
+// ok), else it is zero. Reads only elements that are used, or the operand's first one.
+__device__ __forceinline__ uint4 load8_any(const uint16_t* base, size_t off, int n, bool ok) {
+  uint32_t v[8];
+#pragma unroll
+  for (int j = 0; j < 8; j++) {
+    const bool use = ok && j < n;
+    const uint16_t e = base[use ? off + j : 0];
+    v[j] = use ? e : 0u;
+  }
+  return make_uint4(v[0] | (v[1] << 16), v[2] | (v[3] << 16), v[4] | (v[5] << 16), v[6] | (v[7] << 16));
+}
+
+// Operand stored as rows (summed axis contiguous), B rows per slice, staged by NW waves.
+template <int B, int NW, bool ALIGNED>
+struct RowOperand {
+  static constexpr int kSlots = B / 8 / NW;   // copies per lane and slice (8 rows each)
+  static_assert(B % (8 * NW) == 0, "rows per slice");
+  const uint16_t* base;
+  size_t off[kSlots];        // element offset of the lane's row (clamped to a readable one)
+  int red;                   // length of the summed axis
+
+  // row_off(i): element offset of row i of the tile (any readable row past the end)
+  template <class F>
+  __device__ __forceinline__ void init(const uint16_t* b, int red_, int wave, int lane, F row_off) {
+    base = b;
+    red = red_;
+#pragma unroll
+    for (int i = 0; i < kSlots; i++) off[i] = row_off((i * NW + wave) * 8 + (lane >> 3));
+  }
+  __device__ __forceinline__ void stage(uint16_t* lds, int k0, int wave, int lane) const {
+#pragma unroll
+    for (int i = 0; i < kSlots; i++) {
+      const int row = (i * NW + wave) * 8 + (lane >> 3);
+      const int col = k0 + 8 * ((lane & 7) ^ ((row >> 1) & 7));
+      uint16_t* dst = lds + (i * NW + wave) * 8 * kBK;
+      if constexpr (ALIGNED) {
+        const uint16_t* src = base + off[i] + col;
+        if (k0 + kBK > red && col >= red) src = g_zero16;
+        lds_copy16(src, dst);
+      } else {
+        const uint4 v = load8_any(base, off[i] + col, red - col, true);
+        *reinterpret_cast<uint4*>(dst + 8 * lane) = v;
+      }
+    }
+  }
+  // fragment of rows r0..r0+15, summed positions 32 kk + 8 (lane / 16) + 0..7
+  static __device__ __forceinline__ bf16x8 frag(const uint16_t* lds, int r0, int kk, int lane) {
+    const int row = r0 + (lane & 15);
+    const int pos = (4 * kk + (lane >> 4)) ^ ((row >> 1) & 7);
+    return *reinterpret_cast<const bf16x8*>(lds + row * kBK + 8 * pos);
+  }
+};
+
+// Operand stored as columns (summed axis outermost), B columns per slice.
+template <int B, int NW, bool ALIGNED>
+struct ColOperand {
+  static constexpr int kChunks = B / 8;                 // 16-byte chunks per row
+  static constexpr int kRows = 64 / kChunks;            // rows per wave-wide copy
+  static constexpr int kSlots = kBK / (kRows * NW);
+  static_assert(B >= 128 && B <= 512 && kBK % (kRows * NW) == 0, "columns per slice");
+  const uint16_t* base;      // column 0 of the tile, row 0 of the summed axis
+  size_t ld;
+  int red;                   // rows of the summed axis
+  int ncols;                 // readable columns from base on
+
+  __device__ __forceinline__ void init(const uint16_t* b, size_t ld_, int red_, int ncols_) {
+    base = b;
+    ld = ld_;
+    red = red_;
+    ncols = ncols_;
+  }
+  // row_off(r, i): element offset of row r (0 <= r < red; i: the lane's slot), or ~0 for zeros
+  template <class F>
+  __device__ __forceinline__ void stage(uint16_t* lds, int k0, int wave, int lane, F row_off) const {
+#pragma unroll
+    for (int i = 0; i < kSlots; i++) {
+      const int row = (i * NW + wave) * kRows + lane / kChunks;
+      const int pos = lane % kChunks;
+      const int col = 16 * ((pos >> 1) ^ col_swz(row)) + 8 * (pos & 1);
+      uint16_t* dst = lds + (i * NW + wave) * kRows * B;
+      const size_t o = k0 + row < red ? row_off(k0 + row, i) : ~(size_t)0;
+      if constexpr (ALIGNED) {
+        const uint16_t* src = base + o + (col < ncols ? col : 0);
+        if (o == ~(size_t)0) src = g_zero16;
+        lds_copy16(src, dst);
+      } else {
+        const uint4 v = load8_any(base, o + col, ncols - col, o != ~(size_t)0);
+        *reinterpret_cast<uint4*>(dst + 8 * lane) = v;
+      }
+    }
+  }
+  // fragment of columns c0..c0+15, summed positions 32 kk + 8 (lane / 16) + 0..7: two
+  // transposing reads, each turning a block of 4 rows x 16 columns per 16 lanes into 4
+  // consecutive rows of one column per lane
+  static __device__ __forceinline__ bf16x8 frag(const uint16_t* lds, int c0, int kk, int lane) {
+    const int f = ((lane >> 2) & 3) | (((lane >> 4) & 1) << 2);   // col_swz of both rows read
+    const int row = 32 * kk + 8 * (lane >> 4) + ((lane >> 2) & 3);
+    const uint16_t* p = lds + row * B + 16 * ((c0 >> 4) ^ f) + 4 * (lane & 3);
+    typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * B));
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  }
+};
+
+// Four consecutive outputs q..q+3 of a row: one wide store where the row allows it (vec),
+// else element by element up to n.
+template <class ET>
+__device__ __forceinline__ void store4(void* out, size_t off, bool out_f32, bool vec, int n, f32x4 v) {
+  if (out_f32) {
+    float* o = static_cast<float*>(out) + off;
+    if (vec && n >= 4) {
+      *reinterpret_cast<f32x4*>(o) = v;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; i++)
+        if (i < n) o[i] = v[i];
+    }
+  } else {
+    uint16_t* o = static_cast<uint16_t*>(out) + off;
+    if (vec && n >= 4) {
+      *reinterpret_cast<uint2*>(o) = make_uint2(ET::pack2(v[0], v[1]), ET::pack2(v[2], v[3]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; i++)
+        if (i < n) o[i] = ET::from_f32(v[i]);
+    }
+  }
+}
+
+// Workgroup b of a launch of n runs on XCD b % 8 (round-robin dispatch). This gives each
+// XCD a contiguous run of the logical indices 0..n-1, so that tiles that share operand
+// slices share an L2.
+__device__ __forceinline__ int xcd_contiguous(int b, int n) {
+  const int x = b & 7, i = b >> 3, q = n >> 3, r = n & 7;
+  return x * q + (x < r ? x : r) + i;
+}
+
+}  // namespace exmoe
