@@ -394,6 +394,43 @@ int exmoe_grouped_mm_wgrad(const void* dy, size_t lddy, const void* x, size_t ld
                            hipStream_t stream);
 
 /* ------------------------------------------------------------------------------------
+ * A projection shared by many requests beside a low-rank adapter per request (device,
+ * asynchronous). Attention and the other layers around the experts stay 16-bit (abstract);
+ * this is such a layer when requests bring adapters, and, without w, the adapters beside
+ * the expert layer itself (x the layer's input, y its output):
+ *   y[t, n] = sum_k x[t, k] w[n, k] + scale_a sum_{r < rank_a} b_a[n, r] v[t, r]
+ *   v[t, r] = sum_k x[t, k] a_a[r, k],  a = adapter_ids[t]
+ *   (w NULL: y[t, n] += the second term; tokens without an adapter are left as they are).
+ * An id outside [0, adapters) is a token without an adapter. v is held in 32 bits (as two
+ * 16-bit halves for the product with b_a), sums are fp32, y is rounded once. Where v or an
+ * element of b_a is infinite, that output is infinite or NaN.
+ *
+ * x [T, K], w [N, K], y [T, N] and the bank are bf16 or all fp16 (dtype), last axis
+ * contiguous, ld* elements between rows. K and rank_max are multiples of 8, rank_max <= 128,
+ * rows of x, w, a and b 16-byte aligned (ld and strides multiples of 8); N is any size. The
+ * bank's adapters lie a_stride / b_stride elements apart; ranks int32 [adapters] (clamped to
+ * [0, rank_max]; what a and b hold past an adapter's rank is not used) and scales fp32
+ * [adapters] are device arrays or NULL (rank_max, 1). y must not overlap the inputs.
+ * Workspace: exmoe_lora_workspace_bytes bytes, no initialization, not kept; calls that
+ * overlap in time must not share one. Equal calls give equal bits.
+ * ---------------------------------------------------------------------------------- */
+typedef struct exmoe_lora_bank {
+  const void* a; /* [adapters][rank_max][K] */
+  size_t lda, a_stride;
+  const void* b; /* [adapters][N][rank_max] */
+  size_t ldb, b_stride;
+  const int32_t* ranks;
+  const float* scales;
+  int adapters, rank_max;
+} exmoe_lora_bank;
+
+size_t exmoe_lora_workspace_bytes(int T, int N, int K, int adapters, int rank_max);
+
+int exmoe_lora_linear(const void* x, size_t ldx, const void* w, size_t ldw, const exmoe_lora_bank* bank,
+                      const int32_t* adapter_ids, int T, int N, int K, int dtype, void* y, size_t ldy, void* workspace,
+                      size_t ws_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------------------
  * Per-kernel timing for benchmarks (not part of the layer's semantics). While enabled,
  * each kernel of the library is launched with a hipEvent pair that stamps that kernel's
  * own start and end on its launch stream (hipExtLaunchKernelGGL; skipped on a stream that

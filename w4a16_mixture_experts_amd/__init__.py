@@ -54,6 +54,11 @@ class ExpertBankC(ctypes.Structure):
     _fields_ = [("base", _vp), ("stride", _sz), ("expert_to_slot", _vp)]
 
 
+class LoraBankC(ctypes.Structure):
+    _fields_ = [("a", _vp), ("lda", _sz), ("a_stride", _sz), ("b", _vp), ("ldb", _sz), ("b_stride", _sz),
+                ("ranks", _vp), ("scales", _vp), ("adapters", _i), ("rank_max", _i)]
+
+
 class CacheStatsC(ctypes.Structure):
     _fields_ = [("lookups", ctypes.c_uint64), ("hits", ctypes.c_uint64), ("misses", ctypes.c_uint64),
                 ("evictions", ctypes.c_uint64), ("h2d_bytes", ctypes.c_uint64), ("h2d_copies", ctypes.c_uint64),
@@ -110,6 +115,9 @@ _SIGS = {
                                     _vp]),
     "exmoe_grouped_mm_wgrad": (_i, [_vp, _sz, _vp, _sz, _i, _vp, _i, _vp, _i, _i, _i, _i, _i, _i, _vp, _sz, _sz, _vp,
                                     _sz, _vp]),
+    "exmoe_lora_workspace_bytes": (_sz, [_i] * 5),
+    "exmoe_lora_linear": (_i, [_vp, _sz, _vp, _sz, ctypes.POINTER(LoraBankC), _vp, _i, _i, _i, _i, _vp, _sz, _vp, _sz,
+                               _vp]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -516,6 +524,56 @@ def grouped_mm_wgrad(dy, x, offsets, row_index=None, row_div: int = 1, out_dtype
             _int32("row_index", row_index, dy, rows), row_div, _int32("offsets", offsets, dy, E + 1), rows, N, K, E,
             _dtype_code(dy.dtype), _dtype_code(out_dtype), dw.data_ptr(), lddw, _expert_stride(dw, lddw), ws, ws_bytes)
     return dw
+
+
+# ----------------------------------------------------------------------------- low-rank adapters
+class LoraBank:
+    """Low-rank adapters in device memory: a [L, R, K], b [L, N, R] (16-bit, last axis
+    contiguous), ranks int32 [L] (None: all R) and scales fp32 [L] (None: all 1)."""
+
+    def __init__(self, a, b, ranks=None, scales=None):
+        torch = _torch()
+        lda, ldb = _rows_ld("a", a, 3), _rows_ld("b", b, 3)
+        _same("b", b, a)
+        if a.shape[0] != b.shape[0] or a.shape[1] != b.shape[2]:
+            raise ValueError(f"a {tuple(a.shape)} and b {tuple(b.shape)} must be [L, R, K] and [L, N, R]")
+        L, R, self.K = a.shape
+        self.N = b.shape[1]
+        self.a, self.b, self.ranks, self.scales = a, b, ranks, scales      # kept alive
+        if scales is not None and (scales.dtype != torch.float32 or scales.device != a.device
+                                   or not scales.is_contiguous() or scales.numel() != L):
+            raise ValueError(f"scales must be a contiguous float32 tensor of {L} on {a.device}")
+        self.c = LoraBankC(a.data_ptr(), lda, _expert_stride(a, lda), b.data_ptr(), ldb, _expert_stride(b, ldb),
+                           _int32("ranks", ranks, a, L), _ptr(scales), L, R)
+
+
+def lora_workspace_bytes(T: int, N: int, K: int, adapters: int, rank_max: int) -> int:
+    return _lib.exmoe_lora_workspace_bytes(T, N, K, adapters, rank_max)
+
+
+def lora_linear(x, w, bank: LoraBank, ids, y=None, workspace=None):
+    """y[t] = w @ x[t] + scale * b[id] @ (a[id] @ x[t]) with id = ids[t] (int32 [T]; outside
+    [0, L): no adapter). w [N, K], or None: the adapters' part is added to y in place."""
+    ldx = _rows_ld("x", x)
+    T, K = x.shape
+    _same("bank", bank.a, x)
+    if bank.K != K:
+        raise ValueError(f"x has {K} columns, the adapters take {bank.K}")
+    if w is None:
+        if y is None:
+            raise ValueError("without w, y must be given (it is added to)")
+        wp, ldw = None, 0
+    else:
+        wp, ldw = w.data_ptr(), _rows_ld("w", w)
+        _same("w", w, x)
+        if tuple(w.shape) != (bank.N, K):
+            raise ValueError(f"w must be {(bank.N, K)} (got {tuple(w.shape)})")
+    y = _result("y", y, (T, bank.N), x.dtype, x)
+    need = 0 if workspace is not None else lora_workspace_bytes(T, bank.N, K, bank.c.adapters, bank.c.rank_max)
+    ws, ws_bytes, _keep = _scratch(workspace, need, x)
+    _run_on(x, _lib.exmoe_lora_linear, x.data_ptr(), ldx, wp, ldw, ctypes.byref(bank.c), _int32("ids", ids, x, T), T,
+            bank.N, K, _dtype_code(x.dtype), y.data_ptr(), _rows_ld("y", y), ws, ws_bytes)
+    return y
 
 
 # ----------------------------------------------------------------------------- slot cache
