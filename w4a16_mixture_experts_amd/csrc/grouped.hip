@@ -10,72 +10,94 @@
 #include "grouped.h"
 
 #include "exmoe.h"
-#include "gemm_tile.h"
+#include "gemm_wide.h"
 
 namespace exmoe {
 
 enum { kMM = 0, kDG = 1, kWG = 2 };
 
 struct RowTile {
-  int e, seg0, cnt, p0, qt;
+  int e, seg0, cnt, p0, p1, qt;   // rows p0..p1 of the segment
 };
 
 __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? lo : (v > hi ? hi : v); }
 
-// Tile of workgroup b among ceil(count_e / BP) x q_tiles tiles per expert: all row tiles of
-// one column tile follow each other (they read the same slice of W). Whole workgroup.
+// Order of the np x nq tiles of one matrix: bands of up to 8 row tiles, in a band column by
+// column. The 32 tiles that run at once on an XCD are then about 8 x 4, which shares both
+// operands' slices in its L2 (one row of tiles would read 33 slices a step instead of 12;
+// 8192 x 8192 x 8192: 1394 -> XX us).
+__device__ __forceinline__ void band_order(int idx, int np, int nq, int& pt, int& qt) {
+  constexpr int kBand = 8;
+  const int band = idx / (kBand * nq), rows = min(kBand, np - band * kBand);
+  idx -= band * kBand * nq;
+  qt = idx / rows;
+  pt = band * kBand + idx - qt * rows;
+}
+
+// Inclusive sum over the lanes of a wave: row shifts inside 16 lanes, then the rows' totals.
+__device__ __forceinline__ int wave_scan(int v) {
+  auto step = [&](auto ctrl) __attribute__((always_inline)) {
+    v += __builtin_amdgcn_update_dpp(0, v, decltype(ctrl)::value, 0xF, 0xF, true);   // row_shr: zeros shifted in
+  };
+  step(std::integral_constant<int, 0x111>{});
+  step(std::integral_constant<int, 0x112>{});
+  step(std::integral_constant<int, 0x114>{});
+  step(std::integral_constant<int, 0x118>{});
+  const int t0 = __builtin_amdgcn_readlane(v, 15), t1 = __builtin_amdgcn_readlane(v, 31),
+            t2 = __builtin_amdgcn_readlane(v, 47);
+  const int row = (int)lane_id() >> 4;
+  return v + (row > 0 ? t0 : 0) + (row > 1 ? t1 : 0) + (row > 2 ? t2 : 0);
+}
+
+// Tile of workgroup b among ceil(count_e / BP) x q_tiles tiles per expert. Every wave finds
+// it by itself (no barrier): lane l holds experts 4 l .. 4 l + 3.
 template <int BP>
-__device__ bool resolve_rows(const int32_t* __restrict__ offsets, int rows, int E, int q_tiles, int b, RowTile& t,
-                             int* s_scan, int* s_off) {
-  const int tid = threadIdx.x;
-  if (tid < 64) {
-    int o[5];
+__device__ __forceinline__ bool resolve_rows(const int32_t* __restrict__ offsets, int rows, int E, int q_tiles, int b,
+                                             RowTile& t) {
+  const int lane = (int)lane_id();
+  int o[5], v[4], run = 0;
 #pragma unroll
-    for (int q = 0; q < 5; q++) {
-      const int e = tid * 4 + q;
-      o[q] = offsets[e <= E ? e : E];
-    }
-    int v[4], run = 0;
-#pragma unroll
-    for (int q = 0; q < 5; q++) o[q] = clampi(o[q], 0, rows);
-#pragma unroll
-    for (int q = 0; q < 4; q++) {
-      const int c = tid * 4 + q < E ? o[q + 1] - o[q] : 0;
-      v[q] = c > 0 ? (c + BP - 1) / BP : 0;
-      run += v[q];
-      s_off[tid * 4 + q] = o[q];
-    }
-    if (tid == 63) s_off[kMaxExperts] = o[4];
-    int incl = run;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const int u = __shfl_up(incl, off, 64);
-      if (tid >= off) incl += u;
-    }
-    int ex = incl - run;
-#pragma unroll
-    for (int q = 0; q < 4; q++) {
-      s_scan[tid * 4 + q] = ex;
-      ex += v[q];
-    }
-    if (tid == 63) s_scan[kMaxExperts] = incl;
+  for (int q = 0; q < 5; q++) {
+    const int e = lane * 4 + q;
+    o[q] = offsets[e <= E ? e : E];
   }
-  __syncthreads();
-  const int total = s_scan[kMaxExperts] * q_tiles;
+#pragma unroll
+  for (int q = 0; q < 5; q++) o[q] = clampi(o[q], 0, rows);
+#pragma unroll
+  for (int q = 0; q < 4; q++) {
+    const int c = lane * 4 + q < E ? o[q + 1] - o[q] : 0;
+    v[q] = c > 0 ? (c + BP - 1) / BP : 0;
+    run += v[q];
+  }
+  const int incl = wave_scan(run);
+  const int total = __builtin_amdgcn_readlane(incl, 63) * q_tiles;
   if (b >= total) return false;
   const int idx = xcd_contiguous(b, total);
-  int lo = 0, hi = E - 1;   // the largest e with scan[e] * q_tiles <= idx owns it
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (s_scan[mid] * q_tiles <= idx) lo = mid; else hi = mid - 1;
+  // the first lane whose experts end past the tile, then the expert of the four
+  const int own = __ffsll((long long)__ballot(incl * q_tiles > idx)) - 1;
+  int start = __builtin_amdgcn_readlane(incl - run, own), seg0 = 0, end = 0, e = 0;
+  bool found = false;
+#pragma unroll
+  for (int q = 0; q < 4; q++) {
+    const int vq = __builtin_amdgcn_readlane(v[q], own);
+    if (!found && (start + vq) * q_tiles > idx) {
+      found = true;
+      e = own * 4 + q;
+      seg0 = __builtin_amdgcn_readlane(o[q], own);
+      end = __builtin_amdgcn_readlane(o[q + 1], own);
+    }
+    if (!found) start += vq;
   }
-  t.e = lo;
-  t.seg0 = s_off[lo];
-  t.cnt = s_off[lo + 1] - t.seg0;
+  t.e = e;
+  t.seg0 = seg0;
+  t.cnt = end - seg0;
+  // the expert's rows are dealt evenly to its tiles, in whole blocks of 32
   const int np = (t.cnt + BP - 1) / BP;
-  const int local = idx - s_scan[lo] * q_tiles;
-  t.qt = local / np;
-  t.p0 = (local - t.qt * np) * BP;
+  int pt;
+  band_order(idx - start * q_tiles, np, q_tiles, pt, t.qt);
+  const int blocks = (t.cnt + 31) / 32, each = blocks / np, more = blocks - each * np;
+  t.p0 = 32 * (each * pt + min(pt, more));
+  t.p1 = min(t.cnt, t.p0 + 32 * (each + (pt < more ? 1 : 0)));
   return true;
 }
 
@@ -87,95 +109,118 @@ __device__ __forceinline__ int div_by(int v, int d, uint32_t mul) {
   return (int)q;
 }
 
-// One BP x BQ output tile per workgroup of WP x WQ waves, each owning a BP/WP x BQ/WQ part;
-// 64-deep slices of both operands double-buffered in LDS, one barrier per slice.
-template <class ET, int MODE, int BP, int BQ, int WP, int WQ, bool ALIGNED>
-__global__ __launch_bounds__(64 * WP * WQ) void grouped_kernel(GroupedArgs a, int p_tiles, int q_tiles, int splits) {
-  constexpr int NW = WP * WQ, TP = BP / WP / 16, TQ = BQ / WQ / 16;
-  using OpP = std::conditional_t<MODE == kWG, ColOperand<BP, NW, ALIGNED>, RowOperand<BP, NW, ALIGNED>>;
-  using OpQ = std::conditional_t<MODE == kMM, RowOperand<BQ, NW, ALIGNED>, ColOperand<BQ, NW, ALIGNED>>;
-  __shared__ __attribute__((aligned(16))) uint16_t s_p0[BP * kBK], s_p1[BP * kBK], s_q0[BQ * kBK], s_q1[BQ * kBK];
-  __shared__ int s_scan[kMaxExperts + 1], s_off[kMaxExperts + 1];
+// The tile of a workgroup: expert e, whose rows start at seg0 of the sorted order; rows
+// p0..cnt of them (gradient of W: the cnt rows of this part of the sum, output rows from p0),
+// columns from q0, length red of the summed axis.
+struct TilePlace {
+  int e, seg0, cnt, p0, q0, red, split;
+};
 
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wp = wave / WQ, wq = wave % WQ;
-  const int Q = MODE == kMM ? a.N : a.K;    // output columns
-  const uint32_t dmul = 0xFFFFFFFFu / (uint32_t)a.row_div;
-
-  int e, seg0, cnt, p0, q0, red, r_begin = 0, split = 0;
+template <int MODE, int BP, int BQ>
+__device__ __forceinline__ bool place_tile(const GroupedArgs& a, int p_tiles, int q_tiles, int splits, TilePlace& t) {
+  t.split = 0;
   if constexpr (MODE == kWG) {
     int idx = xcd_contiguous(blockIdx.x, gridDim.x);
     const int per = p_tiles * q_tiles;
     const int es = idx / per;
     idx -= es * per;
-    e = es / splits;
-    split = es - e * splits;
-    p0 = idx / q_tiles * BP;
-    q0 = idx % q_tiles * BQ;
-    const int o0 = clampi(a.offsets[e], 0, a.rows), o1 = clampi(a.offsets[e + 1], 0, a.rows);
-    seg0 = o0;
-    cnt = o1 > o0 ? o1 - o0 : 0;
-    const int steps = (cnt + kBK - 1) / kBK;
-    r_begin = (int)((long long)steps * split / splits) * kBK;
-    const int r_end = (int)((long long)steps * (split + 1) / splits) * kBK;
-    seg0 += r_begin;
-    cnt = (r_end < cnt ? r_end : cnt) - r_begin;
-    if (cnt < 0) cnt = 0;
-    red = cnt;
+    t.e = es / splits;
+    t.split = es - t.e * splits;
+    int pt, qt;
+    band_order(idx, p_tiles, q_tiles, pt, qt);
+    t.p0 = pt * BP;
+    t.q0 = qt * BQ;
+    t.seg0 = clampi(a.offsets[t.e], 0, a.rows);
+    const int o1 = clampi(a.offsets[t.e + 1], 0, a.rows);
+    t.cnt = o1 > t.seg0 ? o1 - t.seg0 : 0;
+    const int steps = (t.cnt + kBK - 1) / kBK;
+    const int r_begin = (int)((long long)steps * t.split / splits) * kBK;
+    const int r_end = (int)((long long)steps * (t.split + 1) / splits) * kBK;
+    t.seg0 += r_begin;
+    t.cnt = (r_end < t.cnt ? r_end : t.cnt) - r_begin;
+    if (t.cnt < 0) t.cnt = 0;
+    t.red = t.cnt;
   } else {
-    RowTile t;
-    if (!resolve_rows<BP>(a.offsets, a.rows, a.E, q_tiles, blockIdx.x, t, s_scan, s_off)) return;
-    e = t.e;
-    seg0 = t.seg0;
-    cnt = t.cnt;
-    p0 = t.p0;
-    q0 = t.qt * BQ;
-    red = MODE == kMM ? a.K : a.N;
+    RowTile r;
+    if (!resolve_rows<BP>(a.offsets, a.rows, a.E, q_tiles, blockIdx.x, r)) return false;
+    t.e = r.e;
+    t.seg0 = r.seg0;
+    t.cnt = r.p1;
+    t.p0 = r.p0;
+    t.q0 = r.qt * BQ;
+    t.red = MODE == kMM ? a.K : a.N;
   }
+  return true;
+}
 
+// Where a tile's outputs go: the caller's matrix, or the partial sums [split][E][N][K].
+template <int MODE>
+__device__ __forceinline__ TileOut tile_out(const GroupedArgs& a, const TilePlace& t, int splits) {
+  TileOut o{a.out, 0, a.ldo, a.out_f32 != 0, a.vec != 0};
+  if (MODE == kWG) {
+    if (splits > 1) o = TileOut{a.ws, ((size_t)t.split * a.E + t.e) * a.N * a.K, (size_t)a.K, true, a.K % 4 == 0};
+    else o.base = (size_t)t.e * a.o_stride;
+  }
+  return o;
+}
+
+// The simple form's operands and the staging of a slice.
+template <int MODE, class OpP, class OpQ, int BP, int BQ, int NW>
+struct TileWork {
+  const GroupedArgs& a;
+  int wave, lane, Q;
+  uint32_t dmul;
+  TilePlace t;
   OpP op_p;
   OpQ op_q;
-  if constexpr (MODE == kWG) {
-    op_p.init(a.a + (size_t)seg0 * a.lda + p0, a.lda, red, a.N - p0);
-    op_q.init(a.b + q0, a.ldb, red, a.K - q0);
-  } else {
-    // rows past the segment repeat its last one; an index outside x reads row 0 (such rows
-    // are stored as zeros)
-    op_p.init(a.a, red, wave, lane, [&](int i) {
-      int s = seg0 + (p0 + i < cnt ? p0 + i : cnt - 1);
-      if (MODE == kMM && a.row_index) {
-        const int v = a.row_index[s];
-        s = v < 0 ? a.x_rows : div_by(v, a.row_div, dmul);
-        if (s >= a.x_rows) s = 0;
-      } else if (MODE == kMM && s >= a.x_rows) {
-        s = 0;
-      }
-      return (size_t)s * a.lda;
-    });
-    if constexpr (MODE == kMM) {
-      op_q.init(a.b + (size_t)e * a.b_stride, red, wave, lane, [&](int i) {
-        return (size_t)(q0 + i < Q ? q0 + i : Q - 1) * a.ldb;
-      });
+  // gradient of W: the rows of x behind a slice's sorted rows, loaded a slice ahead
+  int gidx[MODE == kWG ? OpQ::kSlots : 1];
+
+  __device__ __forceinline__ TileWork(const GroupedArgs& args, int wave_, int lane_)
+      : a(args), wave(wave_), lane(lane_), Q(MODE == kMM ? args.N : args.K), dmul(0xFFFFFFFFu / (uint32_t)args.row_div) {}
+
+  __device__ __forceinline__ bool resolve(int p_tiles, int q_tiles, int splits) {
+    if (!place_tile<MODE, BP, BQ>(a, p_tiles, q_tiles, splits, t)) return false;
+    if constexpr (MODE == kWG) {
+      op_p.init(a.a + (size_t)t.seg0 * a.lda + t.p0, a.lda, t.red, a.N - t.p0);
+      op_q.init(a.b + t.q0, a.ldb, t.red, a.K - t.q0);
     } else {
-      op_q.init(a.b + (size_t)e * a.b_stride + q0, a.ldb, red, Q - q0);
+      // rows past the segment repeat its last one; an index outside x reads row 0 (such rows
+      // are stored as zeros)
+      op_p.init(a.a, t.red, wave, lane, [&](int i) {
+        int s = t.seg0 + (t.p0 + i < t.cnt ? t.p0 + i : t.cnt - 1);
+        if (MODE == kMM) {
+          if (a.row_index) {
+            const int v = a.row_index[s];
+            s = v < 0 ? a.x_rows : div_by(v, a.row_div, dmul);
+          }
+          if (s >= a.x_rows) s = 0;
+        }
+        return (size_t)s * a.lda;
+      });
+      if constexpr (MODE == kMM) {
+        op_q.init(a.b + (size_t)t.e * a.b_stride, t.red, wave, lane,
+                  [&](int i) { return (size_t)(t.q0 + i < Q ? t.q0 + i : Q - 1) * a.ldb; });
+      } else {
+        op_q.init(a.b + (size_t)t.e * a.b_stride + t.q0, a.ldb, t.red, Q - t.q0);
+      }
     }
+    return true;
   }
 
-  // gradient of W: the rows of x behind the next slice's sorted rows, loaded a slice ahead
-  int gidx[MODE == kWG ? OpQ::kSlots : 1];
-  auto load_idx = [&](int k0) {
+  __device__ __forceinline__ void load_idx(int k0) {
     if constexpr (MODE == kWG) {
 #pragma unroll
       for (int i = 0; i < OpQ::kSlots; i++) {
         const int r = k0 + (i * NW + wave) * OpQ::kRows + lane / OpQ::kChunks;
-        int v = seg0 + r;
-        if (r < red && a.row_index) v = a.row_index[v];
+        int v = t.seg0 + r;
+        if (r < t.red && a.row_index) v = a.row_index[v];
         gidx[i] = v;
       }
     }
-  };
-  auto stage = [&](int k0, uint16_t* lp, uint16_t* lq) {
+  }
+  // (gradient of W: with the rows of load_idx(k0))
+  __device__ __forceinline__ void stage(int k0, uint16_t* lp, uint16_t* lq) const {
     if constexpr (MODE == kWG) {
       op_p.stage(lp, k0, wave, lane, [&](int r, int) { return (size_t)r * a.lda; });
       op_q.stage(lq, k0, wave, lane, [&](int, int i) {
@@ -183,13 +228,35 @@ __global__ __launch_bounds__(64 * WP * WQ) void grouped_kernel(GroupedArgs a, in
         const int s = v < 0 ? a.x_rows : (a.row_index ? div_by(v, a.row_div, dmul) : v);
         return s < a.x_rows ? (size_t)s * a.ldb : ~(size_t)0;
       });
-      load_idx(k0 + kBK);
     } else {
       op_p.stage(lp, k0, wave, lane);
       if constexpr (MODE == kMM) op_q.stage(lq, k0, wave, lane);
       else op_q.stage(lq, k0, wave, lane, [&](int r, int) { return (size_t)r * a.ldb; });
     }
-  };
+  }
+  // whether row p of x lies outside x (its outputs are zeros)
+  __device__ __forceinline__ bool zero_row(int p) const {
+    if (MODE != kMM) return false;
+    const int v = a.row_index ? a.row_index[t.seg0 + p] : t.seg0 + p;
+    return v < 0 || (a.row_index ? div_by(v, a.row_div, dmul) : v) >= a.x_rows;
+  }
+};
+
+// One BP x BQ output tile per workgroup of WP x WQ waves, each owning a BP/WP x BQ/WQ part;
+// 64-deep slices of both operands double-buffered in LDS, one barrier per slice. The form
+// for operands of any alignment (their elements are loaded one by one).
+template <class ET, int MODE, int BP, int BQ, int WP, int WQ, bool ALIGNED>
+__global__ __launch_bounds__(64 * WP * WQ) void grouped_kernel(GroupedArgs a, int p_tiles, int q_tiles, int splits) {
+  constexpr int NW = WP * WQ, TP = BP / WP / 16, TQ = BQ / WQ / 16;
+  using OpP = std::conditional_t<MODE == kWG, ColOperand<BP, NW, ALIGNED>, RowOperand<BP, NW, ALIGNED>>;
+  using OpQ = std::conditional_t<MODE == kMM, RowOperand<BQ, NW, ALIGNED>, ColOperand<BQ, NW, ALIGNED>>;
+  __shared__ __attribute__((aligned(16))) uint16_t s_p0[BP * kBK], s_p1[BP * kBK], s_q0[BQ * kBK], s_q1[BQ * kBK];
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wp = wave / WQ, wq = wave % WQ;
+  TileWork<MODE, OpP, OpQ, BP, BQ, NW> t(a, wave, lane);
+  if (!t.resolve(p_tiles, q_tiles, splits)) return;
 
   f32x4 acc[TQ][TP];
 #pragma unroll
@@ -197,11 +264,14 @@ __global__ __launch_bounds__(64 * WP * WQ) void grouped_kernel(GroupedArgs a, in
 #pragma unroll
     for (int i = 0; i < TP; i++) acc[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  const int steps = (red + kBK - 1) / kBK;
+  const int steps = (t.t.red + kBK - 1) / kBK;
   auto step = [&](int s, const uint16_t* cp, const uint16_t* cq, uint16_t* np, uint16_t* nq) {
     __builtin_amdgcn_s_waitcnt(0);   // this slice has landed; everyone is past the last one
     __syncthreads();
-    if (s + 1 < steps) stage((s + 1) * kBK, np, nq);
+    if (s + 1 < steps) {
+      t.stage((s + 1) * kBK, np, nq);
+      t.load_idx((s + 2) * kBK);
+    }
 #pragma unroll
     for (int kk = 0; kk < 2; kk++) {
       bf16x8 fq[TQ], fp[TP];
@@ -216,8 +286,9 @@ __global__ __launch_bounds__(64 * WP * WQ) void grouped_kernel(GroupedArgs a, in
     }
   };
   if (steps > 0) {
-    load_idx(0);
-    stage(0, s_p0, s_q0);
+    t.load_idx(0);
+    t.stage(0, s_p0, s_q0);
+    t.load_idx(kBK);
     for (int s = 0; s < steps; s += 2) {
       step(s, s_p0, s_q0, s_p1, s_q1);
       if (s + 1 < steps) step(s + 1, s_p1, s_q1, s_p0, s_q0);
@@ -225,37 +296,73 @@ __global__ __launch_bounds__(64 * WP * WQ) void grouped_kernel(GroupedArgs a, in
   }
 
   // lane l holds p = l % 16 and q = 4 (l / 16) + 0..3 of each 16 x 16 part
-  void* out = a.out;
-  bool f32 = a.out_f32;
-  size_t obase = 0, ldo = a.ldo;
-  if (MODE == kWG) {
-    if (splits > 1) {   // partial sums, [split][E][N][K]
-      out = a.ws;
-      f32 = true;
-      ldo = (size_t)a.K;
-      obase = ((size_t)split * a.E + e) * a.N * a.K;
-    } else {
-      obase = (size_t)e * a.o_stride;
-    }
-  }
-  const bool vec = MODE == kWG && splits > 1 ? a.K % 4 == 0 : a.vec;
-  const int plim = MODE == kWG ? a.N : cnt;
+  const TileOut out = tile_out<MODE>(a, t.t, splits);
+  const int plim = MODE == kWG ? a.N : t.t.cnt;
 #pragma unroll
   for (int i = 0; i < TP; i++) {
-    const int p = p0 + (wp * TP + i) * 16 + (lane & 15);
+    const int p = t.t.p0 + (wp * TP + i) * 16 + (lane & 15);
     if (p >= plim) continue;
-    const size_t prow = MODE == kWG ? (size_t)p : (size_t)(seg0 + p);
-    bool zero = false;
-    if (MODE == kMM) {
-      const int v = a.row_index ? a.row_index[prow] : (int)prow;
-      zero = v < 0 || (a.row_index ? div_by(v, a.row_div, dmul) : v) >= a.x_rows;
-    }
+    const bool zero = t.zero_row(p);
+    const size_t row = out.base + (size_t)(MODE == kWG ? p : t.t.seg0 + p) * out.ld;
 #pragma unroll
     for (int j = 0; j < TQ; j++) {
-      const int q = q0 + (wq * TQ + j) * 16 + 4 * (lane >> 4);
-      if (q < Q) store4<ET>(out, obase + prow * ldo + q, f32, vec, Q - q, zero ? f32x4{0.f, 0.f, 0.f, 0.f} : acc[j][i]);
+      const int q = t.t.q0 + (wq * TQ + j) * 16 + 4 * (lane >> 4);
+      if (q < t.Q)
+        store4<ET>(out.ptr, row + q, out.f32, out.vec, t.Q - q, zero ? f32x4{0.f, 0.f, 0.f, 0.f} : acc[j][i]);
     }
   }
+}
+
+// The pipelined form for aligned operands (gemm_wide.h).
+template <class ET, int MODE, int TP, int TQ, int WP, int WQ, int D, int OCC>
+__global__ __launch_bounds__(64 * WP * WQ, OCC) void grouped_wide_kernel(GroupedArgs a, int p_tiles, int q_tiles,
+                                                                        int splits) {
+  constexpr int NW = WP * WQ, BP = 32 * TP * WP, BQ = 32 * TQ * WQ;
+  using OpP = std::conditional_t<MODE == kWG, WideCols<BP, NW, D>, WideRows<BP, NW, D>>;
+  using OpQ = std::conditional_t<MODE == kMM, WideRows<BQ, NW, D>, WideCols<BQ, NW, D>>;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  TilePlace t;
+  if (!place_tile<MODE, BP, BQ>(a, p_tiles, q_tiles, splits, t)) return;
+  const int Q = MODE == kMM ? a.N : a.K;
+  const uint32_t dmul = 0xFFFFFFFFu / (uint32_t)a.row_div;
+  OpP op_p;
+  OpQ op_q;
+  if constexpr (MODE == kWG) {
+    op_p.template init<false>(make_buf(a.a + (size_t)t.seg0 * a.lda + t.p0, t.red ? 2 * ((t.red - 1) * a.lda + (a.N - t.p0)) : 0),
+              2 * (uint32_t)a.lda, t.red, a.N - t.p0, wave, lane);
+    op_q.template init<true>(make_buf(a.b + t.q0, a.x_rows ? 2 * ((a.x_rows - 1) * a.ldb + (a.K - t.q0)) : 0), 2 * (uint32_t)a.ldb,
+              t.red, a.K - t.q0, wave, lane);
+  } else {
+    const int rows_a = MODE == kMM ? a.x_rows : a.rows;
+    op_p.init(make_buf(a.a, 2 * ((rows_a - 1) * a.lda + t.red)), t.red, wave, lane, [&](int i) {
+      int s = t.seg0 + t.p0 + i;
+      bool ok = t.p0 + i < t.cnt;
+      if (MODE == kMM && a.row_index) {
+        const int v = ok ? a.row_index[s] : -1;
+        s = v < 0 ? a.x_rows : div_by(v, a.row_div, dmul);
+        ok = s < a.x_rows;
+      }
+      return ok ? (uint32_t)((size_t)s * a.lda * 2) : kNowhere;
+    });
+    const uint16_t* w = a.b + (size_t)t.e * a.b_stride;
+    if constexpr (MODE == kMM) {
+      op_q.init(make_buf(w, 2 * ((a.N - 1) * a.ldb + a.K)), t.red, wave, lane, [&](int i) {
+        return t.q0 + i < Q ? (uint32_t)((size_t)(t.q0 + i) * a.ldb * 2) : kNowhere;
+      });
+    } else {
+      op_q.template init<false>(make_buf(w + t.q0, 2 * ((a.N - 1) * a.ldb + (Q - t.q0))), 2 * (uint32_t)a.ldb, t.red, Q - t.q0,
+                wave, lane);
+    }
+  }
+  wide_tile<ET, TP, TQ, WP, WQ, D, MODE == kWG>(
+      op_p, op_q, t.red, t.p0, MODE == kWG ? a.N : t.cnt, t.q0, Q, tile_out<MODE>(a, t, splits),
+      [&](int r) { return a.row_index ? a.row_index[t.seg0 + r] : t.seg0 + r; },
+      [&](int v) {
+        const int s = a.row_index ? div_by(v, a.row_div, dmul) : v;
+        return s < a.x_rows ? (uint32_t)s * 2 * (uint32_t)a.ldb : kNowhere;
+      },
+      [](int, int, auto&) {}, [&](int p) { return MODE == kWG ? p : t.seg0 + p; });
 }
 
 // dx[t, :] = sum_j rows[flat_to_sorted[t k + j], :] in slot order, rounded once. Entries
@@ -343,15 +450,43 @@ static hipError_t launch_rows(const GroupedArgs& a, const char* name, hipStream_
   return hipGetLastError();
 }
 
+template <class ET, int MODE, int TP, int TQ, int WP, int WQ, int D, int OCC>
+static hipError_t launch_wide(const GroupedArgs& a, const char* name, hipStream_t s) {
+  constexpr int BP = 32 * TP * WP, BQ = 32 * TQ * WQ;
+  const long long max_p = a.rows / BP + (a.E < a.rows ? a.E : a.rows);
+  const int qt = ceil_div(MODE == kMM ? a.N : a.K, BQ);
+  if (max_p * qt * (64 * WP * WQ) > kMaxThreads) return hipErrorInvalidConfiguration;
+  ProfScope prof(name, s);
+  EXMOE_LAUNCH(prof, (grouped_wide_kernel<ET, MODE, TP, TQ, WP, WQ, D, OCC>), dim3((unsigned)(max_p * qt)),
+               dim3(64 * WP * WQ), 0, s, a, 0, qt, 1);
+  return hipGetLastError();
+}
+
 static bool op_aligned(const void* p, size_t ld, size_t stride, int len) {
   return aligned16(p) && ld % 8 == 0 && stride % 8 == 0 && len % 8 == 0;
+}
+
+// Whether an operand of n rows, ld apart, len long, can be addressed with 32-bit offsets.
+static bool op_span(size_t n, size_t ld, int len) { return n == 0 || 2 * ((n - 1) * ld + len) < kMaxSpan; }
+
+// Tiles of 256 x 256 on 8 waves (one workgroup per compute unit) move half the bytes per
+// product of 128 x 128 tiles on 4 waves (two per unit, so that one's start and end hide
+// behind the other's loop). Measured, large / small: 4096 tokens, 8 experts of 14336 x 4096
+// (1024 rows each) 879 / 1096 us; 64 experts of 2048 x 2048 with 256 rows each 202 / 217 us,
+// with 256 on average but skewed 215 / 211 us. Large from 256 rows per expert on, when that
+// still gives every compute unit a tile.
+static bool large_tiles(int rows, int Q, int E) {
+  return rows / E >= 256 && (long long)(rows / 256) * ceil_div(Q, 256) >= 256;
 }
 
 template <class ET>
 static hipError_t mm_type(const GroupedArgs& a, hipStream_t s) {
   const bool al = op_aligned(a.a, a.lda, 0, a.K) && op_aligned(a.b, a.ldb, a.b_stride, a.K);
-  if (al) return launch_rows<ET, kMM, 128, 128, 2, 2, true>(a, "grouped_mm", s);
-  return launch_rows<ET, kMM, 128, 128, 2, 2, false>(a, "grouped_mm", s);
+  if (!al) return launch_rows<ET, kMM, 128, 128, 2, 2, false>(a, "grouped_mm", s);
+  if (!op_span(a.x_rows, a.lda, a.K) || !op_span(a.N, a.ldb, a.K))
+    return launch_rows<ET, kMM, 128, 128, 2, 2, true>(a, "grouped_mm", s);
+  if (large_tiles(a.rows, a.N, a.E)) return launch_wide<ET, kMM, 4, 2, 2, 4, 64, 2>(a, "grouped_mm", s);
+  return launch_wide<ET, kMM, 2, 2, 2, 2, 64, 2>(a, "grouped_mm", s);
 }
 
 hipError_t launch_grouped_mm(const GroupedArgs& a, hipStream_t s) {
@@ -369,8 +504,12 @@ static hipError_t dgrad_type(const GroupedArgs& a, hipStream_t s) {
     r.ldo = (size_t)a.K;
     r.out_f32 = 1;
   }
-  hipError_t e = al ? launch_rows<ET, kDG, 128, 128, 2, 2, true>(r, "grouped_dgrad", s)
-                    : launch_rows<ET, kDG, 128, 128, 2, 2, false>(r, "grouped_dgrad", s);
+  hipError_t e;
+  if (!al) e = launch_rows<ET, kDG, 128, 128, 2, 2, false>(r, "grouped_dgrad", s);
+  else if (!op_span(a.rows, a.lda, a.N) || !op_span(a.N, a.ldb, a.K))
+    e = launch_rows<ET, kDG, 128, 128, 2, 2, true>(r, "grouped_dgrad", s);
+  else if (large_tiles(a.rows, a.K, a.E)) e = launch_wide<ET, kDG, 4, 2, 2, 4, 64, 2>(r, "grouped_dgrad", s);
+  else e = launch_wide<ET, kDG, 2, 2, 2, 2, 64, 2>(r, "grouped_dgrad", s);
   if (e != hipSuccess || !a.flat_to_sorted) return e;
   const int T = a.rows / a.k;
   ProfScope prof("token_sum", s);
@@ -390,17 +529,36 @@ hipError_t launch_grouped_dgrad(const GroupedArgs& a, hipStream_t s) {
   return a.fp16 ? dgrad_type<ElemFP16>(a, s) : dgrad_type<ElemBF16>(a, s);
 }
 
-template <class ET, bool ALIGNED>
-static hipError_t wgrad_tiles(const GroupedArgs& a, hipStream_t s) {
-  const int pt = ceil_div(a.N, 128), qt = ceil_div(a.K, 128), splits = wgrad_splits(a.rows, a.N, a.K, a.E);
+template <int BP, int BQ, int THREADS, class F>
+static hipError_t launch_weights(const GroupedArgs& a, hipStream_t s, int splits, F kernel) {
+  const int pt = ceil_div(a.N, BP), qt = ceil_div(a.K, BQ);
   const long long grid = (long long)pt * qt * a.E * splits;
-  if (grid * 256 > kMaxThreads) return hipErrorInvalidConfiguration;
-  {
-    ProfScope prof("grouped_wgrad", s);
-    EXMOE_LAUNCH(prof, (grouped_kernel<ET, kWG, 128, 128, 2, 2, ALIGNED>), dim3((unsigned)grid), dim3(256), 0, s, a, pt,
-                 qt, splits);
-  }
-  hipError_t e = hipGetLastError();
+  if (grid * THREADS > kMaxThreads) return hipErrorInvalidConfiguration;
+  ProfScope prof("grouped_wgrad", s);
+  EXMOE_LAUNCH(prof, kernel, dim3((unsigned)grid), dim3(THREADS), 0, s, a, pt, qt, splits);
+  return hipGetLastError();
+}
+template <class ET, int TP, int TQ, int WP, int WQ, int D, int OCC>
+static hipError_t launch_weights_wide(const GroupedArgs& a, hipStream_t s, int splits) {
+  return launch_weights<32 * TP * WP, 32 * TQ * WQ, 64 * WP * WQ>(a, s, splits, grouped_wide_kernel<ET, kWG, TP, TQ, WP, WQ, D, OCC>);
+}
+
+template <class ET>
+static hipError_t wgrad_type(const GroupedArgs& a, hipStream_t s) {
+  const int splits = wgrad_splits(a.rows, a.N, a.K, a.E);
+  hipError_t e;
+  if (!op_aligned(a.a, a.lda, 0, a.N) || !op_aligned(a.b, a.ldb, 0, a.K))
+    e = launch_weights<128, 128, 256>(a, s, splits, grouped_kernel<ET, kWG, 128, 128, 2, 2, false>);
+  else if (!op_span(a.rows, a.lda, a.N) || !op_span(a.x_rows, a.ldb, a.K))
+    e = launch_weights<128, 128, 256>(a, s, splits, grouped_kernel<ET, kWG, 128, 128, 2, 2, true>);
+  else if (a.rows / a.E >= 768 && splits == 1 && (long long)a.E * ceil_div(a.N, 256) * ceil_div(a.K, 256) >= 256)
+    e = launch_weights_wide<ET, 4, 2, 2, 4, 64, 2>(a, s, splits);
+  else
+    // few rows per output: 128 x 128 tiles with shallow slices, three workgroups per compute
+    // unit, so that the stores of one run beside the loops of others (256 rows per expert of
+    // 2048 x 2048: 289 us against 329 us on 256 x 256 tiles; 1024 rows of 14336 x 4096:
+    // 1166 against 1103 us)
+    e = launch_weights_wide<ET, 2, 2, 2, 2, 32, 3>(a, s, splits);
   if (e != hipSuccess || splits == 1) return e;
   const size_t n = (size_t)a.E * a.N * a.K;
   ProfScope prof("split_sum", s);
@@ -410,9 +568,7 @@ static hipError_t wgrad_tiles(const GroupedArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_grouped_wgrad(const GroupedArgs& a, hipStream_t s) {
-  const bool al = op_aligned(a.a, a.lda, 0, a.N) && op_aligned(a.b, a.ldb, 0, a.K);
-  if (a.fp16) return al ? wgrad_tiles<ElemFP16, true>(a, s) : wgrad_tiles<ElemFP16, false>(a, s);
-  return al ? wgrad_tiles<ElemBF16, true>(a, s) : wgrad_tiles<ElemBF16, false>(a, s);
+  return a.fp16 ? wgrad_type<ElemFP16>(a, s) : wgrad_type<ElemBF16>(a, s);
 }
 
 }  // namespace exmoe
@@ -465,9 +621,10 @@ static int launched(hipError_t e, const char* what) {
   return hip_error(e, what);
 }
 
-// Whether four consecutive outputs of a row can be stored at once.
+// Whether rows of outputs can be stored 16 bytes at a time.
 static int vec_store(const void* p, size_t ld, size_t stride, int out_f32) {
-  return (uintptr_t)p % (out_f32 ? 16 : 8) == 0 && ld % 4 == 0 && stride % 4 == 0;
+  const size_t n = out_f32 ? 4 : 8;
+  return aligned16(p) && ld % n == 0 && stride % n == 0;
 }
 
 #define EXMOE_TRY(call)        \
