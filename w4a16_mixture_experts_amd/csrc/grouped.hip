@@ -22,18 +22,6 @@ struct RowTile {
 
 __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? lo : (v > hi ? hi : v); }
 
-// Order of the np x nq tiles of one matrix: bands of up to 8 row tiles, in a band column by
-// column. The 32 tiles that run at once on an XCD are then about 8 x 4, which shares both
-// operands' slices in its L2 (one row of tiles would read 33 slices a step instead of 12;
-// 8192 x 8192 x 8192: 1394 -> XX us).
-__device__ __forceinline__ void band_order(int idx, int np, int nq, int& pt, int& qt) {
-  constexpr int kBand = 8;
-  const int band = idx / (kBand * nq), rows = min(kBand, np - band * kBand);
-  idx -= band * kBand * nq;
-  qt = idx / rows;
-  pt = band * kBand + idx - qt * rows;
-}
-
 // Inclusive sum over the lanes of a wave: row shifts inside 16 lanes, then the rows' totals.
 __device__ __forceinline__ int wave_scan(int v) {
   auto step = [&](auto ctrl) __attribute__((always_inline)) {

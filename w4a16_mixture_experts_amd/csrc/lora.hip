@@ -4,18 +4,18 @@
 //
 // (or y[t, :] += the adapter's part when there is no W). Tokens come in any order: nothing is
 // sorted. Two launches:
-//   shrink  v[t, :] = A_a x[t, :] for every token with an adapter. One workgroup per 16 tokens
-//           and adapter among them: the 16 tokens are one MFMA operand, so an adapter is read
-//           once per 16 tokens that hold it; tokens of other adapters are computed along and
-//           dropped.
+//   shrink  v[t, :] = A_a x[t, :] for every token with an adapter. One workgroup per 16 tokens,
+//           adapter among them and 16 ranks of it: the 16 tokens are one MFMA operand, so an
+//           adapter is read once per 16 tokens that hold it; tokens of other adapters are
+//           computed along and dropped.
 //   main    the tiles of x W^T; then, per 16 tokens, one short MFMA chain per adapter among
 //           them adds B_a v to the accumulators of that adapter's tokens.
-// v has 32 bits but B_a v runs on 16-bit MFMA: v is scaled per token by a power of two into
-// [-2, 2] and split into hi + lo, two 16-bit values whose sum is v to 2^-18 (bf16) or 2^-22
-// (fp16) of it; both halves multiply the same B_a in one MFMA (16 summed positions hi, 16 lo).
-// The power of two and the adapter's scale are applied in fp32 to the chain's result.
+// v has 32 bits but B_a v runs on 16-bit MFMA: 16 ranks of a token's v are scaled by a power
+// of two into [-2, 2] and split into hi + lo, two 16-bit values whose sum is v to 2^-16 (bf16)
+// or 2^-22 (fp16) of it; both halves multiply the same B_a in one MFMA (16 summed positions
+// hi, 16 lo). The power of two and the adapter's scale are applied in fp32 to the result.
 #include "exmoe.h"
-#include "gemm_tile.h"
+#include "gemm_wide.h"
 
 namespace exmoe {
 
@@ -33,9 +33,10 @@ struct LoraArgs {
   const int32_t* ids;
   int adapters, rank_max, T, N, K;
   uint16_t* y;
-  int vec;
-  uint16_t* hl;               // [T][2][rank_max]: hi and lo of the scaled v
-  float* mul;                 // [T]: scale_a times the power of two taken out of v
+  int vec8, vec16;            // rows of y can be stored 8 / 16 bytes at a time
+  int rank_blocks;            // ceil(rank_max / 16)
+  uint16_t* hl;               // [T][rank_blocks][2][16]: hi and lo of the scaled v
+  float* mul;                 // [T][rank_blocks]: scale_a times the power of two taken out of v
 };
 
 __device__ __forceinline__ int token_adapter(const LoraArgs& a, int t) {
@@ -47,224 +48,248 @@ __device__ __forceinline__ int adapter_rank(const LoraArgs& a, int ad) {
   return r < 0 ? 0 : (r > a.rank_max ? a.rank_max : r);
 }
 
-// One workgroup of NW waves: 16 tokens, the j-th distinct adapter among them; the waves split
-// K in 32-deep steps and their sums are added in wave order.
-template <class ET, int NW>
-__global__ __launch_bounds__(64 * NW) void lora_shrink_kernel(LoraArgs a) {
-  constexpr int kRB = kMaxRank / 16;
-  __shared__ float s_part[NW][kMaxRank][16];
-  __shared__ uint32_t s_max[16];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int t0 = blockIdx.x * 16;
-  const int id = token_adapter(a, t0 + (lane & 15));
+// The j-th distinct adapter (in token order) among 16 tokens, or -1 (id: the adapter of the
+// lane's token, lane % 16, or -1).
+__device__ __forceinline__ int nth_adapter(int id, int j) {
   uint32_t left = (uint32_t)__ballot(id >= 0) & 0xFFFFu;
-  int ad = -1;
-  for (int j = 0; left; j++) {
-    ad = __builtin_amdgcn_readlane(id, __ffs((int)left) - 1);
-    if (j == (int)blockIdx.y) break;
+  for (; left; j--) {
+    const int ad = __builtin_amdgcn_readlane(id, __ffs((int)left) - 1);
+    if (j == 0) return ad;
     left &= ~(uint32_t)__ballot(id == ad);
   }
-  if (!left) return;   // fewer adapters than workgroups
-  if (tid < 16) s_max[tid] = 0;
-  const int rank = adapter_rank(a, ad), nrb = (rank + 15) / 16;
-  const int t = t0 + (lane & 15);
-  const uint16_t* xp = a.x + (size_t)(t < a.T ? t : a.T - 1) * a.ldx + 8 * (lane >> 4);
-  const uint16_t* ap = a.a + (size_t)ad * a.a_stride + 8 * (lane >> 4);
-  f32x4 acc[kRB];
-#pragma unroll
-  for (int r = 0; r < kRB; r++) acc[r] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const bf16x8 zero = {0, 0, 0, 0, 0, 0, 0, 0};
-  for (int k = 32 * wave; k < a.K; k += 32 * NW) {
-    const bool in = k + 8 * (lane >> 4) < a.K;     // K is a multiple of 8
-    const bf16x8 xv = in ? *reinterpret_cast<const bf16x8*>(xp + k) : zero;
-#pragma unroll
-    for (int r = 0; r < kRB; r++) {
-      if (r >= nrb) break;
-      const int row = 16 * r + (lane & 15);
-      const bf16x8 av = in && row < rank ? *reinterpret_cast<const bf16x8*>(ap + (size_t)row * a.lda + k) : zero;
-      acc[r] = ET::mfma(av, xv, acc[r]);
-    }
-  }
-#pragma unroll
-  for (int r = 0; r < kRB; r++) {
-    if (r >= nrb) break;
-#pragma unroll
-    for (int i = 0; i < 4; i++) s_part[wave][16 * r + 4 * (lane >> 4) + i][lane & 15] = acc[r][i];
-  }
-  __syncthreads();
-  // thread: token tid % 16, rows tid / 16 + 4 NW i
-  constexpr int kPer = kMaxRank / (4 * NW);
-  const int tt = tid & 15, mine = t0 + tt;
-  float v[kPer];
-  float m = 0.f;
-#pragma unroll
-  for (int i = 0; i < kPer; i++) {
-    const int r = (tid >> 4) + 4 * NW * i;
-    v[i] = 0.f;
-    if (r < rank) {
-#pragma unroll
-      for (int w = 0; w < NW; w++) v[i] += s_part[w][r][tt];
-    }
-    m = fmaxf(m, fabsf(v[i]));
-  }
-  atomicMax(&s_max[tt], __float_as_uint(m));   // non-negative floats order as their bits; any order, same result
-  __syncthreads();
-  if (mine >= a.T || token_adapter(a, mine) != ad) return;
-  // 2^e with the largest |v| / 2^e in [1, 2); 1 where nothing finite and normal is there
-  const uint32_t eb = s_max[tt] >> 23;
-  const bool scale = eb >= 1 && eb <= 253;
-  const float down = scale ? __uint_as_float((254 - eb) << 23) : 1.f, up = scale ? __uint_as_float(eb << 23) : 1.f;
-  uint16_t* out = a.hl + (size_t)mine * 2 * a.rank_max;
-#pragma unroll
-  for (int i = 0; i < kPer; i++) {
-    const int r = (tid >> 4) + 4 * NW * i;
-    if (r < a.rank_max) {
-      const float n = v[i] * down;
-      const uint16_t hi = ET::from_f32(n);
-      const float rest = n - ET::to_f32(hi);
-      out[r] = hi;
-      out[a.rank_max + r] = __builtin_isfinite(rest) ? ET::from_f32(rest) : 0;
-    }
-  }
-  if (tid < 16) a.mul[mine] = up * (a.scales ? a.scales[ad] : 1.f);
+  return -1;
 }
 
-// Adds the adapters' parts to the accumulators of one 16-token subtile (acc[j]: 16 columns
-// n0 + 16 j..): per adapter among the tokens one chain over its rank, 16 ranks (hi and lo) a
-// step, kept for the lanes of its own tokens.
-template <class ET, int TQ, int STRIDE>
-__device__ __forceinline__ void lora_expand(const LoraArgs& a, int t, int n0, int lane, f32x4 (&acc)[TQ][STRIDE], int i) {
+// Workgroup (16 tokens, the j-th adapter among them, 16 ranks of it): the waves split K and
+// their sums are added in wave order.
+template <class ET, int NW>
+__global__ __launch_bounds__(64 * NW) void lora_shrink_kernel(LoraArgs a) {
+  static_assert(NW >= 4, "256 threads hold the 16 x 16 sums");
+  __shared__ float s_part[NW][16][17];   // [wave][token][rank]
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int t0 = blockIdx.x * 16, r0 = 16 * blockIdx.z;
+  const int ad = nth_adapter(token_adapter(a, t0 + (lane & 15)), blockIdx.y);
+  if (ad < 0) return;   // fewer adapters than workgroups
+  const int rank = adapter_rank(a, ad);
+  if (r0 >= rank) return;
+  const int t = t0 + (lane & 15), r = r0 + (lane & 15);
+  const size_t xrow[1] = {(size_t)(t < a.T ? t : a.T - 1) * a.ldx};
+  const size_t arow[1] = {(size_t)ad * a.a_stride + (size_t)(r < rank ? r : rank - 1) * a.lda};
+  f32x4 acc[1][1] = {{{0.f, 0.f, 0.f, 0.f}}};
+  skinny_product<ET, 1, 1, NW, true>(a.x, xrow, a.a, arow, a.K, wave, lane, acc);
+#pragma unroll
+  for (int i = 0; i < 4; i++) s_part[wave][lane & 15][4 * (lane >> 4) + i] = acc[0][0][i];
+  __syncthreads();
+  // thread: token tid / 16, rank tid % 16 (rows of 16 lanes hold a token)
+  const int mine = t0 + (tid >> 4);
+  if (tid >= 256 || mine >= a.T || token_adapter(a, mine) != ad) return;
+  float v = 0.f;
+  if (r0 + (tid & 15) < rank) {
+#pragma unroll
+    for (int w = 0; w < NW; w++) v += s_part[w][tid >> 4][tid & 15];
+  }
+  float m = fabsf(v);   // (fmaxf drops a NaN)
+  m = fmaxf(m, __uint_as_float(dpp_u32<0x121>(__float_as_uint(m))));
+  m = fmaxf(m, __uint_as_float(dpp_u32<0x122>(__float_as_uint(m))));
+  m = fmaxf(m, __uint_as_float(dpp_u32<0x124>(__float_as_uint(m))));
+  m = fmaxf(m, __uint_as_float(dpp_u32<0x128>(__float_as_uint(m))));
+  // 2^e with the largest |v| / 2^e in [1, 2); 1 where nothing finite and normal is there
+  const uint32_t eb = __float_as_uint(m) >> 23;
+  const bool scale = eb >= 1 && eb <= 253;
+  const float down = scale ? __uint_as_float((254 - eb) << 23) : 1.f, up = scale ? __uint_as_float(eb << 23) : 1.f;
+  const float n = v * down;
+  const uint16_t hi = ET::from_f32(n);
+  const float rest = n - ET::to_f32(hi);
+  const size_t block = (size_t)mine * a.rank_blocks + blockIdx.z;
+  uint16_t* out = a.hl + 32 * block + (tid & 15);
+  out[0] = hi;
+  out[16] = __builtin_isfinite(rest) ? ET::from_f32(rest) : 0;
+  if ((tid & 15) == 0) a.mul[block] = up * (a.scales ? a.scales[ad] : 1.f);
+}
+
+// Eight elements of b: ranks c..c + 7 of column n, zeros from the adapter's rank on (what
+// lies there may be anything).
+__device__ __forceinline__ bf16x8 load_b(const LoraArgs& a, int ad, int rank, int n, int c) {
+  const int have = rank - c;
+  bf16x8 v = {0, 0, 0, 0, 0, 0, 0, 0};
+  if (have > 0)
+    v = *reinterpret_cast<const bf16x8*>(a.b + (size_t)ad * a.b_stride + (size_t)(n < a.N ? n : a.N - 1) * a.ldb + c);
+  if (have < 8) {
+#pragma unroll
+    for (int q = 0; q < 8; q++) v[q] = q < have ? v[q] : (short)0;
+  }
+  return v;
+}
+
+// Adds the adapters' parts to the sums of one block of 16 tokens and 16 columns (acc[j]:
+// columns n0 + 16 j..): per adapter and 16 ranks one MFMA (hi and lo), kept for the lanes of
+// the adapter's own tokens. This wave takes the adapters w, w + NW, ... among the tokens.
+template <class ET, int TQ, int TP, int NW>
+__device__ __forceinline__ void lora_expand16(const LoraArgs& a, int t, int n0, int wave, int lane, f32x4 (&acc)[TQ][TP],
+                                              int i) {
   const int id = token_adapter(a, t);
+  const size_t tok = (size_t)(t < a.T ? t : a.T - 1) * a.rank_blocks;
   uint32_t left = (uint32_t)__ballot(id >= 0) & 0xFFFFu;
-  if (!left) return;
-  const float mul = id >= 0 ? a.mul[t] : 0.f;
-  const uint16_t* hl = a.hl + (size_t)(t < a.T ? t : a.T - 1) * 2 * a.rank_max + (lane >> 5) * a.rank_max;
-  const bf16x8 zero = {0, 0, 0, 0, 0, 0, 0, 0};
+  for (int which = 0; left; which++) {
+    const int ad = __builtin_amdgcn_readlane(id, __ffs((int)left) - 1);
+    left &= ~(uint32_t)__ballot(id == ad);
+    if (which % NW != wave) continue;
+    const int rank = adapter_rank(a, ad);
+    for (int rb = 0; 16 * rb < rank; rb++) {
+      bf16x8 vv = {0, 0, 0, 0, 0, 0, 0, 0};
+      float mul = 0.f;
+      if (id == ad) {
+        vv = *reinterpret_cast<const bf16x8*>(a.hl + 32 * (tok + rb) + 8 * (lane >> 4));
+        mul = a.mul[tok + rb];
+      }
+#pragma unroll
+      for (int j = 0; j < TQ; j++) {
+        const f32x4 d = ET::mfma(load_b(a, ad, rank, n0 + 16 * j + (lane & 15), 16 * rb + 8 * ((lane >> 4) & 1)), vv,
+                                 f32x4{0.f, 0.f, 0.f, 0.f});
+        if (id == ad) {
+#pragma unroll
+          for (int q = 0; q < 4; q++) acc[j][i][q] += mul * d[q];
+        }
+      }
+    }
+  }
+}
+
+// The same for a block of 32 tokens and TQ blocks of 32 columns on 32 x 32 x 16 MFMA: two per
+// adapter and 16 ranks (8 ranks each: hi in lanes 0..31, lo in lanes 32..63).
+template <class ET, int TQ, int TP>
+__device__ __forceinline__ void lora_expand32(const LoraArgs& a, int t, int n0, int lane, f32x16 (&acc)[TQ][TP], int i) {
+  const int id = token_adapter(a, t);
+  const size_t tok = (size_t)(t < a.T ? t : a.T - 1) * a.rank_blocks;
+  uint32_t left = (uint32_t)__ballot(id >= 0);
   while (left) {
     const int ad = __builtin_amdgcn_readlane(id, __ffs((int)left) - 1);
     left &= ~(uint32_t)__ballot(id == ad);
     const int rank = adapter_rank(a, ad);
-    f32x4 d[TQ];
-#pragma unroll
-    for (int j = 0; j < TQ; j++) d[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int r0 = 0; r0 < rank; r0 += 16) {
-      const int col = r0 + 8 * ((lane >> 4) & 1), have = rank - col;
-      const bf16x8 vv = have > 0 && id == ad ? *reinterpret_cast<const bf16x8*>(hl + col) : zero;
+    for (int rb = 0; 16 * rb < rank; rb++) {
+      bf16x8 v0 = {0, 0, 0, 0, 0, 0, 0, 0}, v1 = v0;
+      float mul = 0.f;
+      if (id == ad) {
+        const uint16_t* p = a.hl + 32 * (tok + rb) + 16 * (lane >> 5);
+        v0 = *reinterpret_cast<const bf16x8*>(p);
+        v1 = *reinterpret_cast<const bf16x8*>(p + 8);
+        mul = a.mul[tok + rb];
+      }
 #pragma unroll
       for (int j = 0; j < TQ; j++) {
-        int n = n0 + 16 * j + (lane & 15);
-        n = n < a.N ? n : a.N - 1;
-        bf16x8 bv = have > 0 ? *reinterpret_cast<const bf16x8*>(a.b + (size_t)ad * a.b_stride + (size_t)n * a.ldb + col) : zero;
-        if (have < 8) {   // columns past the rank may hold anything
+        const int n = n0 + 32 * j + (lane & 31);
+        f32x16 d;
 #pragma unroll
-          for (int q = 0; q < 8; q++) bv[q] = q < have ? bv[q] : (short)0;
+        for (int q = 0; q < 16; q++) d[q] = 0.f;
+        d = mfma32(ET{}, load_b(a, ad, rank, n, 16 * rb), v0, d);
+        d = mfma32(ET{}, load_b(a, ad, rank, n, 16 * rb + 8), v1, d);
+        if (id == ad) {
+#pragma unroll
+          for (int q = 0; q < 16; q++) acc[j][i][q] += mul * d[q];
         }
-        d[j] = ET::mfma(bv, vv, d[j]);
       }
-    }
-    if (id == ad) {
-#pragma unroll
-      for (int j = 0; j < TQ; j++)
-#pragma unroll
-        for (int q = 0; q < 4; q++) acc[j][i][q] += mul * d[j][q];
     }
   }
 }
 
-// One BP x BQ tile of y (BP tokens, BQ columns) per workgroup: the product with W on the
-// shared tile loop (W given), the adapters' parts, one rounding.
-template <class ET, int BP, int BQ, int WP, int WQ>
-__global__ __launch_bounds__(64 * WP * WQ) void lora_tile_kernel(LoraArgs a, int p_tiles) {
-  constexpr int NW = WP * WQ, TP = BP / WP / 16, TQ = BQ / WQ / 16;
-  using OpP = RowOperand<BP, NW, true>;
-  using OpQ = RowOperand<BQ, NW, true>;
-  __shared__ __attribute__((aligned(16))) uint16_t s_p0[BP * kBK], s_p1[BP * kBK], s_q0[BQ * kBK], s_q1[BQ * kBK];
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wp = wave / WQ, wq = wave % WQ;
-  const int idx = xcd_contiguous(blockIdx.x, gridDim.x);
-  const int p0 = idx % p_tiles * BP, q0 = idx / p_tiles * BQ;
-
+// Few tokens: 16 TP tokens x 16 TQ columns per workgroup, W streamed once per 16 TP tokens;
+// the waves split K, and the adapters among the tokens, before their sums are added.
+template <class ET, int TP, int TQ, int NW>
+__global__ __launch_bounds__(64 * NW) void lora_skinny_kernel(LoraArgs a) {
+  __shared__ f32x4 s_part[NW][TQ * TP][64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int n0 = blockIdx.x * 16 * TQ, t0 = blockIdx.y * 16 * TP;
   f32x4 acc[TQ][TP];
+  size_t xrow[TP], wrow[TQ];
 #pragma unroll
-  for (int j = 0; j < TQ; j++)
+  for (int j = 0; j < TQ; j++) {
+    const int n = n0 + 16 * j + (lane & 15);
+    wrow[j] = (size_t)(n < a.N ? n : a.N - 1) * a.ldw;
 #pragma unroll
     for (int i = 0; i < TP; i++) acc[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-  if (a.w) {
-    OpP op_p;
-    OpQ op_q;
-    op_p.init(a.x, a.K, wave, lane, [&](int i) { return (size_t)(p0 + i < a.T ? p0 + i : a.T - 1) * a.ldx; });
-    op_q.init(a.w, a.K, wave, lane, [&](int i) { return (size_t)(q0 + i < a.N ? q0 + i : a.N - 1) * a.ldw; });
-    const int steps = (a.K + kBK - 1) / kBK;
-    auto step = [&](int s, const uint16_t* cp, const uint16_t* cq, uint16_t* np, uint16_t* nq) {
-      __builtin_amdgcn_s_waitcnt(0);
-      __syncthreads();
-      if (s + 1 < steps) {
-        op_p.stage(np, (s + 1) * kBK, wave, lane);
-        op_q.stage(nq, (s + 1) * kBK, wave, lane);
-      }
-#pragma unroll
-      for (int kk = 0; kk < 2; kk++) {
-        bf16x8 fq[TQ], fp[TP];
-#pragma unroll
-        for (int j = 0; j < TQ; j++) fq[j] = OpQ::frag(cq, (wq * TQ + j) * 16, kk, lane);
-#pragma unroll
-        for (int i = 0; i < TP; i++) fp[i] = OpP::frag(cp, (wp * TP + i) * 16, kk, lane);
-#pragma unroll
-        for (int i = 0; i < TP; i++)
-#pragma unroll
-          for (int j = 0; j < TQ; j++) acc[j][i] = ET::mfma(fq[j], fp[i], acc[j][i]);
-      }
-    };
-    op_p.stage(s_p0, 0, wave, lane);
-    op_q.stage(s_q0, 0, wave, lane);
-    for (int s = 0; s < steps; s += 2) {
-      step(s, s_p0, s_q0, s_p1, s_q1);
-      if (s + 1 < steps) step(s + 1, s_p1, s_q1, s_p0, s_q0);
-    }
   }
-
-  const int n0 = q0 + wq * TQ * 16;
 #pragma unroll
   for (int i = 0; i < TP; i++) {
-    const int t = p0 + (wp * TP + i) * 16 + (lane & 15);
-    if (!a.w && t < a.T) {
-#pragma unroll
-      for (int j = 0; j < TQ; j++)
-#pragma unroll
-        for (int q = 0; q < 4; q++) {
-          const int n = n0 + 16 * j + 4 * (lane >> 4) + q;
-          if (n < a.N) acc[j][i][q] = ET::to_f32(a.y[(size_t)t * a.ldy + n]);
-        }
-    }
-    lora_expand<ET, TQ, TP>(a, t, n0, lane, acc, i);
-    // without W, tokens without an adapter keep their y as it is
-    if (t >= a.T || (!a.w && token_adapter(a, t) < 0)) continue;
-#pragma unroll
-    for (int j = 0; j < TQ; j++) {
-      const int n = n0 + 16 * j + 4 * (lane >> 4);
-      if (n < a.N) store4<ET>(a.y, (size_t)t * a.ldy + n, false, a.vec, a.N - n, acc[j][i]);
-    }
+    const int t = t0 + 16 * i + (lane & 15);
+    xrow[i] = (size_t)(t < a.T ? t : a.T - 1) * a.ldx;
   }
+  if (a.w) skinny_product<ET, TP, TQ, NW, true>(a.x, xrow, a.w, wrow, a.K, wave, lane, acc);
+#pragma unroll
+  for (int i = 0; i < TP; i++) lora_expand16<ET, TQ, TP, NW>(a, t0 + 16 * i + (lane & 15), n0, wave, lane, acc, i);
+  f32x4 v = skinny_reduce<TP, TQ, NW>(s_part, acc, wave, lane);
+  const int t = t0 + 16 * (wave % TP) + (lane & 15), n = n0 + 16 * (wave / TP) + 4 * (lane >> 4);
+  if (wave >= TQ * TP || t >= a.T || n >= a.N) return;
+  if (!a.w) {
+    if (token_adapter(a, t) < 0) return;   // keeps its y as it is
+#pragma unroll
+    for (int q = 0; q < 4; q++)
+      if (n + q < a.N) v[q] += ET::to_f32(a.y[(size_t)t * a.ldy + n + q]);
+  }
+  store4<ET>(a.y, (size_t)t * a.ldy + n, false, a.vec8, a.N - n, v);
+}
+
+// Many tokens: the pipelined tiles of x W^T (gemm_wide.h), the adapters' parts added to a
+// tile's sums before they are stored.
+template <class ET, int TP, int TQ, int WP, int WQ, int OCC>
+__global__ __launch_bounds__(64 * WP * WQ, OCC) void lora_wide_kernel(LoraArgs a, int p_tiles, int q_tiles) {
+  constexpr int NW = WP * WQ, BP = 32 * TP * WP, BQ = 32 * TQ * WQ;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int pt, qt;
+  band_order(xcd_contiguous(blockIdx.x, gridDim.x), p_tiles, q_tiles, pt, qt);
+  const int p0 = pt * BP, q0 = qt * BQ;
+  WideRows<BP, NW, 64> op_p;
+  WideRows<BQ, NW, 64> op_q;
+  op_p.init(make_buf(a.x, 2 * ((a.T - 1) * a.ldx + a.K)), a.K, wave, lane,
+            [&](int i) { return p0 + i < a.T ? (uint32_t)((size_t)(p0 + i) * a.ldx * 2) : kNowhere; });
+  op_q.init(make_buf(a.w, 2 * ((a.N - 1) * a.ldw + a.K)), a.K, wave, lane,
+            [&](int i) { return q0 + i < a.N ? (uint32_t)((size_t)(q0 + i) * a.ldw * 2) : kNowhere; });
+  const int n0 = q0 + 32 * TQ * (wave % WQ);
+  wide_tile<ET, TP, TQ, WP, WQ, 64, false>(
+      op_p, op_q, a.K, p0, a.T, q0, a.N, TileOut{a.y, 0, a.ldy, false, a.vec16 != 0}, [](int) { return 0; },
+      [](int) { return 0u; }, [&](int i, int t, auto& acc) { lora_expand32<ET, TQ, TP>(a, t, n0, lane, acc, i); },
+      [](int p) { return p; });
 }
 
 // ------------------------------------------------------------------------------------ host
-static inline size_t lora_hl_bytes(int T, int rank_max) { return ((size_t)T * 2 * rank_max * 2 + 255) & ~(size_t)255; }
+static inline size_t lora_hl_bytes(int T, int rank_max) { return (size_t)T * ((rank_max + 15) / 16) * 64; }
 
+template <class ET, int TP, int TQ, int NW>
+static hipError_t launch_skinny(const LoraArgs& a, hipStream_t s) {
+  ProfScope prof("lora_linear", s);
+  EXMOE_LAUNCH(prof, (lora_skinny_kernel<ET, TP, TQ, NW>), dim3((a.N + 16 * TQ - 1) / (16 * TQ), (a.T + 16 * TP - 1) / (16 * TP)),
+               dim3(64 * NW), 0, s, a);
+  return hipGetLastError();
+}
+template <class ET, int TP, int TQ, int WP, int WQ, int OCC>
+static hipError_t launch_lora_wide(const LoraArgs& a, hipStream_t s) {
+  constexpr int BP = 32 * TP * WP, BQ = 32 * TQ * WQ;
+  const int pt = (a.T + BP - 1) / BP, qt = (a.N + BQ - 1) / BQ;
+  ProfScope prof("lora_linear", s);
+  EXMOE_LAUNCH(prof, (lora_wide_kernel<ET, TP, TQ, WP, WQ, OCC>), dim3(pt * qt), dim3(64 * WP * WQ), 0, s, a, pt, qt);
+  return hipGetLastError();
+}
+
+#ifndef SKT
+#define SKT 512
+#endif
 template <class ET>
 static hipError_t launch_lora(const LoraArgs& a, hipStream_t s) {
-  const int pt = (a.T + 127) / 128, qt = (a.N + 127) / 128;
   const int distinct = a.adapters < 16 ? a.adapters : 16;
   {
     ProfScope prof("lora_shrink", s);
-    EXMOE_LAUNCH(prof, (lora_shrink_kernel<ET, 4>), dim3((a.T + 15) / 16, distinct), dim3(256), 0, s, a);
+    EXMOE_LAUNCH(prof, (lora_shrink_kernel<ET, 8>), dim3((a.T + 15) / 16, distinct, a.rank_blocks), dim3(512), 0, s, a);
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  ProfScope prof("lora_linear", s);
-  EXMOE_LAUNCH(prof, (lora_tile_kernel<ET, 128, 128, 2, 2>), dim3(pt * qt), dim3(256), 0, s, a, pt);
-  return hipGetLastError();
+  const bool span = 2 * ((size_t)(a.T - 1) * a.ldx + a.K) < kMaxSpan && 2 * ((size_t)(a.N - 1) * a.ldw + a.K) < kMaxSpan;
+  if (a.w && span && a.T > SKT) {
+    if ((long long)((a.T + 255) / 256) * ((a.N + 255) / 256) >= 256) return launch_lora_wide<ET, 4, 2, 2, 4, 2>(a, s);
+    return launch_lora_wide<ET, 2, 2, 2, 2, 2>(a, s);
+  }
+  if (a.T <= 16) return launch_skinny<ET, 1, 1, 8>(a, s);
+  if (a.T <= 32) return launch_skinny<ET, 2, 1, 8>(a, s);
+  return launch_skinny<ET, 4, 1, 8>(a, s);
 }
 
 static int lora_shape(int T, int N, int K, int adapters, int rank_max) {
@@ -274,7 +299,7 @@ static int lora_shape(int T, int N, int K, int adapters, int rank_max) {
   if (adapters < 1) return set_error(EXMOE_ERR_INVALID_ARGUMENT, "adapters must be positive (got %d)", adapters);
   if (rank_max < 8 || rank_max % 8 || rank_max > kMaxRank)
     return set_error(EXMOE_ERR_INVALID_ARGUMENT, "rank_max must be a multiple of 8 in [8, 128] (got %d)", rank_max);
-  if ((long long)((T + 127) / 128) * ((N + 127) / 128) * 256 > 0xFFFFFFFFll)
+  if ((long long)((T + 63) / 64) * ((N + 15) / 16) * 512 > 0xFFFFFFFFll)
     return set_error(EXMOE_ERR_UNSUPPORTED, "T x N has too many output tiles for one launch");
   return EXMOE_OK;
 }
@@ -293,7 +318,7 @@ using namespace exmoe;
 
 extern "C" size_t exmoe_lora_workspace_bytes(int T, int N, int K, int adapters, int rank_max) {
   if (lora_shape(T, N, K, adapters, rank_max)) return 0;
-  return lora_hl_bytes(T, rank_max) + (size_t)T * 4;
+  return lora_hl_bytes(T, rank_max) + (size_t)T * ((rank_max + 15) / 16) * 4;
 }
 
 extern "C" int exmoe_lora_linear(const void* x, size_t ldx, const void* w, size_t ldw, const exmoe_lora_bank* bank,
@@ -325,7 +350,8 @@ extern "C" int exmoe_lora_linear(const void* x, size_t ldx, const void* w, size_
   a.a = static_cast<const uint16_t*>(bank->a); a.b = static_cast<const uint16_t*>(bank->b); a.lda = bank->lda;
   a.a_stride = bank->a_stride; a.ldb = bank->ldb; a.b_stride = bank->b_stride; a.ranks = bank->ranks;
   a.scales = bank->scales; a.ids = adapter_ids; a.adapters = bank->adapters; a.rank_max = bank->rank_max; a.T = T;
-  a.N = N; a.K = K; a.y = static_cast<uint16_t*>(y); a.vec = (uintptr_t)y % 8 == 0 && ldy % 4 == 0;
+  a.N = N; a.K = K; a.y = static_cast<uint16_t*>(y); a.vec8 = (uintptr_t)y % 8 == 0 && ldy % 4 == 0;
+  a.vec16 = aligned16(y) && ldy % 8 == 0; a.rank_blocks = (bank->rank_max + 15) / 16;
   a.hl = static_cast<uint16_t*>(workspace);
   a.mul = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + lora_hl_bytes(T, bank->rank_max));
   const hipError_t e = dtype == EXMOE_DTYPE_FP16 ? launch_lora<ElemFP16>(a, stream) : launch_lora<ElemBF16>(a, stream);
