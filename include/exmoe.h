@@ -407,7 +407,7 @@ int exmoe_grouped_mm_wgrad(const void* dy, size_t lddy, const void* x, size_t ld
  *
  * x [T, K], w [N, K], y [T, N] and the bank are bf16 or all fp16 (dtype), last axis
  * contiguous, ld* elements between rows. K and rank_max are multiples of 8, rank_max <= 128,
- * rows of x, w, a and b 16-byte aligned (ld and strides multiples of 8); N is any size. The
+ * rows of x, w, a and b 16-byte aligned (ld and strides multiples of 8, ld <= 2^24); N is any size. The
  * bank's adapters lie a_stride / b_stride elements apart; ranks int32 [adapters] (clamped to
  * [0, rank_max]; what a and b hold past an adapter's rank is not used) and scales fp32
  * [adapters] are device arrays or NULL (rank_max, 1). y must not overlap the inputs.

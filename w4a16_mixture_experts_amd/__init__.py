@@ -388,72 +388,80 @@ def moe_layer_noalloc(x, w_router, bank: ExpertBank, I: int, k: int, buffers: La
 
 # ----------------------------------------------------------------------------- grouped products
 def _dtype_code(dtype) -> int:
-    torch = _torch()
-    codes = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_FP16, torch.float32: DTYPE_FP32}
-    if dtype not in codes:
+    global _DTYPE_CODES
+    if _DTYPE_CODES is None:
+        torch = _torch()
+        _DTYPE_CODES = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_FP16, torch.float32: DTYPE_FP32}
+    code = _DTYPE_CODES.get(dtype)
+    if code is None:
         raise ValueError(f"unsupported dtype {dtype}: bfloat16, float16 or float32")
-    return codes[dtype]
+    return code
+
+
+_DTYPE_CODES = None
 
 
 def _rows_ld(name: str, t, ndim: int = 2) -> int:
     """Elements between the rows of a GPU tensor whose last axis is contiguous."""
-    if t.dim() != ndim:
-        raise ValueError(f"{name} must have {ndim} axes (got shape {tuple(t.shape)})")
+    stride, shape = t.stride(), t.shape
+    if len(stride) != ndim:
+        raise ValueError(f"{name} must have {ndim} axes (got shape {tuple(shape)})")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    if stride[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name}: the last axis must be contiguous")
-    return t.stride(-2) if t.shape[-2] > 1 else max(t.stride(-2), t.shape[-1])
+    return stride[-2] if shape[-2] > 1 else max(stride[-2], shape[-1])
 
 
 def _expert_stride(t, ld: int) -> int:
     return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * ld)
 
 
-def _int32(name: str, t, like, numel: Optional[int] = None):
-    torch = _torch()
+def _int32(name: str, t, dev: int, numel: Optional[int] = None):
     if t is None:
         return None
-    if t.dtype != torch.int32 or t.device != like.device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor on {like.device}")
+    if t.dtype is not _torch().int32 or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor on GPU {dev}")
     if numel is not None and t.numel() != numel:
         raise ValueError(f"{name} must have {numel} entries (got {t.numel()})")
     return t.data_ptr()
 
 
-def _result(name: str, out, shape, dtype, like):
-    torch = _torch()
+def _result(name: str, out, shape, dtype, dev: int):
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    if tuple(out.shape) != tuple(shape) or out.dtype != dtype or out.device != like.device:
-        raise ValueError(f"{name} must be {tuple(shape)} {dtype} on {like.device}")
+        return _torch().empty(shape, dtype=dtype, device=f"cuda:{dev}")
+    if out.shape != shape or out.dtype is not dtype or out.get_device() != dev:
+        raise ValueError(f"{name} must be {tuple(shape)} {dtype} on GPU {dev}")
     return out
 
 
-def _scratch(workspace, need: int, like):
-    """(pointer, bytes) of the caller's workspace, or of a new one of the needed size."""
+def _scratch(workspace, need, dev: int):
+    """(pointer, bytes, tensor) of the caller's workspace, or of a new one of need() bytes."""
     if workspace is None:
-        if not need:
+        n = need()
+        if not n:
             return None, 0, None
-        workspace = _torch().empty(need, dtype=_torch().uint8, device=like.device)
-    elif workspace.device != like.device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {like.device}")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+        workspace = _torch().empty(n, dtype=_torch().uint8, device=f"cuda:{dev}")
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on GPU {dev}")
+    return workspace.data_ptr(), workspace.nbytes, workspace
 
 
-def _run_on(like, fn, *args):
-    """Calls a C entry point on the device of `like`, on that device's current stream."""
+def _run_on(dev: int, fn, *args):
+    """Calls a C entry point on GPU dev, on that device's current stream."""
     torch = _torch()
-    if like.device.index == torch.cuda.current_device():
-        _check(fn(*args, torch.cuda.current_stream().cuda_stream))
+    if dev == torch.cuda.current_device():
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
-        with torch.cuda.device(like.device):
-            _check(fn(*args, torch.cuda.current_stream().cuda_stream))
+        with torch.cuda.device(dev):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        _check(st)
 
 
-def _same(name: str, t, like):
-    if t.dtype != like.dtype or t.device != like.device:
-        raise ValueError(f"{name} must be {like.dtype} on {like.device}")
+def _same(name: str, t, dtype, dev: int):
+    if t.dtype is not dtype or t.get_device() != dev:
+        raise ValueError(f"{name} must be {dtype} on GPU {dev}")
 
 
 def grouped_mm_workspace_bytes(op: int, rows: int, N: int, K: int, E: int, k: int = 0) -> int:
@@ -468,18 +476,19 @@ def grouped_mm(x, w, offsets, row_index=None, row_div: int = 1, out_dtype=None, 
     of a routed batch), or None for src(s) = s. Returns y [rows, N] in out_dtype (x's type
     or fp32); its rows outside every segment are left as they are."""
     ldx, ldw = _rows_ld("x", x), _rows_ld("w", w, 3)
-    _same("w", w, x)
+    dev, dtype = x.get_device(), x.dtype
+    _same("w", w, dtype, dev)
     E, N, K = w.shape
-    if x.shape[1] != K:
-        raise ValueError(f"x has {x.shape[1]} columns, w takes {K}")
-    rows = x.shape[0] if row_index is None else row_index.numel()
-    out_dtype = x.dtype if out_dtype is None else out_dtype
-    y = _result("y", y, (rows, N), out_dtype, x)
-    need = grouped_mm_workspace_bytes(GROUPED_MM, rows, N, K, E) if workspace is None else 0
-    ws, ws_bytes, _keep = _scratch(workspace, need, x)
-    _run_on(x, _lib.exmoe_grouped_mm, x.data_ptr(), ldx, x.shape[0], _int32("row_index", row_index, x), row_div,
-            _int32("offsets", offsets, x, E + 1), w.data_ptr(), ldw, _expert_stride(w, ldw), rows, N, K, E,
-            _dtype_code(x.dtype), _dtype_code(out_dtype), y.data_ptr(), _rows_ld("y", y), ws, ws_bytes)
+    x_rows, x_cols = x.shape
+    if x_cols != K:
+        raise ValueError(f"x has {x_cols} columns, w takes {K}")
+    rows = x_rows if row_index is None else row_index.numel()
+    out_dtype = dtype if out_dtype is None else out_dtype
+    y = _result("y", y, (rows, N), out_dtype, dev)
+    ws, ws_bytes, _keep = _scratch(workspace, lambda: grouped_mm_workspace_bytes(GROUPED_MM, rows, N, K, E), dev)
+    _run_on(dev, _lib.exmoe_grouped_mm, x.data_ptr(), ldx, x_rows, _int32("row_index", row_index, dev), row_div,
+            _int32("offsets", offsets, dev, E + 1), w.data_ptr(), ldw, _expert_stride(w, ldw), rows, N, K, E,
+            _dtype_code(dtype), _dtype_code(out_dtype), y.data_ptr(), _rows_ld("y", y), ws, ws_bytes)
     return y
 
 
@@ -487,42 +496,42 @@ def grouped_mm_dgrad(dy, w, offsets, flat_to_sorted=None, k: int = 1, out_dtype=
     """Gradient of grouped_mm with respect to x: dx[s, :] = dy[s, :] @ w[e] per row, or, with
     flat_to_sorted int32 [T * k], summed over the k rows of each token (dx [T, K])."""
     lddy, ldw = _rows_ld("dy", dy), _rows_ld("w", w, 3)
-    _same("w", w, dy)
+    dev, dtype = dy.get_device(), dy.dtype
+    _same("w", w, dtype, dev)
     E, N, K = w.shape
-    rows = dy.shape[0]
-    if dy.shape[1] != N:
-        raise ValueError(f"dy has {dy.shape[1]} columns, w gives {N}")
+    rows, dy_cols = dy.shape
+    if dy_cols != N:
+        raise ValueError(f"dy has {dy_cols} columns, w gives {N}")
     if flat_to_sorted is not None and (k < 1 or rows % k):
         raise ValueError(f"dy's {rows} rows are no multiple of k = {k}")
-    out_dtype = dy.dtype if out_dtype is None else out_dtype
-    dx = _result("dx", dx, (rows if flat_to_sorted is None else rows // k, K), out_dtype, dy)
-    sum_k = 0 if flat_to_sorted is None else k
-    need = grouped_mm_workspace_bytes(GROUPED_DGRAD, rows, N, K, E, sum_k) if workspace is None else 0
-    ws, ws_bytes, _keep = _scratch(workspace, need, dy)
-    _run_on(dy, _lib.exmoe_grouped_mm_dgrad, dy.data_ptr(), lddy, _int32("offsets", offsets, dy, E + 1), w.data_ptr(),
-            ldw, _expert_stride(w, ldw), _int32("flat_to_sorted", flat_to_sorted, dy, rows), k, rows, N, K, E,
-            _dtype_code(dy.dtype), _dtype_code(out_dtype), dx.data_ptr(), _rows_ld("dx", dx), ws, ws_bytes)
+    out_dtype = dtype if out_dtype is None else out_dtype
+    dx = _result("dx", dx, (rows if flat_to_sorted is None else rows // k, K), out_dtype, dev)
+    ws, ws_bytes, _keep = _scratch(
+        workspace, lambda: grouped_mm_workspace_bytes(GROUPED_DGRAD, rows, N, K, E, 0 if flat_to_sorted is None else k), dev)
+    _run_on(dev, _lib.exmoe_grouped_mm_dgrad, dy.data_ptr(), lddy, _int32("offsets", offsets, dev, E + 1), w.data_ptr(),
+            ldw, _expert_stride(w, ldw), _int32("flat_to_sorted", flat_to_sorted, dev, rows), k, rows, N, K, E,
+            _dtype_code(dtype), _dtype_code(out_dtype), dx.data_ptr(), _rows_ld("dx", dx), ws, ws_bytes)
     return dx
 
 
 def grouped_mm_wgrad(dy, x, offsets, row_index=None, row_div: int = 1, out_dtype=None, dw=None, workspace=None):
     """Gradient of grouped_mm with respect to w: dw[e] = sum over its rows of dy[s]^T x[src(s)],
     zeros for an expert without rows. out_dtype defaults to fp32."""
-    torch = _torch()
     lddy, ldx = _rows_ld("dy", dy), _rows_ld("x", x)
-    _same("x", x, dy)
+    dev, dtype = dy.get_device(), dy.dtype
+    _same("x", x, dtype, dev)
     rows, N = dy.shape
-    K, E = x.shape[1], offsets.numel() - 1
-    out_dtype = torch.float32 if out_dtype is None else out_dtype
-    dw = _result("dw", dw, (E, N, K), out_dtype, dy)
+    x_rows, K = x.shape
+    E = offsets.numel() - 1
+    if row_index is None and x_rows < rows:
+        raise ValueError(f"x has {x_rows} rows, dy has {rows}")
+    out_dtype = _torch().float32 if out_dtype is None else out_dtype
+    dw = _result("dw", dw, (E, N, K), out_dtype, dev)
     lddw = _rows_ld("dw", dw, 3)
-    need = grouped_mm_workspace_bytes(GROUPED_WGRAD, rows, N, K, E) if workspace is None else 0
-    ws, ws_bytes, _keep = _scratch(workspace, need, dy)
-    if row_index is None and x.shape[0] < rows:
-        raise ValueError(f"x has {x.shape[0]} rows, dy has {rows}")
-    _run_on(dy, _lib.exmoe_grouped_mm_wgrad, dy.data_ptr(), lddy, x.data_ptr(), ldx, x.shape[0],
-            _int32("row_index", row_index, dy, rows), row_div, _int32("offsets", offsets, dy, E + 1), rows, N, K, E,
-            _dtype_code(dy.dtype), _dtype_code(out_dtype), dw.data_ptr(), lddw, _expert_stride(dw, lddw), ws, ws_bytes)
+    ws, ws_bytes, _keep = _scratch(workspace, lambda: grouped_mm_workspace_bytes(GROUPED_WGRAD, rows, N, K, E), dev)
+    _run_on(dev, _lib.exmoe_grouped_mm_wgrad, dy.data_ptr(), lddy, x.data_ptr(), ldx, x_rows,
+            _int32("row_index", row_index, dev, rows), row_div, _int32("offsets", offsets, dev, E + 1), rows, N, K, E,
+            _dtype_code(dtype), _dtype_code(out_dtype), dw.data_ptr(), lddw, _expert_stride(dw, lddw), ws, ws_bytes)
     return dw
 
 
@@ -532,19 +541,20 @@ class LoraBank:
     contiguous), ranks int32 [L] (None: all R) and scales fp32 [L] (None: all 1)."""
 
     def __init__(self, a, b, ranks=None, scales=None):
-        torch = _torch()
         lda, ldb = _rows_ld("a", a, 3), _rows_ld("b", b, 3)
-        _same("b", b, a)
+        dev = a.get_device()
+        _same("b", b, a.dtype, dev)
         if a.shape[0] != b.shape[0] or a.shape[1] != b.shape[2]:
             raise ValueError(f"a {tuple(a.shape)} and b {tuple(b.shape)} must be [L, R, K] and [L, N, R]")
         L, R, self.K = a.shape
         self.N = b.shape[1]
-        self.a, self.b, self.ranks, self.scales = a, b, ranks, scales      # kept alive
-        if scales is not None and (scales.dtype != torch.float32 or scales.device != a.device
+        if scales is not None and (scales.dtype is not _torch().float32 or scales.get_device() != dev
                                    or not scales.is_contiguous() or scales.numel() != L):
-            raise ValueError(f"scales must be a contiguous float32 tensor of {L} on {a.device}")
+            raise ValueError(f"scales must be a contiguous float32 tensor of {L} on GPU {dev}")
+        self.a, self.b, self.ranks, self.scales = a, b, ranks, scales      # kept alive
         self.c = LoraBankC(a.data_ptr(), lda, _expert_stride(a, lda), b.data_ptr(), ldb, _expert_stride(b, ldb),
-                           _int32("ranks", ranks, a, L), _ptr(scales), L, R)
+                           _int32("ranks", ranks, dev, L), _ptr(scales), L, R)
+        self.ref = ctypes.byref(self.c)
 
 
 def lora_workspace_bytes(T: int, N: int, K: int, adapters: int, rank_max: int) -> int:
@@ -556,7 +566,9 @@ def lora_linear(x, w, bank: LoraBank, ids, y=None, workspace=None):
     [0, L): no adapter). w [N, K], or None: the adapters' part is added to y in place."""
     ldx = _rows_ld("x", x)
     T, K = x.shape
-    _same("bank", bank.a, x)
+    dev, dtype = x.get_device(), x.dtype
+    _same("bank", bank.a, dtype, dev)
+    N = bank.N
     if bank.K != K:
         raise ValueError(f"x has {K} columns, the adapters take {bank.K}")
     if w is None:
@@ -565,14 +577,13 @@ def lora_linear(x, w, bank: LoraBank, ids, y=None, workspace=None):
         wp, ldw = None, 0
     else:
         wp, ldw = w.data_ptr(), _rows_ld("w", w)
-        _same("w", w, x)
-        if tuple(w.shape) != (bank.N, K):
-            raise ValueError(f"w must be {(bank.N, K)} (got {tuple(w.shape)})")
-    y = _result("y", y, (T, bank.N), x.dtype, x)
-    need = 0 if workspace is not None else lora_workspace_bytes(T, bank.N, K, bank.c.adapters, bank.c.rank_max)
-    ws, ws_bytes, _keep = _scratch(workspace, need, x)
-    _run_on(x, _lib.exmoe_lora_linear, x.data_ptr(), ldx, wp, ldw, ctypes.byref(bank.c), _int32("ids", ids, x, T), T,
-            bank.N, K, _dtype_code(x.dtype), y.data_ptr(), _rows_ld("y", y), ws, ws_bytes)
+        _same("w", w, dtype, dev)
+        if w.shape != (N, K):
+            raise ValueError(f"w must be {(N, K)} (got {tuple(w.shape)})")
+    y = _result("y", y, (T, N), dtype, dev)
+    ws, ws_bytes, _keep = _scratch(workspace, lambda: lora_workspace_bytes(T, N, K, bank.c.adapters, bank.c.rank_max), dev)
+    _run_on(dev, _lib.exmoe_lora_linear, x.data_ptr(), ldx, wp, ldw, bank.ref, _int32("ids", ids, dev, T), T, N, K,
+            _dtype_code(dtype), y.data_ptr(), _rows_ld("y", y), ws, ws_bytes)
     return y
 
 

@@ -190,41 +190,25 @@ __device__ __forceinline__ void store4(void* out, size_t off, bool out_f32, bool
   }
 }
 
-// ---- few rows: no LDS staging. The waves of a workgroup split the summed axis in 32-deep
-// steps (wave w: steps w, w + NW, ...), each lane loads its fragments from memory (16 bytes:
-// row or column l % 16, positions 8 (l / 16) + 0..7), and the waves' sums are added in wave
-// order through LDS. TP rows blocks x TQ column blocks of 16.
+// ---- few rows, operands of any alignment: the waves of a workgroup split the summed axis in
+// 32-deep steps (wave w: steps w, w + NW, ...), each lane loads its fragments element by
+// element (row or column l % 16, positions 8 (l / 16) + 0..7).
 // xrow[i] / wrow[j]: element offset of the lane's row of each block in x / w.
-template <class ET, int TP, int TQ, int NW, bool ALIGNED>
-__device__ __forceinline__ void skinny_product(const uint16_t* __restrict__ x, const size_t (&xrow)[TP],
-                                               const uint16_t* __restrict__ w, const size_t (&wrow)[TQ], int red, int wave,
-                                               int lane, f32x4 (&acc)[TQ][TP]) {
-  constexpr int kU = TP * TQ >= 4 ? 2 : 4;   // steps whose loads are in flight together
-  const int k8 = 8 * (lane >> 4);
-  auto load = [&](const uint16_t* p, size_t off, int k) __attribute__((always_inline)) {
-    if constexpr (ALIGNED) {   // red is a multiple of 8
-      const bool in = k < red;
-      const bf16x8 v = *reinterpret_cast<const bf16x8*>(p + off + (in ? k : 0));
-      return in ? v : bf16x8{0, 0, 0, 0, 0, 0, 0, 0};
-    } else {
-      return __builtin_bit_cast(bf16x8, load8_any(p, off + k, red - k, true));
-    }
-  };
-  for (int k = 32 * wave + k8; k - k8 < red; k += 32 * NW * kU) {
-    bf16x8 fw[kU][TQ], fx[kU][TP];
+template <class ET, int TP, int TQ, int NW>
+__device__ __forceinline__ void skinny_product_any(const uint16_t* __restrict__ x, const size_t (&xrow)[TP],
+                                                   const uint16_t* __restrict__ w, const size_t (&wrow)[TQ], int red,
+                                                   int wave, int lane, f32x4 (&acc)[TQ][TP]) {
+  for (int k0 = 32 * wave; k0 < red; k0 += 32 * NW) {
+    const int k = k0 + 8 * (lane >> 4);
+    bf16x8 fw[TQ], fx[TP];
 #pragma unroll
-    for (int u = 0; u < kU; u++) {
+    for (int j = 0; j < TQ; j++) fw[j] = __builtin_bit_cast(bf16x8, load8_any(w, wrow[j] + k, red - k, true));
 #pragma unroll
-      for (int j = 0; j < TQ; j++) fw[u][j] = load(w, wrow[j], k + 32 * NW * u);
+    for (int i = 0; i < TP; i++) fx[i] = __builtin_bit_cast(bf16x8, load8_any(x, xrow[i] + k, red - k, true));
 #pragma unroll
-      for (int i = 0; i < TP; i++) fx[u][i] = load(x, xrow[i], k + 32 * NW * u);
-    }
+    for (int j = 0; j < TQ; j++)
 #pragma unroll
-    for (int u = 0; u < kU; u++)
-#pragma unroll
-      for (int j = 0; j < TQ; j++)
-#pragma unroll
-        for (int i = 0; i < TP; i++) acc[j][i] = ET::mfma(fw[u][j], fx[u][i], acc[j][i]);
+      for (int i = 0; i < TP; i++) acc[j][i] = ET::mfma(fw[j], fx[i], acc[j][i]);
   }
 }
 

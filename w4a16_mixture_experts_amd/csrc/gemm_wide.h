@@ -145,6 +145,90 @@ struct WideCols {
   }
 };
 
+// ---- few rows: each wave copies its own slices of both operands into its own part of LDS
+// (no barrier), two D-deep slices in flight, and the waves split the summed axis slice by
+// slice. Straight loads in fragment order touch a different row in each of four neighbouring
+// lanes, which costs a vector memory unit four times the cycles of a copy of whole 128- or
+// 256-byte row pieces (64 tokens beside W 2048 x 2048 and their adapters: 16.5 -> 9.7 us).
+template <int B, int D>
+struct NarrowRows {
+  static constexpr int kChunks = D / 8, kRows = 64 / kChunks, kSlots = B / kRows, kElems = B * D;
+  static_assert((D == 64 || D == 128) && B % 16 == 0, "rows of a slice");
+  buf_t buf;
+  int red, c0;               // c0: the lane's chunk in its first row
+  uint32_t voff[kSlots];
+
+  static __device__ __forceinline__ int swz(int row) { return D == 128 ? row & 15 : (row >> 1) & 7; }
+  // row_off(i): byte offset of row i, or kNowhere for zeros
+  template <class F>
+  __device__ __forceinline__ void init(buf_t b, int red_, int lane, F row_off) {
+    buf = b;
+    red = red_;
+    c0 = (lane % kChunks) ^ swz(lane / kChunks);
+#pragma unroll
+    for (int i = 0; i < kSlots; i++) {
+      const uint32_t o = row_off(i * kRows + lane / kChunks);
+      voff[i] = o == kNowhere ? o : o + 16 * chunk(i);
+    }
+  }
+  __device__ __forceinline__ int chunk(int i) const { return c0 ^ swz(i * kRows); }   // (row bits of i and of the lane are apart)
+  // positions past the summed axis are zeros (a slice wholly past it moves nothing)
+  __device__ __forceinline__ void stage(uint16_t* lds, int k0) const {
+    const uint32_t soff = k0 < red ? 2 * (uint32_t)k0 : 0;
+#pragma unroll
+    for (int i = 0; i < kSlots; i++)
+      buf_copy16(buf, lds + i * kRows * D, k0 + 8 * chunk(i) < red ? voff[i] : kNowhere, soff);
+  }
+  // rows r0..r0 + 15, positions 32 kk + 8 (lane / 16) + 0..7 of the slice
+  static __device__ __forceinline__ bf16x8 frag(const uint16_t* lds, int r0, int kk, int lane) {
+    const int row = r0 + (lane & 15);
+    return *reinterpret_cast<const bf16x8*>(lds + row * D + 8 * ((4 * kk + (lane >> 4)) ^ swz(row)));
+  }
+};
+
+// acc[j][i] += rows 16 j.. of w (columns of the output) times rows 16 i.. of x, over this
+// wave's slices; s_a, s_b: this wave's two parts of LDS, (TP + TQ) 16 D elements each.
+template <class ET, int TP, int TQ, int NW, int D>
+__device__ __forceinline__ void narrow_product(const NarrowRows<16 * TP, D>& x, const NarrowRows<16 * TQ, D>& w, int red,
+                                               int wave, int lane, uint16_t* s_a, uint16_t* s_b, f32x4 (&acc)[TQ][TP]) {
+  constexpr int kCopies = NarrowRows<16 * TP, D>::kSlots + NarrowRows<16 * TQ, D>::kSlots;
+  auto issue = [&](int s, uint16_t* lds) __attribute__((always_inline)) {
+    const int k0 = (s * NW + wave) * D;
+    w.stage(lds, k0);
+    x.stage(lds + 16 * TQ * D, k0);
+  };
+  auto compute = [&](const uint16_t* lds) __attribute__((always_inline)) {
+#pragma unroll
+    for (int kk = 0; kk < D / 32; kk++) {
+      bf16x8 fw[TQ], fx[TP];
+#pragma unroll
+      for (int j = 0; j < TQ; j++) fw[j] = NarrowRows<16 * TQ, D>::frag(lds, 16 * j, kk, lane);
+#pragma unroll
+      for (int i = 0; i < TP; i++) fx[i] = NarrowRows<16 * TP, D>::frag(lds + 16 * TQ * D, 16 * i, kk, lane);
+#pragma unroll
+      for (int j = 0; j < TQ; j++)
+#pragma unroll
+        for (int i = 0; i < TP; i++) acc[j][i] = ET::mfma(fw[j], fx[i], acc[j][i]);
+    }
+    wait_lds();   // read, before the next copies into this part
+    asm volatile("" ::: "memory");
+  };
+  const int n = (red + D * NW - 1) / (D * NW);
+  issue(0, s_a);
+  issue(1, s_b);
+  for (int s = 0; s < n; s += 2) {
+    wait_vm<kCopies>();
+    asm volatile("" ::: "memory");
+    compute(s_a);
+    issue(s + 2, s_a);
+    wait_vm<kCopies>();
+    asm volatile("" ::: "memory");
+    compute(s_b);
+    issue(s + 3, s_b);
+  }
+  wait_vm<0>();   // no copy is left behind
+}
+
 // Where a tile's outputs go: element base + row ld + q of ptr.
 struct TileOut {
   void* ptr;

@@ -14,6 +14,8 @@
 // of two into [-2, 2] and split into hi + lo, two 16-bit values whose sum is v to 2^-16 (bf16)
 // or 2^-22 (fp16) of it; both halves multiply the same B_a in one MFMA (16 summed positions
 // hi, 16 lo). The power of two and the adapter's scale are applied in fp32 to the result.
+#include <algorithm>
+
 #include "exmoe.h"
 #include "gemm_wide.h"
 
@@ -35,8 +37,10 @@ struct LoraArgs {
   uint16_t* y;
   int vec8, vec16;            // rows of y can be stored 8 / 16 bytes at a time
   int rank_blocks;            // ceil(rank_max / 16)
-  uint16_t* hl;               // [T][rank_blocks][2][16]: hi and lo of the scaled v
-  float* mul;                 // [T][rank_blocks]: scale_a times the power of two taken out of v
+  // by groups of 16 tokens and blocks of 16 ranks (group g, block b: index g rank_blocks + b):
+  uint16_t* hl;               // [index][2][2][16][8]: hi, lo; ranks 0..7, 8..15; token; rank (fragment order)
+  float* mul;                 // [index][16]: scale_a times the power of two taken out of a token's v
+  int2* info;                 // [T]: the token's adapter (-1: none) and its rank
 };
 
 __device__ __forceinline__ int token_adapter(const LoraArgs& a, int t) {
@@ -60,51 +64,69 @@ __device__ __forceinline__ int nth_adapter(int id, int j) {
   return -1;
 }
 
-// Workgroup (16 tokens, the j-th adapter among them, 16 ranks of it): the waves split K and
-// their sums are added in wave order.
-template <class ET, int NW>
+// A token's v of 16 ranks, scaled by a power of two and split: m is the largest |v| of the 16.
+struct SplitV {
+  float down, up;   // 1 / 2^e and 2^e with the largest |v| / 2^e in [1, 2); 1 where nothing finite and normal is there
+  __device__ __forceinline__ explicit SplitV(float m) {
+    const uint32_t eb = __float_as_uint(m) >> 23;
+    const bool scale = eb >= 1 && eb <= 253;
+    down = scale ? __uint_as_float((254 - eb) << 23) : 1.f;
+    up = scale ? __uint_as_float(eb << 23) : 1.f;
+  }
+  template <class ET>
+  __device__ __forceinline__ void split(float v, uint16_t& hi, uint16_t& lo) const {
+    const float n = v * down;
+    hi = ET::from_f32(n);
+    const float rest = n - ET::to_f32(hi);
+    lo = __builtin_isfinite(rest) ? ET::from_f32(rest) : (uint16_t)0;
+  }
+};
+
+// Workgroup (16 tokens, the y-th adapter among them and every gridDim.y-th after it, 16
+// ranks): the waves split K and their sums are added in wave order.
+template <class ET, int NW, int D>
 __global__ __launch_bounds__(64 * NW) void lora_shrink_kernel(LoraArgs a) {
   static_assert(NW >= 4, "256 threads hold the 16 x 16 sums");
+  __shared__ __attribute__((aligned(16))) uint16_t s_a[NW][32 * D], s_b[NW][32 * D];
   __shared__ float s_part[NW][16][17];   // [wave][token][rank]
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int t0 = blockIdx.x * 16, r0 = 16 * blockIdx.z;
-  const int ad = nth_adapter(token_adapter(a, t0 + (lane & 15)), blockIdx.y);
-  if (ad < 0) return;   // fewer adapters than workgroups
-  const int rank = adapter_rank(a, ad);
-  if (r0 >= rank) return;
-  const int t = t0 + (lane & 15), r = r0 + (lane & 15);
-  const size_t xrow[1] = {(size_t)(t < a.T ? t : a.T - 1) * a.ldx};
-  const size_t arow[1] = {(size_t)ad * a.a_stride + (size_t)(r < rank ? r : rank - 1) * a.lda};
-  f32x4 acc[1][1] = {{{0.f, 0.f, 0.f, 0.f}}};
-  skinny_product<ET, 1, 1, NW, true>(a.x, xrow, a.a, arow, a.K, wave, lane, acc);
+  const int t0 = blockIdx.x * 16, r0 = 16 * blockIdx.z, t = t0 + (lane & 15);
+  const int id = token_adapter(a, t), mine = t0 + ((tid >> 4) & 15), mine_id = token_adapter(a, mine);
+  if (blockIdx.y == 0 && blockIdx.z == 0 && tid < 16 && t < a.T) a.info[t] = make_int2(id, id >= 0 ? adapter_rank(a, id) : 0);
+  NarrowRows<16, D> op_x, op_a;
+  op_x.init(make_buf(a.x + (size_t)t0 * a.ldx, 2 * ((size_t)(min(16, a.T - t0) - 1) * a.ldx + a.K)), a.K, lane,
+            [&](int i) { return t0 + i < a.T ? (uint32_t)(i * a.ldx * 2) : kNowhere; });
+  for (int j = blockIdx.y;; j += gridDim.y) {
+    const int ad = nth_adapter(id, j);
+    if (ad < 0) return;   // fewer adapters than workgroups
+    const int rank = adapter_rank(a, ad);
+    if (r0 >= rank) continue;
+    op_a.init(make_buf(a.a + (size_t)ad * a.a_stride + (size_t)r0 * a.lda, 2 * ((size_t)(min(16, rank - r0) - 1) * a.lda + a.K)),
+              a.K, lane, [&](int i) { return r0 + i < rank ? (uint32_t)(i * a.lda * 2) : kNowhere; });
+    f32x4 acc[1][1] = {{{0.f, 0.f, 0.f, 0.f}}};
+    narrow_product<ET, 1, 1, NW, D>(op_x, op_a, a.K, wave, lane, s_a[wave], s_b[wave], acc);
+    __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 4; i++) s_part[wave][lane & 15][4 * (lane >> 4) + i] = acc[0][0][i];
-  __syncthreads();
-  // thread: token tid / 16, rank tid % 16 (rows of 16 lanes hold a token)
-  const int mine = t0 + (tid >> 4);
-  if (tid >= 256 || mine >= a.T || token_adapter(a, mine) != ad) return;
-  float v = 0.f;
-  if (r0 + (tid & 15) < rank) {
+    for (int i = 0; i < 4; i++) s_part[wave][lane & 15][4 * (lane >> 4) + i] = acc[0][0][i];
+    __syncthreads();
+    // thread: token tid / 16, rank tid % 16 (rows of 16 lanes hold a token)
+    if (tid >= 256 || mine_id != ad) continue;
+    float v = 0.f;
+    if (r0 + (tid & 15) < rank) {
 #pragma unroll
-    for (int w = 0; w < NW; w++) v += s_part[w][tid >> 4][tid & 15];
+      for (int w = 0; w < NW; w++) v += s_part[w][tid >> 4][tid & 15];
+    }
+    float m = fabsf(v);   // (fmaxf drops a NaN)
+    m = fmaxf(m, __uint_as_float(dpp_u32<0x121>(__float_as_uint(m))));
+    m = fmaxf(m, __uint_as_float(dpp_u32<0x122>(__float_as_uint(m))));
+    m = fmaxf(m, __uint_as_float(dpp_u32<0x124>(__float_as_uint(m))));
+    m = fmaxf(m, __uint_as_float(dpp_u32<0x128>(__float_as_uint(m))));
+    const SplitV sv(m);
+    const size_t block = (size_t)blockIdx.x * a.rank_blocks + blockIdx.z;
+    uint16_t* out = a.hl + 512 * block + 128 * ((tid >> 3) & 1) + 8 * (tid >> 4) + (tid & 7);
+    sv.split<ET>(v, out[0], out[256]);
+    if ((tid & 15) == 0) a.mul[16 * block + (tid >> 4)] = sv.up * (a.scales ? a.scales[ad] : 1.f);
   }
-  float m = fabsf(v);   // (fmaxf drops a NaN)
-  m = fmaxf(m, __uint_as_float(dpp_u32<0x121>(__float_as_uint(m))));
-  m = fmaxf(m, __uint_as_float(dpp_u32<0x122>(__float_as_uint(m))));
-  m = fmaxf(m, __uint_as_float(dpp_u32<0x124>(__float_as_uint(m))));
-  m = fmaxf(m, __uint_as_float(dpp_u32<0x128>(__float_as_uint(m))));
-  // 2^e with the largest |v| / 2^e in [1, 2); 1 where nothing finite and normal is there
-  const uint32_t eb = __float_as_uint(m) >> 23;
-  const bool scale = eb >= 1 && eb <= 253;
-  const float down = scale ? __uint_as_float((254 - eb) << 23) : 1.f, up = scale ? __uint_as_float(eb << 23) : 1.f;
-  const float n = v * down;
-  const uint16_t hi = ET::from_f32(n);
-  const float rest = n - ET::to_f32(hi);
-  const size_t block = (size_t)mine * a.rank_blocks + blockIdx.z;
-  uint16_t* out = a.hl + 32 * block + (tid & 15);
-  out[0] = hi;
-  out[16] = __builtin_isfinite(rest) ? ET::from_f32(rest) : 0;
-  if ((tid & 15) == 0) a.mul[block] = up * (a.scales ? a.scales[ad] : 1.f);
 }
 
 // Eight elements of b: ranks c..c + 7 of column n, zeros from the adapter's rank on (what
@@ -121,104 +143,120 @@ __device__ __forceinline__ bf16x8 load_b(const LoraArgs& a, int ad, int rank, in
   return v;
 }
 
-// Adds the adapters' parts to the sums of one block of 16 tokens and 16 columns (acc[j]:
-// columns n0 + 16 j..): per adapter and 16 ranks one MFMA (hi and lo), kept for the lanes of
-// the adapter's own tokens. This wave takes the adapters w, w + NW, ... among the tokens.
-template <class ET, int TQ, int TP, int NW>
-__device__ __forceinline__ void lora_expand16(const LoraArgs& a, int t, int n0, int wave, int lane, f32x4 (&acc)[TQ][TP],
-                                              int i) {
-  const int id = token_adapter(a, t);
-  const size_t tok = (size_t)(t < a.T ? t : a.T - 1) * a.rank_blocks;
-  uint32_t left = (uint32_t)__ballot(id >= 0) & 0xFFFFu;
-  for (int which = 0; left; which++) {
-    const int ad = __builtin_amdgcn_readlane(id, __ffs((int)left) - 1);
-    left &= ~(uint32_t)__ballot(id == ad);
-    if (which % NW != wave) continue;
-    const int rank = adapter_rank(a, ad);
-    for (int rb = 0; 16 * rb < rank; rb++) {
-      bf16x8 vv = {0, 0, 0, 0, 0, 0, 0, 0};
-      float mul = 0.f;
-      if (id == ad) {
-        vv = *reinterpret_cast<const bf16x8*>(a.hl + 32 * (tok + rb) + 8 * (lane >> 4));
-        mul = a.mul[tok + rb];
+// The adapters' parts of one block of 16 tokens and 16 columns from n0 that this wave adds:
+// those of the adapters wave + m NW (m < kSlots) among the tokens, in token order. The first
+// 64 ranks of their B are loaded when they are found, ahead of the pass over K; add() runs
+// one MFMA (hi and lo) per adapter and 16 ranks, kept for the lanes of the adapter's own tokens.
+template <class ET, int NW>
+struct ExpandBlock {
+  static constexpr int kSlots = 16 / NW;
+  int id;
+  size_t group;              // first block index of the 16 tokens
+  int ad[kSlots], rank[kSlots];
+  bf16x8 bv[kSlots][4];
+
+  __device__ __forceinline__ void find(const LoraArgs& a, int t0, int2 info, int n0, int wave, int lane) {
+    id = info.x;
+    group = (size_t)min(t0 / 16, (a.T - 1) / 16) * a.rank_blocks;
+    uint32_t left = (uint32_t)__ballot(info.y > 0) & 0xFFFFu;
+    int which = 0;
+#pragma unroll
+    for (int m = 0; m < kSlots; m++) {
+      ad[m] = 0;
+      rank[m] = 0;
+      for (bool found = false; left && !found; which++) {
+        const int lead = __ffs((int)left) - 1, cand = __builtin_amdgcn_readlane(id, lead);
+        left &= ~(uint32_t)__ballot(id == cand);
+        found = which == wave + m * NW;
+        if (found) {
+          ad[m] = cand;
+          rank[m] = __builtin_amdgcn_readlane(info.y, lead);
+        }
       }
 #pragma unroll
-      for (int j = 0; j < TQ; j++) {
-        const f32x4 d = ET::mfma(load_b(a, ad, rank, n0 + 16 * j + (lane & 15), 16 * rb + 8 * ((lane >> 4) & 1)), vv,
-                                 f32x4{0.f, 0.f, 0.f, 0.f});
-        if (id == ad) {
+      for (int u = 0; u < 4; u++)
+        bv[m][u] = load_b(a, ad[m], rank[m], n0 + (lane & 15), 16 * u + 8 * ((lane >> 4) & 1));
+    }
+  }
+  __device__ __forceinline__ void add(const LoraArgs& a, int n0, int lane, f32x4& acc) {
 #pragma unroll
-          for (int q = 0; q < 4; q++) acc[j][i][q] += mul * d[q];
+    for (int m = 0; m < kSlots; m++) {
+      for (int r0 = 0; r0 < rank[m]; r0 += 64) {
+        bf16x8 vv[4];
+        float mul[4];
+#pragma unroll
+        for (int u = 0; u < 4; u++) {
+          const size_t blk = group + (r0 + 16 * u < rank[m] ? r0 / 16 + u : 0);
+          vv[u] = *reinterpret_cast<const bf16x8*>(a.hl + 512 * blk + 8 * lane);   // (tokens of other adapters: dropped)
+          mul[u] = a.mul[16 * blk + (lane & 15)];
+          if (r0) bv[m][u] = load_b(a, ad[m], rank[m], n0 + (lane & 15), r0 + 16 * u + 8 * ((lane >> 4) & 1));
+        }
+#pragma unroll
+        for (int u = 0; u < 4; u++) {
+          const f32x4 d = ET::mfma(bv[m][u], vv[u], f32x4{0.f, 0.f, 0.f, 0.f});
+          if (id == ad[m] && r0 + 16 * u < rank[m]) {
+#pragma unroll
+            for (int q = 0; q < 4; q++) acc[q] += mul[u] * d[q];
+          }
         }
       }
     }
   }
-}
+};
 
 // The same for a block of 32 tokens and TQ blocks of 32 columns on 32 x 32 x 16 MFMA: two per
 // adapter and 16 ranks (8 ranks each: hi in lanes 0..31, lo in lanes 32..63).
 template <class ET, int TQ, int TP>
 __device__ __forceinline__ void lora_expand32(const LoraArgs& a, int t, int n0, int lane, f32x16 (&acc)[TQ][TP], int i) {
-  const int id = token_adapter(a, t);
-  const size_t tok = (size_t)(t < a.T ? t : a.T - 1) * a.rank_blocks;
+  const int2 info = t < a.T ? a.info[t] : make_int2(-1, 0);
+  const int id = info.x;
+  const size_t group = (size_t)((t < a.T ? t : a.T - 1) / 16) * a.rank_blocks;
   uint32_t left = (uint32_t)__ballot(id >= 0);
   while (left) {
-    const int ad = __builtin_amdgcn_readlane(id, __ffs((int)left) - 1);
+    const int lead = __ffs((int)left) - 1;
+    const int ad = __builtin_amdgcn_readlane(id, lead), rank = __builtin_amdgcn_readlane(info.y, lead);
     left &= ~(uint32_t)__ballot(id == ad);
-    const int rank = adapter_rank(a, ad);
-    for (int rb = 0; 16 * rb < rank; rb++) {
-      bf16x8 v0 = {0, 0, 0, 0, 0, 0, 0, 0}, v1 = v0;
-      float mul = 0.f;
-      if (id == ad) {
-        const uint16_t* p = a.hl + 32 * (tok + rb) + 16 * (lane >> 5);
-        v0 = *reinterpret_cast<const bf16x8*>(p);
-        v1 = *reinterpret_cast<const bf16x8*>(p + 8);
-        mul = a.mul[tok + rb];
+    // two blocks of 16 ranks a turn, their loads together
+    for (int rb = 0; 16 * rb < rank; rb += 2) {
+      bf16x8 v[2][2], bv[2][TQ][2];
+      float mul[2];
+#pragma unroll
+      for (int u = 0; u < 2; u++) {
+        const bool in = 16 * (rb + u) < rank;
+        const size_t blk = group + (in ? rb + u : 0);
+        const uint16_t* p = a.hl + 512 * blk + 256 * (lane >> 5) + 8 * (lane & 15);
+        v[u][0] = *reinterpret_cast<const bf16x8*>(p);   // (tokens of other adapters: dropped)
+        v[u][1] = *reinterpret_cast<const bf16x8*>(p + 128);
+        mul[u] = a.mul[16 * blk + (lane & 15)];
+#pragma unroll
+        for (int j = 0; j < TQ; j++)
+#pragma unroll
+          for (int h = 0; h < 2; h++) bv[u][j][h] = load_b(a, ad, rank, n0 + 32 * j + (lane & 31), 16 * (rb + u) + 8 * h);
       }
 #pragma unroll
-      for (int j = 0; j < TQ; j++) {
-        const int n = n0 + 32 * j + (lane & 31);
-        f32x16 d;
+      for (int u = 0; u < 2; u++) {
+        if (16 * (rb + u) >= rank) break;
 #pragma unroll
-        for (int q = 0; q < 16; q++) d[q] = 0.f;
-        d = mfma32(ET{}, load_b(a, ad, rank, n, 16 * rb), v0, d);
-        d = mfma32(ET{}, load_b(a, ad, rank, n, 16 * rb + 8), v1, d);
-        if (id == ad) {
+        for (int j = 0; j < TQ; j++) {
+          f32x16 d;
 #pragma unroll
-          for (int q = 0; q < 16; q++) acc[j][i][q] += mul * d[q];
+          for (int q = 0; q < 16; q++) d[q] = 0.f;
+          d = mfma32(ET{}, bv[u][j][0], v[u][0], d);
+          d = mfma32(ET{}, bv[u][j][1], v[u][1], d);
+          if (id == ad) {
+#pragma unroll
+            for (int q = 0; q < 16; q++) acc[j][i][q] += mul[u] * d[q];
+          }
         }
       }
     }
   }
 }
 
-// Few tokens: 16 TP tokens x 16 TQ columns per workgroup, W streamed once per 16 TP tokens;
-// the waves split K, and the adapters among the tokens, before their sums are added.
-template <class ET, int TP, int TQ, int NW>
-__global__ __launch_bounds__(64 * NW) void lora_skinny_kernel(LoraArgs a) {
-  __shared__ f32x4 s_part[NW][TQ * TP][64];
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int n0 = blockIdx.x * 16 * TQ, t0 = blockIdx.y * 16 * TP;
-  f32x4 acc[TQ][TP];
-  size_t xrow[TP], wrow[TQ];
-#pragma unroll
-  for (int j = 0; j < TQ; j++) {
-    const int n = n0 + 16 * j + (lane & 15);
-    wrow[j] = (size_t)(n < a.N ? n : a.N - 1) * a.ldw;
-#pragma unroll
-    for (int i = 0; i < TP; i++) acc[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  }
-#pragma unroll
-  for (int i = 0; i < TP; i++) {
-    const int t = t0 + 16 * i + (lane & 15);
-    xrow[i] = (size_t)(t < a.T ? t : a.T - 1) * a.ldx;
-  }
-  if (a.w) skinny_product<ET, TP, TQ, NW, true>(a.x, xrow, a.w, wrow, a.K, wave, lane, acc);
-#pragma unroll
-  for (int i = 0; i < TP; i++) lora_expand16<ET, TQ, TP, NW>(a, t0 + 16 * i + (lane & 15), n0, wave, lane, acc, i);
-  f32x4 v = skinny_reduce<TP, TQ, NW>(s_part, acc, wave, lane);
-  const int t = t0 + 16 * (wave % TP) + (lane & 15), n = n0 + 16 * (wave / TP) + 4 * (lane >> 4);
-  if (wave >= TQ * TP || t >= a.T || n >= a.N) return;
+// Columns n..n + 3 of token t: the sums, rounded, or added to y when there is no W.
+template <class ET>
+__device__ __forceinline__ void lora_store(const LoraArgs& a, int t, int n, f32x4 v) {
+  if (t >= a.T || n >= a.N) return;
   if (!a.w) {
     if (token_adapter(a, t) < 0) return;   // keeps its y as it is
 #pragma unroll
@@ -226,6 +264,200 @@ __global__ __launch_bounds__(64 * NW) void lora_skinny_kernel(LoraArgs a) {
       if (n + q < a.N) v[q] += ET::to_f32(a.y[(size_t)t * a.ldy + n + q]);
   }
   store4<ET>(a.y, (size_t)t * a.ldy + n, false, a.vec8, a.N - n, v);
+}
+
+// Few tokens: 16 TP tokens x 16 columns per workgroup, W streamed once per 16 TP tokens; the
+// waves split K, and the adapters among the tokens, before their sums are added.
+template <class ET, int TP, int NW, int D>
+__global__ __launch_bounds__(64 * NW) void lora_skinny_kernel(LoraArgs a) {
+  constexpr int kPart = 16 * (TP + 1) * D;
+  __shared__ __attribute__((aligned(16))) uint16_t s_a[NW][kPart], s_b[NW][kPart];
+  static_assert(sizeof(f32x4) * TP * 64 <= sizeof(s_a[0]), "the sums fit into the slices' part");
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int n0 = blockIdx.x * 16, t0 = blockIdx.y * 16 * TP;
+  f32x4 acc[1][TP];
+  int2 info[TP];
+  ExpandBlock<ET, NW> part[TP];
+#pragma unroll
+  for (int i = 0; i < TP; i++) {
+    const int t = t0 + 16 * i + (lane & 15);
+    info[i] = t < a.T ? a.info[t] : make_int2(-1, 0);
+    acc[0][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+#pragma unroll
+  for (int i = 0; i < TP; i++) part[i].find(a, t0 + 16 * i, info[i], n0, wave, lane);
+  if (a.w) {
+    NarrowRows<16 * TP, D> op_x;
+    NarrowRows<16, D> op_w;
+    op_x.init(make_buf(a.x + (size_t)t0 * a.ldx, 2 * ((size_t)(min(16 * TP, a.T - t0) - 1) * a.ldx + a.K)), a.K, lane,
+              [&](int i) { return t0 + i < a.T ? (uint32_t)(i * a.ldx * 2) : kNowhere; });
+    op_w.init(make_buf(a.w + (size_t)n0 * a.ldw, 2 * ((size_t)(min(16, a.N - n0) - 1) * a.ldw + a.K)), a.K, lane,
+              [&](int i) { return n0 + i < a.N ? (uint32_t)(i * a.ldw * 2) : kNowhere; });
+    narrow_product<ET, TP, 1, NW, D>(op_x, op_w, a.K, wave, lane, s_a[wave], s_b[wave], acc);
+  }
+#pragma unroll
+  for (int i = 0; i < TP; i++) part[i].add(a, n0, lane, acc[0][i]);
+  __syncthreads();
+  const f32x4 v = skinny_reduce<TP, 1, NW>(reinterpret_cast<f32x4(*)[TP][64]>(&s_a[0][0]), acc, wave, lane);
+  if (wave < TP) lora_store<ET>(a, t0 + 16 * wave + (lane & 15), n0 + 4 * (lane >> 4), v);
+}
+
+// One to sixteen tokens with few 16-rank blocks among their adapters (at most NB): both
+// products in one launch. Every workgroup makes v for itself, from A blocks that ride along
+// the pass over K as further column blocks of the product (A_a is read by every workgroup,
+// from the caches); the adapter's B blocks are loaded behind it.
+template <class ET, int NB, int NW>
+__global__ __launch_bounds__(64 * NW) void lora_token_kernel(LoraArgs a) {
+  constexpr int D = 64, kPart = 16 * (2 + NB) * D, kCopies = 2 * (2 + NB);
+  __shared__ __attribute__((aligned(16))) uint16_t s_a[NW][kPart], s_b[NW][kPart];
+  static_assert(sizeof(f32x4) * (1 + NB) * 64 <= sizeof(s_a[0]), "the sums fit into the slices' part");
+  __shared__ __attribute__((aligned(16))) uint16_t s_hl[NB][512];
+  __shared__ float s_mul[NB][16];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int n0 = blockIdx.x * 16, t = lane & 15, n = n0 + (lane & 15);
+  // the first slices of x and W are on their way while the adapters are found; ranks come by
+  // scalar loads (constant address space), which do not wait for them
+  const int id = token_adapter(a, t);
+  NarrowRows<16, D> op_x, op_w, op_a[NB];
+  op_x.init(make_buf(a.x, 2 * ((size_t)(a.T - 1) * a.ldx + a.K)), a.K, lane,
+            [&](int i) { return i < a.T ? (uint32_t)(i * a.ldx * 2) : kNowhere; });
+  // (without W every copy of it moves nothing: its rows are zeros)
+  op_w.init(make_buf(a.w ? a.w + (size_t)n0 * a.ldw : a.x, a.w ? 2 * ((size_t)(min(16, a.N - n0) - 1) * a.ldw + a.K) : 0),
+            a.w ? a.K : 0, lane, [&](int i) { return a.w && n0 + i < a.N ? (uint32_t)(i * a.ldw * 2) : kNowhere; });
+  uint16_t *const la = s_a[wave], *const lb = s_b[wave];
+  auto issue_xw = [&](int s, uint16_t* lds) __attribute__((always_inline)) {
+    const int k0 = (s * NW + wave) * D;
+    op_x.stage(lds, k0);
+    op_w.stage(lds + 16 * D, k0);
+  };
+  issue_xw(0, la);
+  issue_xw(1, lb);
+  const auto* ranks = (const __attribute__((address_space(4))) int32_t*)a.ranks;
+  // block b: 16 ranks from bfirst[b] on of adapter bad[b], of rank brank[b] (0: no block)
+  int bad[NB], bfirst[NB], brank[NB];
+  {
+    uint32_t left = (uint32_t)__ballot(id >= 0) & 0xFFFFu;
+    int ad = 0, rank = 0, next = 0;
+#pragma unroll
+    for (int b = 0; b < NB; b++) {
+      if (next >= rank) {
+        rank = 0;
+        while (left && rank <= 0) {   // (an adapter of rank 0 has no block)
+          ad = __builtin_amdgcn_readlane(id, __ffs((int)left) - 1);
+          rank = a.ranks ? min(ranks[ad], a.rank_max) : a.rank_max;
+          left &= ~(uint32_t)__ballot(id == ad);
+        }
+        rank = max(rank, 0);
+        next = 0;
+      }
+      bad[b] = ad;
+      bfirst[b] = next;
+      brank[b] = rank;
+      next += 16;
+    }
+  }
+#pragma unroll
+  for (int b = 0; b < NB; b++) {
+    const int rows = min(16, brank[b] - bfirst[b]);
+    op_a[b].init(make_buf(a.a + (size_t)bad[b] * a.a_stride + (size_t)bfirst[b] * a.lda,
+                          rows > 0 ? 2 * ((size_t)(rows - 1) * a.lda + a.K) : 0),
+                 rows > 0 ? a.K : 0, lane, [&](int i) { return i < rows ? (uint32_t)(i * a.lda * 2) : kNowhere; });
+  }
+  auto issue_a = [&](int s, uint16_t* lds) __attribute__((always_inline)) {
+#pragma unroll
+    for (int b = 0; b < NB; b++) op_a[b].stage(lds + 16 * (2 + b) * D, (s * NW + wave) * D);
+  };
+  f32x4 acc[1 + NB];
+#pragma unroll
+  for (int b = 0; b <= NB; b++) acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto compute = [&](const uint16_t* lds) __attribute__((always_inline)) {
+#pragma unroll
+    for (int kk = 0; kk < D / 32; kk++) {
+      const bf16x8 fx = NarrowRows<16, D>::frag(lds, 0, kk, lane);
+#pragma unroll
+      for (int b = 0; b <= NB; b++)
+        acc[b] = ET::mfma(NarrowRows<16, D>::frag(lds + 16 * (1 + b) * D, 0, kk, lane), fx, acc[b]);
+    }
+    wait_lds();   // read, before the next copies into this part
+    asm volatile("" ::: "memory");
+  };
+  const int steps = (a.K + D * NW - 1) / (D * NW);
+  issue_a(0, la);
+  issue_a(1, lb);
+  wait_vm<2 * NB>();   // in order of issue: x and W of both slices, A of the first
+  asm volatile("" ::: "memory");
+  for (int s = 0; s < steps; s += 2) {
+    if (s) {
+      wait_vm<kCopies>();
+      asm volatile("" ::: "memory");
+    }
+    compute(la);
+    issue_xw(s + 2, la);
+    issue_a(s + 2, la);
+    wait_vm<kCopies>();
+    asm volatile("" ::: "memory");
+    compute(lb);
+    issue_xw(s + 3, lb);
+    issue_a(s + 3, lb);
+  }
+  wait_vm<0>();   // no copy is left behind
+  bf16x8 bv[NB];
+  float scale[NB];
+  if (wave == 0) {   // (the loads run while the sums are joined)
+#pragma unroll
+    for (int b = 0; b < NB; b++) {
+      bv[b] = load_b(a, bad[b], brank[b], n, bfirst[b] + 8 * ((lane >> 4) & 1));
+      scale[b] = brank[b] && a.scales ? a.scales[bad[b]] : 1.f;
+    }
+  }
+  __syncthreads();
+  f32x4(*s_part)[1 + NB][64] = reinterpret_cast<f32x4(*)[1 + NB][64]>(&s_a[0][0]);
+#pragma unroll
+  for (int b = 0; b <= NB; b++) s_part[wave][b][lane] = acc[b];
+  __syncthreads();
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  static_assert(NB + 1 <= NW, "a wave per block of sums");
+  if (wave <= NB) {
+    v = s_part[0][wave][lane];
+#pragma unroll
+    for (int w = 1; w < NW; w++) {
+      const f32x4 q = s_part[w][wave][lane];
+#pragma unroll
+      for (int e = 0; e < 4; e++) v[e] += q[e];
+    }
+  }
+#pragma unroll
+  for (int b = 0; b < NB; b++) {
+    if (wave != b + 1 || !brank[b]) continue;
+    // lane: token l % 16, ranks bfirst + 4 (l / 16) + 0..3
+    float m = 0.f;
+#pragma unroll
+    for (int q = 0; q < 4; q++) {
+      if (bfirst[b] + 4 * (lane >> 4) + q >= brank[b]) v[q] = 0.f;
+      m = fmaxf(m, fabsf(v[q]));
+    }
+    m = fmaxf(m, __shfl_xor(m, 16, 64));
+    m = fmaxf(m, __shfl_xor(m, 32, 64));
+    const SplitV sv(m);
+    // (fragment order: hi or lo, ranks 0..7 or 8..15, token, rank)
+    uint16_t* out = &s_hl[b][128 * (lane >> 5) + 8 * t + 4 * ((lane >> 4) & 1)];
+#pragma unroll
+    for (int q = 0; q < 4; q++) sv.split<ET>(v[q], out[q], out[256 + q]);
+    if (lane < 16) s_mul[b][t] = sv.up;
+  }
+  __syncthreads();
+  if (wave != 0) return;
+#pragma unroll
+  for (int b = 0; b < NB; b++) {
+    if (!brank[b]) continue;
+    const f32x4 d = ET::mfma(bv[b], *reinterpret_cast<const bf16x8*>(&s_hl[b][8 * lane]), f32x4{0.f, 0.f, 0.f, 0.f});
+    if (id == bad[b]) {
+      const float mul = s_mul[b][t] * scale[b];
+#pragma unroll
+      for (int q = 0; q < 4; q++) v[q] += mul * d[q];
+    }
+  }
+  lora_store<ET>(a, t, n0 + 4 * (lane >> 4), v);
 }
 
 // Many tokens: the pipelined tiles of x W^T (gemm_wide.h), the adapters' parts added to a
@@ -252,13 +484,20 @@ __global__ __launch_bounds__(64 * WP * WQ, OCC) void lora_wide_kernel(LoraArgs a
 }
 
 // ------------------------------------------------------------------------------------ host
-static inline size_t lora_hl_bytes(int T, int rank_max) { return (size_t)T * ((rank_max + 15) / 16) * 64; }
+// index blocks of 16 tokens and 16 ranks
+static inline size_t lora_blocks(int T, int rank_max) { return (size_t)((T + 15) / 16) * ((rank_max + 15) / 16); }
 
-template <class ET, int TP, int TQ, int NW>
+template <class ET, int TP, int NW, int D>
 static hipError_t launch_skinny(const LoraArgs& a, hipStream_t s) {
   ProfScope prof("lora_linear", s);
-  EXMOE_LAUNCH(prof, (lora_skinny_kernel<ET, TP, TQ, NW>), dim3((a.N + 16 * TQ - 1) / (16 * TQ), (a.T + 16 * TP - 1) / (16 * TP)),
+  EXMOE_LAUNCH(prof, (lora_skinny_kernel<ET, TP, NW, D>), dim3((a.N + 15) / 16, (a.T + 16 * TP - 1) / (16 * TP)),
                dim3(64 * NW), 0, s, a);
+  return hipGetLastError();
+}
+template <class ET, int NB, int NW>
+static hipError_t launch_token(const LoraArgs& a, hipStream_t s) {
+  ProfScope prof("lora_linear", s);
+  EXMOE_LAUNCH(prof, (lora_token_kernel<ET, NB, NW>), dim3((a.N + 15) / 16), dim3(64 * NW), 0, s, a);
   return hipGetLastError();
 }
 template <class ET, int TP, int TQ, int WP, int WQ, int OCC>
@@ -270,26 +509,32 @@ static hipError_t launch_lora_wide(const LoraArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-#ifndef SKT
-#define SKT 512
-#endif
 template <class ET>
 static hipError_t launch_lora(const LoraArgs& a, hipStream_t s) {
-  const int distinct = a.adapters < 16 ? a.adapters : 16;
+  const int distinct = std::min(a.adapters, std::min(a.T, 16));   // adapters among 16 tokens, at most
+  // one launch where every workgroup can make v itself (1 token, rank 16, 2048 x 2048: 7.5 us
+  // against 9.9 us for two launches)
+  if (a.T <= 16 && distinct * a.rank_blocks <= 4) {
+    if (distinct * a.rank_blocks == 1) return launch_token<ET, 1, 8>(a, s);
+    return launch_token<ET, 4, 5>(a, s);
+  }
   {
+    // (with many tokens, most of 16 share an adapter: four workgroups walk them instead of 16)
     ProfScope prof("lora_shrink", s);
-    EXMOE_LAUNCH(prof, (lora_shrink_kernel<ET, 8>), dim3((a.T + 15) / 16, distinct, a.rank_blocks), dim3(512), 0, s, a);
+    EXMOE_LAUNCH(prof, (lora_shrink_kernel<ET, 4, 64>), dim3((a.T + 15) / 16, a.T > 256 ? std::min(distinct, 4) : distinct, a.rank_blocks),
+                 dim3(256), 0, s, a);
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const bool span = 2 * ((size_t)(a.T - 1) * a.ldx + a.K) < kMaxSpan && 2 * ((size_t)(a.N - 1) * a.ldw + a.K) < kMaxSpan;
-  if (a.w && span && a.T > SKT) {
+  // Few-token blocks against pipelined tiles, 2048 x 2048, ranks to 64, us: 256 tokens of 256
+  // requests 43 / 103, of 8 requests 33 / 41; 512 tokens of 512 requests 77 / 109, of 8 requests
+  // 52 / 38; 1024 tokens of 512 requests 117 / 86, of 8 requests 94 / 40.
+  if (a.w && span && a.T > 512) {
     if ((long long)((a.T + 255) / 256) * ((a.N + 255) / 256) >= 256) return launch_lora_wide<ET, 4, 2, 2, 4, 2>(a, s);
     return launch_lora_wide<ET, 2, 2, 2, 2, 2>(a, s);
   }
-  if (a.T <= 16) return launch_skinny<ET, 1, 1, 8>(a, s);
-  if (a.T <= 32) return launch_skinny<ET, 2, 1, 8>(a, s);
-  return launch_skinny<ET, 4, 1, 8>(a, s);
+  return launch_skinny<ET, 1, 8, 64>(a, s);
 }
 
 static int lora_shape(int T, int N, int K, int adapters, int rank_max) {
@@ -299,7 +544,7 @@ static int lora_shape(int T, int N, int K, int adapters, int rank_max) {
   if (adapters < 1) return set_error(EXMOE_ERR_INVALID_ARGUMENT, "adapters must be positive (got %d)", adapters);
   if (rank_max < 8 || rank_max % 8 || rank_max > kMaxRank)
     return set_error(EXMOE_ERR_INVALID_ARGUMENT, "rank_max must be a multiple of 8 in [8, 128] (got %d)", rank_max);
-  if ((long long)((T + 63) / 64) * ((N + 15) / 16) * 512 > 0xFFFFFFFFll)
+  if ((long long)((T + 15) / 16) * ((N + 15) / 16) * 512 > 0xFFFFFFFFll)
     return set_error(EXMOE_ERR_UNSUPPORTED, "T x N has too many output tiles for one launch");
   return EXMOE_OK;
 }
@@ -309,6 +554,7 @@ static int check_rows16(const char* name, const void* p, size_t ld, size_t strid
   if (!aligned16(p) || ld % 8 || stride % 8)
     return set_error(EXMOE_ERR_INVALID_ARGUMENT, "%s: rows must be 16-byte aligned", name);
   if (ld < (size_t)cols) return set_error(EXMOE_ERR_INVALID_ARGUMENT, "%s: row stride %zu smaller than its %d columns", name, ld, cols);
+  if (ld > (1u << 24)) return set_error(EXMOE_ERR_UNSUPPORTED, "%s: row stride %zu larger than 2^24", name, ld);   // 16 rows: 32-bit offsets
   return EXMOE_OK;
 }
 
@@ -318,7 +564,7 @@ using namespace exmoe;
 
 extern "C" size_t exmoe_lora_workspace_bytes(int T, int N, int K, int adapters, int rank_max) {
   if (lora_shape(T, N, K, adapters, rank_max)) return 0;
-  return lora_hl_bytes(T, rank_max) + (size_t)T * ((rank_max + 15) / 16) * 4;
+  return lora_blocks(T, rank_max) * (1024 + 64) + (size_t)T * 8;
 }
 
 extern "C" int exmoe_lora_linear(const void* x, size_t ldx, const void* w, size_t ldw, const exmoe_lora_bank* bank,
@@ -353,7 +599,8 @@ extern "C" int exmoe_lora_linear(const void* x, size_t ldx, const void* w, size_
   a.N = N; a.K = K; a.y = static_cast<uint16_t*>(y); a.vec8 = (uintptr_t)y % 8 == 0 && ldy % 4 == 0;
   a.vec16 = aligned16(y) && ldy % 8 == 0; a.rank_blocks = (bank->rank_max + 15) / 16;
   a.hl = static_cast<uint16_t*>(workspace);
-  a.mul = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + lora_hl_bytes(T, bank->rank_max));
+  a.mul = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + lora_blocks(T, bank->rank_max) * 1024);
+  a.info = reinterpret_cast<int2*>(a.mul + lora_blocks(T, bank->rank_max) * 16);
   const hipError_t e = dtype == EXMOE_DTYPE_FP16 ? launch_lora<ElemFP16>(a, stream) : launch_lora<ElemBF16>(a, stream);
   return e == hipSuccess ? EXMOE_OK : hip_error(e, "exmoe_lora_linear");
 }
