@@ -49,9 +49,9 @@ struct ElemFP16 {
 
 constexpr int kBK = 64;   // depth of one staged slice
 
-// Sixteen zero bytes: what a copy reads in place of elements past the summed axis (device
-// globals start zeroed; never written).
-static __device__ __attribute__((aligned(16))) uint16_t g_zero16[8];
+// Zero bytes: what a copy (16 of them) or load8_any (20) reads in place of elements past the
+// summed axis (device globals start zeroed; never written).
+static __device__ __attribute__((aligned(16))) uint16_t g_zero16[16];
 
 __device__ __forceinline__ void lds_copy16(const void* src, void* dst) {
   __builtin_amdgcn_global_load_lds(src, (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
@@ -59,21 +59,50 @@ __device__ __forceinline__ void lds_copy16(const void* src, void* dst) {
 
 __device__ __forceinline__ int col_swz(int r) { return (r & 3) | (((r >> 3) & 1) << 2); }
 
-// Eight elements of a row-major matrix at any alignment: element i is used when i < n (and
-// ok), else it is zero. Reads only elements that are used, or the operand's first one.
-__device__ __forceinline__ uint4 load8_any(const uint16_t* base, size_t off, int n, bool ok) {
-  uint32_t v[8];
-#pragma unroll
-  for (int j = 0; j < 8; j++) {
-    const bool use = ok && j < n;
-    const uint16_t e = base[use ? off + j : 0];
-    v[j] = use ? e : 0u;
+// Eight elements of a row-major matrix at any alignment: element off + i of base is used when
+// i < n (and ok), else it is zero. Reads only elements of the matrix. fetch() starts the
+// loads, value() gives the elements. Away from the rows' ends (inner): five aligned words
+// around the eight elements, shifted by one element where the address needs it (a fifth of
+// the loads and a tenth of the vector instructions of loading them one by one).
+struct Any8 {
+  uint32_t w0, w1, w2, w3, w4, odd;
+  static __device__ __forceinline__ bool inner(const uint16_t* base, size_t off, int n, bool ok) {
+    // the words hold elements -1 or 0 .. 8 or 9
+    return !ok || (n >= 10 && (off > 0 || ((uintptr_t)base & 2) == 0));
   }
-  return make_uint4(v[0] | (v[1] << 16), v[2] | (v[3] << 16), v[4] | (v[5] << 16), v[6] | (v[7] << 16));
-}
+  __device__ __forceinline__ void fetch(const uint16_t* base, size_t off, bool ok) {   // of an inner one
+    const uint16_t* p = base + off;
+    odd = ok ? (uint32_t)((uintptr_t)p & 2) : 0;
+    typedef uint32_t u32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
+    const uint32_t* q = reinterpret_cast<const uint32_t*>(ok ? (uintptr_t)p & ~(uintptr_t)3 : (uintptr_t)g_zero16);
+    const u32x4_a4 v = *reinterpret_cast<const u32x4_a4*>(q);
+    w0 = v[0];
+    w1 = v[1];
+    w2 = v[2];
+    w3 = v[3];
+    w4 = q[4];
+  }
+  __device__ __forceinline__ void fetch_edge(const uint16_t* base, size_t off, int n, bool ok) {
+    auto pair = [&](int j) __attribute__((always_inline)) {
+      const bool u0 = ok && j < n, u1 = ok && j + 1 < n;
+      const uint32_t e0 = base[u0 ? off + j : 0], e1 = base[u1 ? off + j + 1 : 0];
+      return (u0 ? e0 : 0u) | (u1 ? e1 << 16 : 0u);
+    };
+    w0 = pair(0);
+    w1 = pair(2);
+    w2 = pair(4);
+    w3 = pair(6);
+    w4 = 0;
+    odd = 0;
+  }
+  __device__ __forceinline__ uint4 value() const {
+    return make_uint4(__builtin_amdgcn_alignbyte(w1, w0, odd), __builtin_amdgcn_alignbyte(w2, w1, odd),
+                      __builtin_amdgcn_alignbyte(w3, w2, odd), __builtin_amdgcn_alignbyte(w4, w3, odd));
+  }
+};
 
 // Operand stored as rows (summed axis contiguous), B rows per slice, staged by NW waves.
-template <int B, int NW, bool ALIGNED>
+template <int B, int NW>
 struct RowOperand {
   static constexpr int kSlots = B / 8 / NW;   // copies per lane and slice (8 rows each)
   static_assert(B % (8 * NW) == 0, "rows per slice");
@@ -89,21 +118,37 @@ struct RowOperand {
 #pragma unroll
     for (int i = 0; i < kSlots; i++) off[i] = row_off((i * NW + wave) * 8 + (lane >> 3));
   }
+  __device__ __forceinline__ int column(int i, int k0, int wave, int lane) const {
+    const int row = (i * NW + wave) * 8 + (lane >> 3);
+    return k0 + 8 * ((lane & 7) ^ ((row >> 1) & 7));
+  }
   __device__ __forceinline__ void stage(uint16_t* lds, int k0, int wave, int lane) const {
 #pragma unroll
     for (int i = 0; i < kSlots; i++) {
-      const int row = (i * NW + wave) * 8 + (lane >> 3);
-      const int col = k0 + 8 * ((lane & 7) ^ ((row >> 1) & 7));
+      const int col = column(i, k0, wave, lane);
       uint16_t* dst = lds + (i * NW + wave) * 8 * kBK;
-      if constexpr (ALIGNED) {
-        const uint16_t* src = base + off[i] + col;
-        if (k0 + kBK > red && col >= red) src = g_zero16;
-        lds_copy16(src, dst);
-      } else {
-        const uint4 v = load8_any(base, off[i] + col, red - col, true);
-        *reinterpret_cast<uint4*>(dst + 8 * lane) = v;
-      }
+      const uint16_t* src = base + off[i] + col;
+      if (k0 + kBK > red && col >= red) src = g_zero16;
+      lds_copy16(src, dst);
     }
+  }
+  // any alignment: the slice's loads, and later their values to LDS
+  __device__ __forceinline__ void fetch(Any8 (&r)[kSlots], int k0, int wave, int lane) const {
+    bool in = true;
+#pragma unroll
+    for (int i = 0; i < kSlots; i++) in = in && Any8::inner(base, off[i] + column(i, k0, wave, lane), red - column(i, k0, wave, lane), true);
+    if (__all(in)) {
+#pragma unroll
+      for (int i = 0; i < kSlots; i++) r[i].fetch(base, off[i] + column(i, k0, wave, lane), true);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kSlots; i++)
+        r[i].fetch_edge(base, off[i] + column(i, k0, wave, lane), red - column(i, k0, wave, lane), true);
+    }
+  }
+  __device__ __forceinline__ void commit(const Any8 (&r)[kSlots], uint16_t* lds, int wave, int lane) const {
+#pragma unroll
+    for (int i = 0; i < kSlots; i++) *reinterpret_cast<uint4*>(lds + (i * NW + wave) * 8 * kBK + 8 * lane) = r[i].value();
   }
   // fragment of rows r0..r0+15, summed positions 32 kk + 8 (lane / 16) + 0..7
   static __device__ __forceinline__ bf16x8 frag(const uint16_t* lds, int r0, int kk, int lane) {
@@ -114,7 +159,7 @@ struct RowOperand {
 };
 
 // Operand stored as columns (summed axis outermost), B columns per slice.
-template <int B, int NW, bool ALIGNED>
+template <int B, int NW>
 struct ColOperand {
   static constexpr int kChunks = B / 8;                 // 16-byte chunks per row
   static constexpr int kRows = 64 / kChunks;            // rows per wave-wide copy
@@ -131,25 +176,46 @@ struct ColOperand {
     red = red_;
     ncols = ncols_;
   }
+  __device__ __forceinline__ int row_of(int i, int wave, int lane) const { return (i * NW + wave) * kRows + lane / kChunks; }
+  __device__ __forceinline__ int column(int i, int wave, int lane) const {
+    const int pos = lane % kChunks;
+    return 16 * ((pos >> 1) ^ col_swz(row_of(i, wave, lane))) + 8 * (pos & 1);
+  }
   // row_off(r, i): element offset of row r (0 <= r < red; i: the lane's slot), or ~0 for zeros
   template <class F>
   __device__ __forceinline__ void stage(uint16_t* lds, int k0, int wave, int lane, F row_off) const {
 #pragma unroll
     for (int i = 0; i < kSlots; i++) {
-      const int row = (i * NW + wave) * kRows + lane / kChunks;
-      const int pos = lane % kChunks;
-      const int col = 16 * ((pos >> 1) ^ col_swz(row)) + 8 * (pos & 1);
-      uint16_t* dst = lds + (i * NW + wave) * kRows * B;
-      const size_t o = k0 + row < red ? row_off(k0 + row, i) : ~(size_t)0;
-      if constexpr (ALIGNED) {
-        const uint16_t* src = base + o + (col < ncols ? col : 0);
-        if (o == ~(size_t)0) src = g_zero16;
-        lds_copy16(src, dst);
-      } else {
-        const uint4 v = load8_any(base, o + col, ncols - col, o != ~(size_t)0);
-        *reinterpret_cast<uint4*>(dst + 8 * lane) = v;
-      }
+      const int row = k0 + row_of(i, wave, lane), col = column(i, wave, lane);
+      const size_t o = row < red ? row_off(row, i) : ~(size_t)0;
+      const uint16_t* src = base + o + (col < ncols ? col : 0);
+      if (o == ~(size_t)0) src = g_zero16;
+      lds_copy16(src, lds + (i * NW + wave) * kRows * B);
     }
+  }
+  template <class F>
+  __device__ __forceinline__ void fetch(Any8 (&r)[kSlots], int k0, int wave, int lane, F row_off) const {
+    size_t o[kSlots];
+    bool in = true;
+#pragma unroll
+    for (int i = 0; i < kSlots; i++) {
+      const int row = k0 + row_of(i, wave, lane), col = column(i, wave, lane);
+      o[i] = row < red ? row_off(row, i) : ~(size_t)0;
+      if (col >= ncols) o[i] = ~(size_t)0;
+      in = in && Any8::inner(base, o[i] + col, ncols - col, o[i] != ~(size_t)0);
+    }
+    if (__all(in)) {
+#pragma unroll
+      for (int i = 0; i < kSlots; i++) r[i].fetch(base, o[i] + column(i, wave, lane), o[i] != ~(size_t)0);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kSlots; i++)
+        r[i].fetch_edge(base, o[i] + column(i, wave, lane), ncols - column(i, wave, lane), o[i] != ~(size_t)0);
+    }
+  }
+  __device__ __forceinline__ void commit(const Any8 (&r)[kSlots], uint16_t* lds, int wave, int lane) const {
+#pragma unroll
+    for (int i = 0; i < kSlots; i++) *reinterpret_cast<uint4*>(lds + (i * NW + wave) * kRows * B + 8 * lane) = r[i].value();
   }
   // fragment of columns c0..c0+15, summed positions 32 kk + 8 (lane / 16) + 0..7: two
   // transposing reads, each turning a block of 4 rows x 16 columns per 16 lanes into 4
@@ -198,17 +264,44 @@ template <class ET, int TP, int TQ, int NW>
 __device__ __forceinline__ void skinny_product_any(const uint16_t* __restrict__ x, const size_t (&xrow)[TP],
                                                    const uint16_t* __restrict__ w, const size_t (&wrow)[TQ], int red,
                                                    int wave, int lane, f32x4 (&acc)[TQ][TP]) {
-  for (int k0 = 32 * wave; k0 < red; k0 += 32 * NW) {
-    const int k = k0 + 8 * (lane >> 4);
-    bf16x8 fw[TQ], fx[TP];
+  constexpr int kU = 2;   // steps whose loads are in flight together
+  for (int k0 = 32 * wave; k0 < red; k0 += 32 * NW * kU) {
+    Any8 rw[kU][TQ], rx[kU][TP];
+    bool in = true;
 #pragma unroll
-    for (int j = 0; j < TQ; j++) fw[j] = __builtin_bit_cast(bf16x8, load8_any(w, wrow[j] + k, red - k, true));
+    for (int u = 0; u < kU; u++) {
+      const int k = k0 + 32 * NW * u + 8 * (lane >> 4);
 #pragma unroll
-    for (int i = 0; i < TP; i++) fx[i] = __builtin_bit_cast(bf16x8, load8_any(x, xrow[i] + k, red - k, true));
+      for (int j = 0; j < TQ; j++) in = in && Any8::inner(w, wrow[j] + k, red - k, k < red);
 #pragma unroll
-    for (int j = 0; j < TQ; j++)
+      for (int i = 0; i < TP; i++) in = in && Any8::inner(x, xrow[i] + k, red - k, k < red);
+    }
+    auto fetch_all = [&](auto inner) __attribute__((always_inline)) {
 #pragma unroll
-      for (int i = 0; i < TP; i++) acc[j][i] = ET::mfma(fw[j], fx[i], acc[j][i]);
+      for (int u = 0; u < kU; u++) {
+        const int k = k0 + 32 * NW * u + 8 * (lane >> 4);
+#pragma unroll
+        for (int j = 0; j < TQ; j++) {
+          if constexpr (decltype(inner)::value) rw[u][j].fetch(w, wrow[j] + k, k < red);
+          else rw[u][j].fetch_edge(w, wrow[j] + k, red - k, k < red);
+        }
+#pragma unroll
+        for (int i = 0; i < TP; i++) {
+          if constexpr (decltype(inner)::value) rx[u][i].fetch(x, xrow[i] + k, k < red);
+          else rx[u][i].fetch_edge(x, xrow[i] + k, red - k, k < red);
+        }
+      }
+    };
+    if (__all(in)) fetch_all(std::true_type{});
+    else fetch_all(std::false_type{});
+#pragma unroll
+    for (int u = 0; u < kU; u++)
+#pragma unroll
+      for (int j = 0; j < TQ; j++)
+#pragma unroll
+        for (int i = 0; i < TP; i++)
+          acc[j][i] = ET::mfma(__builtin_bit_cast(bf16x8, rw[u][j].value()), __builtin_bit_cast(bf16x8, rx[u][i].value()),
+                               acc[j][i]);
   }
 }
 

@@ -53,12 +53,12 @@ template <int B, int NW, int D>
 struct WideRows {
   static constexpr int kChunks = D / 8, kRows = 64 / kChunks, kSlots = B / (kRows * NW);
   static constexpr int kReads = 1;   // LDS reads of a fragment
-  static_assert((D == 32 || D == 64) && B % (kRows * NW) == 0 && NW % 2 == 0, "rows per slice");
+  static_assert(B % (kRows * NW) == 0 && (D == 32 || (D == 64 && NW % 2 == 0) || (D == 128 && NW % 4 == 0)), "rows per slice");
   buf_t buf;
   int red, wave, chunk;              // chunk: the lane's first summed position in a slice
   uint32_t voff[kSlots];
 
-  static __device__ __forceinline__ int swz(int row) { return D == 64 ? (row >> 1) & 7 : (row >> 2) & 3; }
+  static __device__ __forceinline__ int swz(int row) { return D == 128 ? row & 15 : D == 64 ? (row >> 1) & 7 : (row >> 2) & 3; }
   // row_off(i): byte offset of row i of the tile, or kNowhere for zeros
   template <class F>
   __device__ __forceinline__ void init(buf_t b, int red_, int wave_, int lane, F row_off) {
@@ -153,12 +153,12 @@ struct WideCols {
 template <int B, int D>
 struct NarrowRows {
   static constexpr int kChunks = D / 8, kRows = 64 / kChunks, kSlots = B / kRows, kElems = B * D;
-  static_assert((D == 64 || D == 128) && B % 16 == 0, "rows of a slice");
+  static_assert((D == 32 || D == 64 || D == 128) && B % 16 == 0, "rows of a slice");
   buf_t buf;
   int red, c0;               // c0: the lane's chunk in its first row
   uint32_t voff[kSlots];
 
-  static __device__ __forceinline__ int swz(int row) { return D == 128 ? row & 15 : (row >> 1) & 7; }
+  static __device__ __forceinline__ int swz(int row) { return D == 128 ? row & 15 : D == 64 ? (row >> 1) & 7 : (row >> 2) & 3; }
   // row_off(i): byte offset of row i, or kNowhere for zeros
   template <class F>
   __device__ __forceinline__ void init(buf_t b, int red_, int lane, F row_off) {
@@ -186,25 +186,67 @@ struct NarrowRows {
   }
 };
 
-// acc[j][i] += rows 16 j.. of w (columns of the output) times rows 16 i.. of x, over this
-// wave's slices; s_a, s_b: this wave's two parts of LDS, (TP + TQ) 16 D elements each.
-template <class ET, int TP, int TQ, int NW, int D>
-__device__ __forceinline__ void narrow_product(const NarrowRows<16 * TP, D>& x, const NarrowRows<16 * TQ, D>& w, int red,
-                                               int wave, int lane, uint16_t* s_a, uint16_t* s_b, f32x4 (&acc)[TQ][TP]) {
-  constexpr int kCopies = NarrowRows<16 * TP, D>::kSlots + NarrowRows<16 * TQ, D>::kSlots;
+// 64 columns of an operand whose summed axis is outermost, D rows of it a slice. The 32-byte
+// unit u of row r lies at position u ^ f(r): the eight rows that 32 lanes of a transposing
+// read touch cover all 64 banks once.
+template <int D>
+struct NarrowCols {
+  static constexpr int kSlots = D / 8, kElems = 64 * D;
+  static_assert(D % 16 == 0, "rows of a slice");
+  buf_t buf;
+  uint32_t ld2;              // bytes per row of the summed axis
+  int red;
+  uint32_t voff[kSlots];
+
+  static __device__ __forceinline__ int f(int row) { return ((row >> 1) & 1) | (((row >> 3) & 1) << 1); }
+  __device__ __forceinline__ void init(buf_t b, uint32_t ld2_, int red_, int ncols, int lane) {
+    buf = b;
+    ld2 = ld2_;
+    red = red_;
+#pragma unroll
+    for (int i = 0; i < kSlots; i++) {
+      const int row = 8 * i + (lane >> 3), pos = lane & 7;
+      const uint32_t c = 32 * ((pos >> 1) ^ f(row)) + 16 * (pos & 1);
+      voff[i] = c < 2 * (uint32_t)ncols ? c + (uint32_t)row * ld2 : kNowhere;
+    }
+  }
+  // rows past the summed axis lie past the buffer's end (a slice wholly past it moves nothing)
+  __device__ __forceinline__ void stage(uint16_t* lds, int k0) const {
+    const bool in = k0 < red;
+    const uint32_t soff = in ? (uint32_t)k0 * ld2 : 0;
+#pragma unroll
+    for (int i = 0; i < kSlots; i++) buf_copy16(buf, lds + 512 * i, in ? voff[i] : kNowhere, soff);
+  }
+  // columns c0..c0 + 15, positions 32 kk + 8 (lane / 16) + 0..7 of the slice
+  static __device__ __forceinline__ bf16x8 frag(const uint16_t* lds, int c0, int kk, int lane) {
+    const int row = 32 * kk + 8 * (lane >> 4) + ((lane >> 2) & 3);   // and row + 4: the same f
+    const uint16_t* p = lds + 64 * row + 16 * ((c0 >> 4) ^ f(row)) + 4 * (lane & 3);
+    typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * 64));
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  }
+};
+
+// acc[j][i] += block j of w (16 columns of the output) times rows 16 i.. of x, over this
+// wave's slices; s_a, s_b: this wave's two parts of LDS, OpX::kElems + OpW::kElems each.
+template <class ET, int TP, int TQ, int NW, int D, class OpX, class OpW>
+__device__ __forceinline__ void narrow_product(const OpX& x, const OpW& w, int red, int wave, int lane, uint16_t* s_a,
+                                               uint16_t* s_b, f32x4 (&acc)[TQ][TP]) {
+  constexpr int kCopies = OpX::kSlots + OpW::kSlots;
   auto issue = [&](int s, uint16_t* lds) __attribute__((always_inline)) {
     const int k0 = (s * NW + wave) * D;
     w.stage(lds, k0);
-    x.stage(lds + 16 * TQ * D, k0);
+    x.stage(lds + OpW::kElems, k0);
   };
   auto compute = [&](const uint16_t* lds) __attribute__((always_inline)) {
 #pragma unroll
     for (int kk = 0; kk < D / 32; kk++) {
       bf16x8 fw[TQ], fx[TP];
 #pragma unroll
-      for (int j = 0; j < TQ; j++) fw[j] = NarrowRows<16 * TQ, D>::frag(lds, 16 * j, kk, lane);
+      for (int j = 0; j < TQ; j++) fw[j] = OpW::frag(lds, 16 * j, kk, lane);
 #pragma unroll
-      for (int i = 0; i < TP; i++) fx[i] = NarrowRows<16 * TP, D>::frag(lds + 16 * TQ * D, 16 * i, kk, lane);
+      for (int i = 0; i < TP; i++) fx[i] = OpX::frag(lds + OpW::kElems, 16 * i, kk, lane);
 #pragma unroll
       for (int j = 0; j < TQ; j++)
 #pragma unroll
@@ -358,11 +400,12 @@ __device__ __forceinline__ void wide_tile(const OpP& op_p, const OpQ& op_q, int 
     read(S1{}, cp, cq, 1);
     multiply(full, S0{});
     interleave(full, None{});
-    if constexpr (D == 64) {
-      read(S0{}, cp, cq, 2);
+#pragma unroll
+    for (int ks = 2; ks < D / 16; ks += 2) {
+      read(S0{}, cp, cq, ks);
       multiply(full, S1{});
       interleave(full, None{});
-      read(S1{}, cp, cq, 3);
+      read(S1{}, cp, cq, ks + 1);
       multiply(full, S0{});
       interleave(full, None{});
     }

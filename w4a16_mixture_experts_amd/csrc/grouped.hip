@@ -39,7 +39,7 @@ __device__ __forceinline__ int wave_scan(int v) {
 
 // Tile of workgroup b among ceil(count_e / BP) x q_tiles tiles per expert. Every wave finds
 // it by itself (no barrier): lane l holds experts 4 l .. 4 l + 3.
-template <int BP>
+template <int BP, int BLOCK = 32>
 __device__ __forceinline__ bool resolve_rows(const int32_t* __restrict__ offsets, int rows, int E, int q_tiles, int b,
                                              RowTile& t) {
   const int lane = (int)lane_id();
@@ -79,13 +79,13 @@ __device__ __forceinline__ bool resolve_rows(const int32_t* __restrict__ offsets
   t.e = e;
   t.seg0 = seg0;
   t.cnt = end - seg0;
-  // the expert's rows are dealt evenly to its tiles, in whole blocks of 32
+  // the expert's rows are dealt evenly to its tiles, in whole blocks
   const int np = (t.cnt + BP - 1) / BP;
   int pt;
   band_order(idx - start * q_tiles, np, q_tiles, pt, t.qt);
-  const int blocks = (t.cnt + 31) / 32, each = blocks / np, more = blocks - each * np;
-  t.p0 = 32 * (each * pt + min(pt, more));
-  t.p1 = min(t.cnt, t.p0 + 32 * (each + (pt < more ? 1 : 0)));
+  const int blocks = (t.cnt + BLOCK - 1) / BLOCK, each = blocks / np, more = blocks - each * np;
+  t.p0 = BLOCK * (each * pt + min(pt, more));
+  t.p1 = min(t.cnt, t.p0 + BLOCK * (each + (pt < more ? 1 : 0)));
   return true;
 }
 
@@ -207,20 +207,34 @@ struct TileWork {
       }
     }
   }
-  // (gradient of W: with the rows of load_idx(k0))
-  __device__ __forceinline__ void stage(int k0, uint16_t* lp, uint16_t* lq) const {
+  // element offset of a row of the Q operand when its summed axis is outermost (gradient of
+  // W: of the rows of load_idx(k0))
+  __device__ __forceinline__ size_t q_row(int r, int i) const {
     if constexpr (MODE == kWG) {
-      op_p.stage(lp, k0, wave, lane, [&](int r, int) { return (size_t)r * a.lda; });
-      op_q.stage(lq, k0, wave, lane, [&](int, int i) {
-        const int v = gidx[i];
-        const int s = v < 0 ? a.x_rows : (a.row_index ? div_by(v, a.row_div, dmul) : v);
-        return s < a.x_rows ? (size_t)s * a.ldb : ~(size_t)0;
-      });
-    } else {
-      op_p.stage(lp, k0, wave, lane);
-      if constexpr (MODE == kMM) op_q.stage(lq, k0, wave, lane);
-      else op_q.stage(lq, k0, wave, lane, [&](int r, int) { return (size_t)r * a.ldb; });
+      const int v = gidx[i];
+      const int s = v < 0 ? a.x_rows : (a.row_index ? div_by(v, a.row_div, dmul) : v);
+      return s < a.x_rows ? (size_t)s * a.ldb : ~(size_t)0;
     }
+    return (size_t)r * a.ldb;
+  }
+  // copies of a slice straight into LDS (aligned operands)
+  __device__ __forceinline__ void stage(int k0, uint16_t* lp, uint16_t* lq) const {
+    if constexpr (MODE == kWG) op_p.stage(lp, k0, wave, lane, [&](int r, int) { return (size_t)r * a.lda; });
+    else op_p.stage(lp, k0, wave, lane);
+    if constexpr (MODE == kMM) op_q.stage(lq, k0, wave, lane);
+    else op_q.stage(lq, k0, wave, lane, [&](int r, int i) { return q_row(r, i); });
+  }
+  // or through registers: the loads, and later the values to LDS
+  __device__ __forceinline__ void fetch(int k0, Any8 (&rp)[OpP::kSlots], Any8 (&rq)[OpQ::kSlots]) const {
+    if constexpr (MODE == kWG) op_p.fetch(rp, k0, wave, lane, [&](int r, int) { return (size_t)r * a.lda; });
+    else op_p.fetch(rp, k0, wave, lane);
+    if constexpr (MODE == kMM) op_q.fetch(rq, k0, wave, lane);
+    else op_q.fetch(rq, k0, wave, lane, [&](int r, int i) { return q_row(r, i); });
+  }
+  __device__ __forceinline__ void commit(const Any8 (&rp)[OpP::kSlots], const Any8 (&rq)[OpQ::kSlots], uint16_t* lp,
+                                         uint16_t* lq) const {
+    op_p.commit(rp, lp, wave, lane);
+    op_q.commit(rq, lq, wave, lane);
   }
   // whether row p of x lies outside x (its outputs are zeros)
   __device__ __forceinline__ bool zero_row(int p) const {
@@ -232,12 +246,13 @@ struct TileWork {
 
 // One BP x BQ output tile per workgroup of WP x WQ waves, each owning a BP/WP x BQ/WQ part;
 // 64-deep slices of both operands double-buffered in LDS, one barrier per slice. The form
-// for operands of any alignment (their elements are loaded one by one).
+// for operands of any alignment (through registers, fetched while the slice before runs) and
+// for aligned ones that 32-bit offsets do not span (ALIGNED).
 template <class ET, int MODE, int BP, int BQ, int WP, int WQ, bool ALIGNED>
 __global__ __launch_bounds__(64 * WP * WQ) void grouped_kernel(GroupedArgs a, int p_tiles, int q_tiles, int splits) {
   constexpr int NW = WP * WQ, TP = BP / WP / 16, TQ = BQ / WQ / 16;
-  using OpP = std::conditional_t<MODE == kWG, ColOperand<BP, NW, ALIGNED>, RowOperand<BP, NW, ALIGNED>>;
-  using OpQ = std::conditional_t<MODE == kMM, RowOperand<BQ, NW, ALIGNED>, ColOperand<BQ, NW, ALIGNED>>;
+  using OpP = std::conditional_t<MODE == kWG, ColOperand<BP, NW>, RowOperand<BP, NW>>;
+  using OpQ = std::conditional_t<MODE == kMM, RowOperand<BQ, NW>, ColOperand<BQ, NW>>;
   __shared__ __attribute__((aligned(16))) uint16_t s_p0[BP * kBK], s_p1[BP * kBK], s_q0[BQ * kBK], s_q1[BQ * kBK];
 
   const int tid = threadIdx.x, lane = tid & 63;
@@ -253,11 +268,13 @@ __global__ __launch_bounds__(64 * WP * WQ) void grouped_kernel(GroupedArgs a, in
     for (int i = 0; i < TP; i++) acc[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   const int steps = (t.t.red + kBK - 1) / kBK;
-  auto step = [&](int s, const uint16_t* cp, const uint16_t* cq, uint16_t* np, uint16_t* nq) {
+  Any8 rp[ALIGNED ? 1 : OpP::kSlots], rq[ALIGNED ? 1 : OpQ::kSlots];
+  auto step = [&](int s, const uint16_t* cp, const uint16_t* cq, uint16_t* np, uint16_t* nq) __attribute__((always_inline)) {
     __builtin_amdgcn_s_waitcnt(0);   // this slice has landed; everyone is past the last one
     __syncthreads();
     if (s + 1 < steps) {
-      t.stage((s + 1) * kBK, np, nq);
+      if constexpr (ALIGNED) t.stage((s + 1) * kBK, np, nq);
+      else t.fetch((s + 1) * kBK, rp, rq);
       t.load_idx((s + 2) * kBK);
     }
 #pragma unroll
@@ -272,10 +289,18 @@ __global__ __launch_bounds__(64 * WP * WQ) void grouped_kernel(GroupedArgs a, in
 #pragma unroll
         for (int j = 0; j < TQ; j++) acc[j][i] = ET::mfma(fq[j], fp[i], acc[j][i]);
     }
+    if constexpr (!ALIGNED) {
+      if (s + 1 < steps) t.commit(rp, rq, np, nq);
+    }
   };
   if (steps > 0) {
     t.load_idx(0);
-    t.stage(0, s_p0, s_q0);
+    if constexpr (ALIGNED) {
+      t.stage(0, s_p0, s_q0);
+    } else {
+      t.fetch(0, rp, rq);
+      t.commit(rp, rq, s_p0, s_q0);
+    }
     t.load_idx(kBK);
     for (int s = 0; s < steps; s += 2) {
       step(s, s_p0, s_q0, s_p1, s_q1);
@@ -351,6 +376,95 @@ __global__ __launch_bounds__(64 * WP * WQ, OCC) void grouped_wide_kernel(Grouped
         return s < a.x_rows ? (uint32_t)s * 2 * (uint32_t)a.ldb : kNowhere;
       },
       [](int, int, auto&) {}, [&](int p) { return MODE == kWG ? p : t.seg0 + p; });
+}
+
+// The forward product for few rows per expert: 16 TP rows x 16 columns per workgroup, the
+// waves split K and W streams through once (gemm_wide.h, narrow_product). Bound by reading W.
+template <class ET, int TP, int NW, int D, bool ALIGNED>
+__global__ __launch_bounds__(64 * NW) void grouped_narrow_kernel(GroupedArgs a, int q_tiles) {
+  constexpr int kPart = ALIGNED ? 16 * (TP + 1) * D : TP * 64 * 8;   // (elements; the sums at least)
+  __shared__ __attribute__((aligned(16))) uint16_t s_a[NW][kPart], s_b[NW][ALIGNED ? kPart : 8];
+  static_assert(sizeof(f32x4) * TP * 64 <= sizeof(s_a[0]), "the sums fit into the slices' part");
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  RowTile r;
+  if (!resolve_rows<16 * TP, 16>(a.offsets, a.rows, a.E, q_tiles, blockIdx.x, r)) return;
+  const int n0 = 16 * r.qt, n = n0 + (lane & 15);
+  const uint32_t dmul = 0xFFFFFFFFu / (uint32_t)a.row_div;
+  // row i of the tile: its row of x, or -1
+  auto source = [&](int i) {
+    const int p = r.p0 + i;
+    if (p >= r.p1) return -1;
+    int s = r.seg0 + p;
+    if (a.row_index) {
+      const int v = a.row_index[s];
+      s = v < 0 ? -1 : div_by(v, a.row_div, dmul);
+    }
+    return s < a.x_rows ? s : -1;
+  };
+  f32x4 acc[1][TP];
+#pragma unroll
+  for (int i = 0; i < TP; i++) acc[0][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const uint16_t* w = a.b + (size_t)r.e * a.b_stride;
+  if constexpr (ALIGNED) {
+    NarrowRows<16 * TP, D> op_x;
+    NarrowRows<16, D> op_w;
+    op_w.init(make_buf(w + (size_t)n0 * a.ldb, 2 * ((size_t)(min(16, a.N - n0) - 1) * a.ldb + a.K)), a.K, lane,
+              [&](int i) { return n0 + i < a.N ? (uint32_t)(i * a.ldb * 2) : kNowhere; });
+    op_x.init(make_buf(a.a, 2 * ((size_t)(a.x_rows - 1) * a.lda + a.K)), a.K, lane, [&](int i) {
+      const int s = source(i);
+      return s < 0 ? kNowhere : (uint32_t)((size_t)s * a.lda * 2);
+    });
+    narrow_product<ET, TP, 1, NW, D>(op_x, op_w, a.K, wave, lane, s_a[wave], s_b[wave], acc);
+  } else {
+    size_t xrow[TP];
+    const size_t wrow[1] = {(size_t)(n < a.N ? n : a.N - 1) * a.ldb};
+    bool zero[TP];
+#pragma unroll
+    for (int i = 0; i < TP; i++) {
+      const int s = source(16 * i + (lane & 15));
+      zero[i] = s < 0;
+      xrow[i] = zero[i] ? 0 : (size_t)s * a.lda;
+    }
+    skinny_product_any<ET, TP, 1, NW>(a.a, xrow, w, wrow, a.K, wave, lane, acc);
+#pragma unroll
+    for (int i = 0; i < TP; i++)
+      if (zero[i]) acc[0][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  __syncthreads();
+  const f32x4 v = skinny_reduce<TP, 1, NW>(reinterpret_cast<f32x4(*)[TP][64]>(&s_a[0][0]), acc, wave, lane);
+  const int p = r.p0 + 16 * wave + (lane & 15), q = n0 + 4 * (lane >> 4);
+  if (wave < TP && p < r.p1 && q < a.N)
+    store4<ET>(a.out, (size_t)(r.seg0 + p) * a.ldo + q, a.out_f32, a.vec, a.N - q, v);
+}
+
+// The gradient of x for few rows per expert: 16 rows x 64 columns per workgroup, the waves
+// split N and W streams through once.
+template <class ET, int NW>
+__global__ __launch_bounds__(64 * NW) void grouped_narrow_dgrad_kernel(GroupedArgs a, int q_tiles) {
+  constexpr int D = 32;
+  using OpX = NarrowRows<16, D>;
+  using OpW = NarrowCols<D>;
+  __shared__ __attribute__((aligned(16))) uint16_t s_a[NW][OpX::kElems + OpW::kElems], s_b[NW][OpX::kElems + OpW::kElems];
+  static_assert(sizeof(f32x4) * 4 * 64 <= sizeof(s_a[0]), "the sums fit into the slices' part");
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  RowTile r;
+  if (!resolve_rows<16, 16>(a.offsets, a.rows, a.E, q_tiles, blockIdx.x, r)) return;
+  const int q0 = 64 * r.qt, p0 = r.seg0 + r.p0, cnt = r.p1 - r.p0;
+  OpX op_x;
+  OpW op_w;
+  op_w.init(make_buf(a.b + (size_t)r.e * a.b_stride + q0, 2 * ((size_t)(a.N - 1) * a.ldb + (a.K - q0))), 2 * (uint32_t)a.ldb,
+            a.N, a.K - q0, lane);
+  op_x.init(make_buf(a.a + (size_t)p0 * a.lda, 2 * ((size_t)(cnt - 1) * a.lda + a.N)), a.N, lane,
+            [&](int i) { return i < cnt ? (uint32_t)(i * a.lda * 2) : kNowhere; });
+  f32x4 acc[4][1];
+#pragma unroll
+  for (int j = 0; j < 4; j++) acc[j][0] = f32x4{0.f, 0.f, 0.f, 0.f};
+  narrow_product<ET, 1, 4, NW, D>(op_x, op_w, a.N, wave, lane, s_a[wave], s_b[wave], acc);
+  __syncthreads();
+  const f32x4 v = skinny_reduce<1, 4, NW>(reinterpret_cast<f32x4(*)[4][64]>(&s_a[0][0]), acc, wave, lane);
+  const int q = q0 + 16 * wave + 4 * (lane >> 4);
+  if (wave < 4 && (lane & 15) < cnt && q < a.K)
+    store4<ET>(a.out, (size_t)(p0 + (lane & 15)) * a.ldo + q, a.out_f32, a.vec, a.K - q, v);
 }
 
 // dx[t, :] = sum_j rows[flat_to_sorted[t k + j], :] in slot order, rounded once. Entries
@@ -467,10 +581,52 @@ static bool large_tiles(int rows, int Q, int E) {
   return rows / E >= 256 && (long long)(rows / 256) * ceil_div(Q, 256) >= 256;
 }
 
+template <class ET, int TP, int NW, int D, bool ALIGNED>
+static hipError_t launch_narrow(const GroupedArgs& a, hipStream_t s) {
+  const long long max_p = a.rows / (16 * TP) + (a.E < a.rows ? a.E : a.rows);
+  const int qt = ceil_div(a.N, 16);
+  if (max_p * qt * (64 * NW) > kMaxThreads) return hipErrorInvalidConfiguration;
+  ProfScope prof("grouped_mm", s);
+  EXMOE_LAUNCH(prof, (grouped_narrow_kernel<ET, TP, NW, D, ALIGNED>), dim3((unsigned)(max_p * qt)), dim3(64 * NW), 0, s, a, qt);
+  return hipGetLastError();
+}
+
+// Rows per expert up to which the forward product runs on 16-row blocks (narrow) instead of
+// 128-row tiles. Measured on 64 experts of 2048 x 2048, us: 2 rows per expert 83 / 117,
+// 8 rows 97 / 128, 16 rows 127 / 130. Operands of any alignment, 13 experts of 517 x 1003: 10
+// rows 11 / 39, 39 rows 21 / 42, 60 rows 28 / 44, 630 rows 193 / 61.
+template <class ET, int NW>
+static hipError_t launch_narrow_dgrad(const GroupedArgs& a, hipStream_t s) {
+  const long long max_p = a.rows / 16 + (a.E < a.rows ? a.E : a.rows);
+  const int qt = ceil_div(a.K, 64);
+  if (max_p * qt * (64 * NW) > kMaxThreads) return hipErrorInvalidConfiguration;
+  ProfScope prof("grouped_dgrad", s);
+  EXMOE_LAUNCH(prof, (grouped_narrow_dgrad_kernel<ET, NW>), dim3((unsigned)(max_p * qt)), dim3(64 * NW), 0, s, a, qt);
+  return hipGetLastError();
+}
+
+// The gradient of x on 16-row blocks instead of 128 x 128 tiles when those leave compute units
+// idle. Measured with 64 experts of 2048 x 2048, us: 1 token (8 rows, 128 tiles) 21 / 31,
+// 4 tokens (512 tiles) 56 / 54, 16 tokens 96 / 95; 16 tokens, 8 experts of 2048 x 512 13 / 25.
+static bool narrow_dgrad(const GroupedArgs& a) {
+  return a.rows <= 10 * a.E && (long long)(a.E < a.rows ? a.E : a.rows) * ceil_div(a.K, 128) < 512 && op_span(16, a.lda, a.N);
+}
+
+// Rows per expert up to which the forward product runs on 16-row blocks (narrow) instead of
+// 128-row tiles. Measured on 64 experts of 2048 x 2048, us: 2 rows per expert 83 / 117,
+// 8 rows 97 / 128, 16 rows 127 / 130, 32 rows 182 / 131. Operands of any alignment, 13 experts
+// of 517 x 1003: 10 rows 11 / 39, 39 rows 21 / 42, 60 rows 28 / 44, 630 rows 193 / 61.
+constexpr int kNarrowRows = 16, kNarrowRowsAny = 128;
+
 template <class ET>
 static hipError_t mm_type(const GroupedArgs& a, hipStream_t s) {
   const bool al = op_aligned(a.a, a.lda, 0, a.K) && op_aligned(a.b, a.ldb, a.b_stride, a.K);
-  if (!al) return launch_rows<ET, kMM, 128, 128, 2, 2, false>(a, "grouped_mm", s);
+  if (!al) {
+    if (a.rows <= kNarrowRowsAny * a.E) return launch_narrow<ET, 1, 8, 64, false>(a, s);
+    return launch_rows<ET, kMM, 128, 128, 2, 2, false>(a, "grouped_mm", s);
+  }
+  if (a.rows <= kNarrowRows * a.E && op_span(a.x_rows, a.lda, a.K) && op_span(16, a.ldb, a.K))
+    return launch_narrow<ET, 1, 4, 64, true>(a, s);
   if (!op_span(a.x_rows, a.lda, a.K) || !op_span(a.N, a.ldb, a.K))
     return launch_rows<ET, kMM, 128, 128, 2, 2, true>(a, "grouped_mm", s);
   if (large_tiles(a.rows, a.N, a.E)) return launch_wide<ET, kMM, 4, 2, 2, 4, 64, 2>(a, "grouped_mm", s);
@@ -496,6 +652,7 @@ static hipError_t dgrad_type(const GroupedArgs& a, hipStream_t s) {
   if (!al) e = launch_rows<ET, kDG, 128, 128, 2, 2, false>(r, "grouped_dgrad", s);
   else if (!op_span(a.rows, a.lda, a.N) || !op_span(a.N, a.ldb, a.K))
     e = launch_rows<ET, kDG, 128, 128, 2, 2, true>(r, "grouped_dgrad", s);
+  else if (narrow_dgrad(a)) e = launch_narrow_dgrad<ET, 8>(r, s);
   else if (large_tiles(a.rows, a.K, a.E)) e = launch_wide<ET, kDG, 4, 2, 2, 4, 64, 2>(r, "grouped_dgrad", s);
   else e = launch_wide<ET, kDG, 2, 2, 2, 2, 64, 2>(r, "grouped_dgrad", s);
   if (e != hipSuccess || !a.flat_to_sorted) return e;
