@@ -144,9 +144,9 @@ __device__ __forceinline__ bool place_tile(const GroupedArgs& a, int p_tiles, in
 // Where a tile's outputs go: the caller's matrix, or the partial sums [split][E][N][K].
 template <int MODE>
 __device__ __forceinline__ TileOut tile_out(const GroupedArgs& a, const TilePlace& t, int splits) {
-  TileOut o{a.out, 0, a.ldo, a.out_f32 != 0, a.vec != 0};
+  TileOut o{a.out, 0, a.ldo, a.out_f32 != 0, a.vec != 0, true};
   if (MODE == kWG) {
-    if (splits > 1) o = TileOut{a.ws, ((size_t)t.split * a.E + t.e) * a.N * a.K, (size_t)a.K, true, a.K % 4 == 0};
+    if (splits > 1) o = TileOut{a.ws, ((size_t)t.split * a.E + t.e) * a.N * a.K, (size_t)a.K, true, a.K % 4 == 0, false};
     else o.base = (size_t)t.e * a.o_stride;
   }
   return o;
@@ -342,13 +342,13 @@ __global__ __launch_bounds__(64 * WP * WQ, OCC) void grouped_wide_kernel(Grouped
   OpP op_p;
   OpQ op_q;
   if constexpr (MODE == kWG) {
-    op_p.template init<false>(make_buf(a.a + (size_t)t.seg0 * a.lda + t.p0, t.red ? 2 * ((t.red - 1) * a.lda + (a.N - t.p0)) : 0),
-              2 * (uint32_t)a.lda, t.red, a.N - t.p0, wave, lane);
-    op_q.template init<true>(make_buf(a.b + t.q0, a.x_rows ? 2 * ((a.x_rows - 1) * a.ldb + (a.K - t.q0)) : 0), 2 * (uint32_t)a.ldb,
-              t.red, a.K - t.q0, wave, lane);
+    op_p.template init<false>(make_buf(a.a + (size_t)t.seg0 * a.lda + t.p0, t.red ? 2 * ((t.red - 1) * a.lda + (a.len_a - t.p0)) : 0),
+              2 * (uint32_t)a.lda, t.red, a.len_a - t.p0, wave, lane);
+    op_q.template init<true>(make_buf(a.b + t.q0, a.x_rows ? 2 * ((a.x_rows - 1) * a.ldb + (a.len_b - t.q0)) : 0),
+                                 2 * (uint32_t)a.ldb, t.red, a.len_b - t.q0, wave, lane);
   } else {
     const int rows_a = MODE == kMM ? a.x_rows : a.rows;
-    op_p.init(make_buf(a.a, 2 * ((rows_a - 1) * a.lda + t.red)), t.red, wave, lane, [&](int i) {
+    op_p.init(make_buf(a.a, 2 * ((rows_a - 1) * a.lda + a.len_a)), t.red, wave, lane, [&](int i) {
       int s = t.seg0 + t.p0 + i;
       bool ok = t.p0 + i < t.cnt;
       if (MODE == kMM && a.row_index) {
@@ -360,11 +360,11 @@ __global__ __launch_bounds__(64 * WP * WQ, OCC) void grouped_wide_kernel(Grouped
     });
     const uint16_t* w = a.b + (size_t)t.e * a.b_stride;
     if constexpr (MODE == kMM) {
-      op_q.init(make_buf(w, 2 * ((a.N - 1) * a.ldb + a.K)), t.red, wave, lane, [&](int i) {
+      op_q.init(make_buf(w, 2 * ((a.N - 1) * a.ldb + a.len_b)), t.red, wave, lane, [&](int i) {
         return t.q0 + i < Q ? (uint32_t)((size_t)(t.q0 + i) * a.ldb * 2) : kNowhere;
       });
     } else {
-      op_q.template init<false>(make_buf(w + t.q0, 2 * ((a.N - 1) * a.ldb + (Q - t.q0))), 2 * (uint32_t)a.ldb, t.red, Q - t.q0,
+      op_q.template init<false>(make_buf(w + t.q0, 2 * ((a.N - 1) * a.ldb + (a.len_b - t.q0))), 2 * (uint32_t)a.ldb, t.red, a.len_b - t.q0,
                 wave, lane);
     }
   }
@@ -452,9 +452,9 @@ __global__ __launch_bounds__(64 * NW) void grouped_narrow_dgrad_kernel(GroupedAr
   const int q0 = 64 * r.qt, p0 = r.seg0 + r.p0, cnt = r.p1 - r.p0;
   OpX op_x;
   OpW op_w;
-  op_w.init(make_buf(a.b + (size_t)r.e * a.b_stride + q0, 2 * ((size_t)(a.N - 1) * a.ldb + (a.K - q0))), 2 * (uint32_t)a.ldb,
-            a.N, a.K - q0, lane);
-  op_x.init(make_buf(a.a + (size_t)p0 * a.lda, 2 * ((size_t)(cnt - 1) * a.lda + a.N)), a.N, lane,
+  op_w.init(make_buf(a.b + (size_t)r.e * a.b_stride + q0, 2 * ((size_t)(a.N - 1) * a.ldb + (a.len_b - q0))),
+            2 * (uint32_t)a.ldb, a.N, a.len_b - q0, lane);
+  op_x.init(make_buf(a.a + (size_t)p0 * a.lda, 2 * ((size_t)(cnt - 1) * a.lda + a.len_a)), a.N, lane,
             [&](int i) { return i < cnt ? (uint32_t)(i * a.lda * 2) : kNowhere; });
   f32x4 acc[4][1];
 #pragma unroll
@@ -502,19 +502,61 @@ __global__ __launch_bounds__(256) void token_sum_kernel(const float* __restrict_
     static_cast<uint16_t*>(out)[o] = ET::from_f32(v[0]);
 }
 
-// dW = sum of the partial sums in split order.
-template <class ET>
-__global__ __launch_bounds__(256) void split_sum_kernel(const float* __restrict__ part, int splits, int E, int N, int K,
-                                                        void* out, size_t ldo, size_t o_stride, int out_f32) {
-  const size_t n = (size_t)E * N * K;
+// Rows of len elements at any alignment into rows of pad (a multiple of 8) elements, zeros
+// behind the len-th. Row r of group g comes from src + g stride + (row of r) ld, the row being
+// r or row_index[r] / row_div (rows outside the src_rows of src: zeros). With offsets, group g
+// is expert g, and experts without rows are left out. One thread per 8 elements.
+__global__ __launch_bounds__(256) void pack_rows_kernel(const uint16_t* __restrict__ src, size_t ld, size_t stride, int len,
+                                                        int rows, int src_rows, const int32_t* __restrict__ row_index,
+                                                        int row_div, const int32_t* __restrict__ offsets,
+                                                        uint16_t* __restrict__ dst, int pad) {
+  const int per = pad / 8, g = blockIdx.y;
+  if (offsets && offsets[g + 1] <= offsets[g]) return;
   const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
+  const bool in = i < (size_t)rows * per;
+  const int r = in ? (int)(i / per) : 0, c = in ? (int)(i - (size_t)r * per) * 8 : 0;
+  int s = r;
+  if (row_index) {
+    const int v = row_index[r];
+    s = v < 0 ? src_rows : div_by(v, row_div, 0xFFFFFFFFu / (uint32_t)row_div);
+  }
+  const bool ok = in && s < src_rows;
+  const uint16_t* base = src + (size_t)g * stride;
+  const size_t off = ok ? (size_t)s * ld + c : 0;
+  Any8 v;
+  if (__all(Any8::inner(base, off, len - c, ok))) v.fetch(base, off, ok);
+  else v.fetch_edge(base, off, len - c, ok);
+  if (in) *reinterpret_cast<uint4*>(dst + ((size_t)g * rows + r) * pad + c) = v.value();
+}
+
+// dW = sum of the partial sums in split order, VEC outputs of a row per thread.
+template <class ET, int VEC>
+__global__ __launch_bounds__(256) void split_sum_kernel(const float* __restrict__ part, int splits, int E, int N, int K,
+                                                        void* out, size_t ldo, size_t o_stride, int out_f32, int vec) {
+  const size_t n = (size_t)E * N * K;
+  const size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * VEC;
   if (i >= n) return;
-  float v = 0.f;
-  for (int s = 0; s < splits; s++) v += part[(size_t)s * n + i];
+  float v[VEC];
+#pragma unroll
+  for (int q = 0; q < VEC; q++) v[q] = 0.f;
+#pragma unroll 8
+  for (int s = 0; s < splits; s++) {
+    if constexpr (VEC == 4) {
+      const f32x4 r = *reinterpret_cast<const f32x4*>(part + (size_t)s * n + i);
+#pragma unroll
+      for (int q = 0; q < 4; q++) v[q] += r[q];
+    } else {
+      v[0] += part[(size_t)s * n + i];
+    }
+  }
   const size_t row = i / K, col = i - row * K, e = row / N;
   const size_t o = e * o_stride + (row - e * N) * ldo + col;
-  if (out_f32) static_cast<float*>(out)[o] = v;
-  else static_cast<uint16_t*>(out)[o] = ET::from_f32(v);
+  if constexpr (VEC == 4)
+    store4<ET>(out, o, out_f32, vec, 4, f32x4{v[0], v[1], v[2], v[3]});
+  else if (out_f32)
+    static_cast<float*>(out)[o] = v[0];
+  else
+    static_cast<uint16_t*>(out)[o] = ET::from_f32(v[0]);
 }
 
 // ------------------------------------------------------------------------------------ host
@@ -526,19 +568,48 @@ constexpr long long kMaxThreads = 0xFFFFFFFFll;   // of one launch; larger calls
 static int wgrad_splits(int rows, int N, int K, int E) {
   const long long tiles = (long long)E * ceil_div(N, 128) * ceil_div(K, 128);
   const int avg = rows / E;
-  long long s = 512 / (tiles > 0 ? tiles : 1);
+  long long s = 384 / (tiles > 0 ? tiles : 1);
   if (s > avg / 256) s = avg / 256;
   if (s > 16) s = 16;
   return s < 1 ? 1 : (int)s;
 }
 
-size_t grouped_workspace_bytes(int op, int rows, int N, int K, int E, int k) {
-  if (op == EXMOE_GROUPED_DGRAD && k > 0) return (size_t)rows * K * 4;
-  if (op == EXMOE_GROUPED_WGRAD) {
+static inline int pad8(int n) { return (n + 7) & ~7; }
+static inline size_t align16(size_t n) { return (n + 15) & ~(size_t)15; }
+constexpr int kNarrowRowsAny = 128;   // see kNarrowRows
+
+// Operands whose rows are no multiple of 16 bytes long are copied with padded rows first, so
+// that the products run on their aligned forms (one pass over the operand against loads
+// through registers in the product: gradient of x, 1384 rows, N = 7827, K = 384: XX -> YY us).
+// Not for the forward product's few rows per expert, which have a form of their own.
+GroupedWorkspace grouped_workspace(int op, int rows, int N, int K, int E, int k) {
+  GroupedWorkspace w{0, 0, 0};
+  const size_t rows_n = align16((size_t)rows * pad8(N) * 2), rows_k = align16((size_t)rows * pad8(K) * 2),
+               weights = align16((size_t)E * N * pad8(K) * 2);
+  if (op == EXMOE_GROUPED_MM) {
+    if (K % 8 && rows > kNarrowRowsAny * (long long)E) w.pack_a = rows_k, w.pack_b = weights;
+  } else if (op == EXMOE_GROUPED_DGRAD) {
+    if (k > 0) w.sums = align16((size_t)rows * K * 4);
+    if (N % 8) w.pack_a = rows_n;
+    if (K % 8) w.pack_b = weights;
+  } else {
     const int s = wgrad_splits(rows, N, K, E);
-    return s > 1 ? (size_t)s * E * N * K * 4 : 0;
+    if (s > 1) w.sums = align16((size_t)s * E * N * K * 4);
+    if (N % 8) w.pack_a = rows_n;
+    if (K % 8) w.pack_b = rows_k;
   }
-  return 0;
+  return w;
+}
+
+static hipError_t pack_rows(const uint16_t* src, size_t ld, size_t stride, int len, int rows, int groups, int src_rows,
+                            const int32_t* row_index, int row_div, const int32_t* offsets, uint16_t* dst, hipStream_t s) {
+  const int pad = pad8(len);
+  const size_t n = (size_t)rows * (pad / 8);
+  if (n > (size_t)kMaxThreads) return hipErrorInvalidConfiguration;
+  ProfScope prof("pack_rows", s);
+  EXMOE_LAUNCH(prof, pack_rows_kernel, dim3((unsigned)((n + 255) / 256), groups), dim3(256), 0, s, src, ld, stride, len, rows,
+               src_rows, row_index, row_div, offsets, dst, pad);
+  return hipGetLastError();
 }
 
 template <class ET, int MODE, int BP, int BQ, int WP, int WQ, bool ALIGNED>
@@ -609,37 +680,63 @@ static hipError_t launch_narrow_dgrad(const GroupedArgs& a, hipStream_t s) {
 // idle. Measured with 64 experts of 2048 x 2048, us: 1 token (8 rows, 128 tiles) 21 / 31,
 // 4 tokens (512 tiles) 56 / 54, 16 tokens 96 / 95; 16 tokens, 8 experts of 2048 x 512 13 / 25.
 static bool narrow_dgrad(const GroupedArgs& a) {
-  return a.rows <= 10 * a.E && (long long)(a.E < a.rows ? a.E : a.rows) * ceil_div(a.K, 128) < 512 && op_span(16, a.lda, a.N);
+  return a.rows <= 10 * a.E && (long long)(a.E < a.rows ? a.E : a.rows) * ceil_div(a.K, 128) < 512 && op_span(16, a.lda, a.len_a);
 }
 
 // Rows per expert up to which the forward product runs on 16-row blocks (narrow) instead of
 // 128-row tiles. Measured on 64 experts of 2048 x 2048, us: 2 rows per expert 83 / 117,
 // 8 rows 97 / 128, 16 rows 127 / 130, 32 rows 182 / 131. Operands of any alignment, 13 experts
 // of 517 x 1003: 10 rows 11 / 39, 39 rows 21 / 42, 60 rows 28 / 44, 630 rows 193 / 61.
-constexpr int kNarrowRows = 16, kNarrowRowsAny = 128;
+constexpr int kNarrowRows = 16;
 
 template <class ET>
 static hipError_t mm_type(const GroupedArgs& a, hipStream_t s) {
-  const bool al = op_aligned(a.a, a.lda, 0, a.K) && op_aligned(a.b, a.ldb, a.b_stride, a.K);
+  const bool al = op_aligned(a.a, a.lda, 0, a.len_a) && op_aligned(a.b, a.ldb, a.b_stride, a.len_b);
   if (!al) {
-    if (a.rows <= kNarrowRowsAny * a.E) return launch_narrow<ET, 1, 8, 64, false>(a, s);
+    if (a.rows <= kNarrowRowsAny * (long long)a.E) return launch_narrow<ET, 1, 8, 64, false>(a, s);
     return launch_rows<ET, kMM, 128, 128, 2, 2, false>(a, "grouped_mm", s);
   }
-  if (a.rows <= kNarrowRows * a.E && op_span(a.x_rows, a.lda, a.K) && op_span(16, a.ldb, a.K))
+  if (a.rows <= kNarrowRows * (long long)a.E && op_span(a.x_rows, a.lda, a.K) && op_span(16, a.ldb, a.K))
     return launch_narrow<ET, 1, 4, 64, true>(a, s);
-  if (!op_span(a.x_rows, a.lda, a.K) || !op_span(a.N, a.ldb, a.K))
+  if (!op_span(a.x_rows, a.lda, a.len_a) || !op_span(a.N, a.ldb, a.len_b))
     return launch_rows<ET, kMM, 128, 128, 2, 2, true>(a, "grouped_mm", s);
   if (large_tiles(a.rows, a.N, a.E)) return launch_wide<ET, kMM, 4, 2, 2, 4, 64, 2>(a, "grouped_mm", s);
   return launch_wide<ET, kMM, 2, 2, 2, 2, 64, 2>(a, "grouped_mm", s);
 }
 
-hipError_t launch_grouped_mm(const GroupedArgs& a, hipStream_t s) {
+// Copies the operands that need it; a then describes the copies. A launch that is too large
+// is refused before: the copies' sizes are bounded by the products' own.
+static hipError_t pack_a_rows(GroupedArgs& a, int len, bool gather, hipStream_t s) {
+  hipError_t e = pack_rows(a.a, a.lda, 0, len, a.rows, 1, gather ? a.x_rows : a.rows, gather ? a.row_index : nullptr,
+                           a.row_div, nullptr, a.pack_a, s);
+  a.a = a.pack_a;
+  a.lda = a.len_a = pad8(len);
+  return e;
+}
+static hipError_t pack_weights(GroupedArgs& a, hipStream_t s) {
+  hipError_t e = pack_rows(a.b, a.ldb, a.b_stride, a.K, a.N, a.E, a.N, nullptr, 1, a.offsets, a.pack_b, s);
+  a.b = a.pack_b;
+  a.ldb = a.len_b = pad8(a.K);
+  a.b_stride = (size_t)a.N * a.ldb;
+  return e;
+}
+
+hipError_t launch_grouped_mm(const GroupedArgs& given, hipStream_t s) {
+  GroupedArgs a = given;
+  hipError_t e = hipSuccess;
+  if (a.pack_a) {
+    if ((e = pack_a_rows(a, a.K, true, s)) != hipSuccess) return e;
+    a.x_rows = a.rows;
+    a.row_index = nullptr;
+    a.row_div = 1;
+  }
+  if (a.pack_b && (e = pack_weights(a, s)) != hipSuccess) return e;
   return a.fp16 ? mm_type<ElemFP16>(a, s) : mm_type<ElemBF16>(a, s);
 }
 
 template <class ET>
 static hipError_t dgrad_type(const GroupedArgs& a, hipStream_t s) {
-  const bool al = op_aligned(a.a, a.lda, 0, a.N) && op_aligned(a.b, a.ldb, a.b_stride, a.K);
+  const bool al = op_aligned(a.a, a.lda, 0, a.len_a) && op_aligned(a.b, a.ldb, a.b_stride, a.len_b);
   GroupedArgs r = a;
   if (a.flat_to_sorted) {
     if ((long long)(a.rows / a.k) * a.K > kMaxThreads) return hipErrorInvalidConfiguration;
@@ -650,7 +747,7 @@ static hipError_t dgrad_type(const GroupedArgs& a, hipStream_t s) {
   }
   hipError_t e;
   if (!al) e = launch_rows<ET, kDG, 128, 128, 2, 2, false>(r, "grouped_dgrad", s);
-  else if (!op_span(a.rows, a.lda, a.N) || !op_span(a.N, a.ldb, a.K))
+  else if (!op_span(a.rows, a.lda, a.len_a) || !op_span(a.N, a.ldb, a.len_b))
     e = launch_rows<ET, kDG, 128, 128, 2, 2, true>(r, "grouped_dgrad", s);
   else if (narrow_dgrad(a)) e = launch_narrow_dgrad<ET, 8>(r, s);
   else if (large_tiles(a.rows, a.K, a.E)) e = launch_wide<ET, kDG, 4, 2, 2, 4, 64, 2>(r, "grouped_dgrad", s);
@@ -670,7 +767,11 @@ static hipError_t dgrad_type(const GroupedArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_grouped_dgrad(const GroupedArgs& a, hipStream_t s) {
+hipError_t launch_grouped_dgrad(const GroupedArgs& given, hipStream_t s) {
+  GroupedArgs a = given;
+  hipError_t e = hipSuccess;
+  if (a.pack_a && (e = pack_a_rows(a, a.N, false, s)) != hipSuccess) return e;
+  if (a.pack_b && (e = pack_weights(a, s)) != hipSuccess) return e;
   return a.fp16 ? dgrad_type<ElemFP16>(a, s) : dgrad_type<ElemBF16>(a, s);
 }
 
@@ -692,9 +793,9 @@ template <class ET>
 static hipError_t wgrad_type(const GroupedArgs& a, hipStream_t s) {
   const int splits = wgrad_splits(a.rows, a.N, a.K, a.E);
   hipError_t e;
-  if (!op_aligned(a.a, a.lda, 0, a.N) || !op_aligned(a.b, a.ldb, 0, a.K))
+  if (!op_aligned(a.a, a.lda, 0, a.len_a) || !op_aligned(a.b, a.ldb, 0, a.len_b))
     e = launch_weights<128, 128, 256>(a, s, splits, grouped_kernel<ET, kWG, 128, 128, 2, 2, false>);
-  else if (!op_span(a.rows, a.lda, a.N) || !op_span(a.x_rows, a.ldb, a.K))
+  else if (!op_span(a.rows, a.lda, a.len_a) || !op_span(a.x_rows, a.ldb, a.len_b))
     e = launch_weights<128, 128, 256>(a, s, splits, grouped_kernel<ET, kWG, 128, 128, 2, 2, true>);
   else if (a.rows / a.E >= 768 && splits == 1 && (long long)a.E * ceil_div(a.N, 256) * ceil_div(a.K, 256) >= 256)
     e = launch_weights_wide<ET, 4, 2, 2, 4, 64, 2>(a, s, splits);
@@ -707,12 +808,28 @@ static hipError_t wgrad_type(const GroupedArgs& a, hipStream_t s) {
   if (e != hipSuccess || splits == 1) return e;
   const size_t n = (size_t)a.E * a.N * a.K;
   ProfScope prof("split_sum", s);
-  EXMOE_LAUNCH(prof, (split_sum_kernel<ET>), dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a.ws, splits, a.E, a.N,
-               a.K, a.out, a.ldo, a.o_stride, a.out_f32);
+  if (a.K % 4 == 0)
+    EXMOE_LAUNCH(prof, (split_sum_kernel<ET, 4>), dim3((unsigned)((n / 4 + 255) / 256)), dim3(256), 0, s, a.ws, splits, a.E,
+                 a.N, a.K, a.out, a.ldo, a.o_stride, a.out_f32, a.vec);
+  else
+    EXMOE_LAUNCH(prof, (split_sum_kernel<ET, 1>), dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a.ws, splits, a.E,
+                 a.N, a.K, a.out, a.ldo, a.o_stride, a.out_f32, a.vec);
   return hipGetLastError();
 }
 
-hipError_t launch_grouped_wgrad(const GroupedArgs& a, hipStream_t s) {
+hipError_t launch_grouped_wgrad(const GroupedArgs& given, hipStream_t s) {
+  GroupedArgs a = given;
+  hipError_t e = hipSuccess;
+  if (a.rows > 0 && a.pack_a && (e = pack_a_rows(a, a.N, false, s)) != hipSuccess) return e;
+  if (a.rows > 0 && a.pack_b) {
+    e = pack_rows(a.b, a.ldb, 0, a.K, a.rows, 1, a.x_rows, a.row_index, a.row_div, nullptr, a.pack_b, s);
+    if (e != hipSuccess) return e;
+    a.b = a.pack_b;
+    a.ldb = a.len_b = pad8(a.K);
+    a.x_rows = a.rows;
+    a.row_index = nullptr;
+    a.row_div = 1;
+  }
   return a.fp16 ? wgrad_type<ElemFP16>(a, s) : wgrad_type<ElemBF16>(a, s);
 }
 
@@ -772,6 +889,13 @@ static int vec_store(const void* p, size_t ld, size_t stride, int out_f32) {
   return aligned16(p) && ld % n == 0 && stride % n == 0;
 }
 
+static void set_workspace(GroupedArgs& a, const GroupedWorkspace& need, void* ws) {
+  uint8_t* p = static_cast<uint8_t*>(ws);
+  a.ws = reinterpret_cast<float*>(p);
+  a.pack_a = need.pack_a ? reinterpret_cast<uint16_t*>(p + need.sums) : nullptr;
+  a.pack_b = need.pack_b ? reinterpret_cast<uint16_t*>(p + need.sums + need.pack_a) : nullptr;
+}
+
 #define EXMOE_TRY(call)        \
   do {                         \
     const int st_ = (call);    \
@@ -784,7 +908,7 @@ extern "C" size_t exmoe_grouped_mm_workspace_bytes(int op, int rows, int N, int 
     return 0;
   }
   if (grouped_shape(rows, N, K, E, EXMOE_DTYPE_BF16, EXMOE_DTYPE_BF16)) return 0;
-  return grouped_workspace_bytes(op, rows, N, K, E, k);
+  return grouped_workspace(op, rows, N, K, E, k).total();
 }
 
 extern "C" int exmoe_grouped_mm(const void* x, size_t ldx, int x_rows, const int32_t* row_index, int row_div,
@@ -803,12 +927,14 @@ extern "C" int exmoe_grouped_mm(const void* x, size_t ldx, int x_rows, const int
   EXMOE_TRY(check_matrix("y", y, ldy, N, ob));
   EXMOE_TRY(check_int32("row_index", row_index, true));
   EXMOE_TRY(check_int32("expert_offsets", expert_offsets, false));
-  EXMOE_TRY(check_ws(grouped_workspace_bytes(EXMOE_GROUPED_MM, rows, N, K, E, 0), workspace, ws_bytes));
+  const GroupedWorkspace need = grouped_workspace(EXMOE_GROUPED_MM, rows, N, K, E, 0);
+  EXMOE_TRY(check_ws(need.total(), workspace, ws_bytes));
   GroupedArgs a{};
   a.a = static_cast<const uint16_t*>(x); a.b = static_cast<const uint16_t*>(w); a.lda = ldx; a.ldb = ldw;
   a.b_stride = w_stride; a.offsets = expert_offsets; a.row_index = row_index; a.row_div = row_div; a.x_rows = x_rows;
   a.rows = rows; a.N = N; a.K = K; a.E = E; a.out = y; a.ldo = ldy; a.fp16 = dtype == EXMOE_DTYPE_FP16;
-  a.out_f32 = ob == 4; a.vec = vec_store(y, ldy, 0, a.out_f32); a.ws = static_cast<float*>(workspace);
+  a.out_f32 = ob == 4; a.vec = vec_store(y, ldy, 0, a.out_f32); a.len_a = a.len_b = K;
+  set_workspace(a, need, workspace);
   return launched(launch_grouped_mm(a, stream), "exmoe_grouped_mm");
 }
 
@@ -827,14 +953,15 @@ extern "C" int exmoe_grouped_mm_dgrad(const void* dy, size_t lddy, const int32_t
   EXMOE_TRY(check_matrix("dx", dx, lddx, K, ob));
   EXMOE_TRY(check_int32("expert_offsets", expert_offsets, false));
   EXMOE_TRY(check_int32("flat_to_sorted", flat_to_sorted, true));
-  EXMOE_TRY(check_ws(grouped_workspace_bytes(EXMOE_GROUPED_DGRAD, rows, N, K, E, flat_to_sorted ? k : 0), workspace,
-                     ws_bytes));
+  const GroupedWorkspace need = grouped_workspace(EXMOE_GROUPED_DGRAD, rows, N, K, E, flat_to_sorted ? k : 0);
+  EXMOE_TRY(check_ws(need.total(), workspace, ws_bytes));
   GroupedArgs a{};
   a.a = static_cast<const uint16_t*>(dy); a.b = static_cast<const uint16_t*>(w); a.lda = lddy; a.ldb = ldw;
   a.b_stride = w_stride; a.offsets = expert_offsets; a.row_div = 1; a.x_rows = rows; a.rows = rows; a.N = N; a.K = K;
   a.E = E; a.out = dx; a.ldo = lddx; a.fp16 = dtype == EXMOE_DTYPE_FP16; a.out_f32 = ob == 4;
-  a.vec = vec_store(dx, lddx, 0, a.out_f32); a.flat_to_sorted = flat_to_sorted; a.k = k;
-  a.ws = static_cast<float*>(workspace);
+  a.vec = vec_store(dx, lddx, 0, a.out_f32); a.flat_to_sorted = flat_to_sorted; a.k = k; a.len_a = N;
+  a.len_b = K;
+  set_workspace(a, need, workspace);
   return launched(launch_grouped_dgrad(a, stream), "exmoe_grouped_mm_dgrad");
 }
 
@@ -855,11 +982,13 @@ extern "C" int exmoe_grouped_mm_wgrad(const void* dy, size_t lddy, const void* x
   EXMOE_TRY(check_experts("dw", lddw, dw_stride, N, K, E));
   EXMOE_TRY(check_int32("row_index", row_index, true));
   EXMOE_TRY(check_int32("expert_offsets", expert_offsets, false));
-  EXMOE_TRY(check_ws(grouped_workspace_bytes(EXMOE_GROUPED_WGRAD, rows, N, K, E, 0), workspace, ws_bytes));
+  const GroupedWorkspace need = grouped_workspace(EXMOE_GROUPED_WGRAD, rows, N, K, E, 0);
+  EXMOE_TRY(check_ws(need.total(), workspace, ws_bytes));
   GroupedArgs a{};
   a.a = static_cast<const uint16_t*>(dy); a.b = static_cast<const uint16_t*>(x); a.lda = lddy; a.ldb = ldx;
   a.offsets = expert_offsets; a.row_index = row_index; a.row_div = row_div; a.x_rows = x_rows; a.rows = rows; a.N = N;
   a.K = K; a.E = E; a.out = dw; a.ldo = lddw; a.o_stride = dw_stride; a.fp16 = dtype == EXMOE_DTYPE_FP16;
-  a.out_f32 = ob == 4; a.vec = vec_store(dw, lddw, dw_stride, a.out_f32); a.ws = static_cast<float*>(workspace);
+  a.out_f32 = ob == 4; a.vec = vec_store(dw, lddw, dw_stride, a.out_f32); a.len_a = N; a.len_b = K;
+  set_workspace(a, need, workspace);
   return launched(launch_grouped_wgrad(a, stream), "exmoe_grouped_mm_wgrad");
 }
