@@ -159,6 +159,18 @@ def test_wgrad_refusals():
     assert _wg(rows=1 << 16, x_rows=1 << 16) == exm.ERR_WORKSPACE
 
 
+def test_odd_row_lengths_need_a_workspace():
+    """Operands whose rows are no multiple of 8 elements are copied with padded rows first."""
+    need = exm.grouped_mm_workspace_bytes(exm.GROUPED_MM, 512, 32, 63, 2)
+    assert need >= (512 * 64 + 2 * 32 * 64) * 2
+    assert _mm(rows=512, x_rows=512, K=63) == exm.ERR_WORKSPACE and str(need) in exm.last_error()
+    for op, call in ((exm.GROUPED_DGRAD, _dg), (exm.GROUPED_WGRAD, _wg)):
+        for n, k in ((31, 64), (32, 63), (31, 63)):
+            need = exm.grouped_mm_workspace_bytes(op, 8, n, k, 2, 0)
+            assert need > 0
+            assert call(N=n, K=k) == exm.ERR_WORKSPACE and str(need) in exm.last_error()
+
+
 def test_workspace_query_of_bad_arguments():
     assert exm.grouped_mm_workspace_bytes(3, 8, 8, 8, 2) == 0
     assert exm.grouped_mm_workspace_bytes(exm.GROUPED_DGRAD, 8, 8, 8, 300, 1) == 0
@@ -395,6 +407,132 @@ def test_offsets_past_32_bits():
     y = ybuf.as_strided((40, N), (ld, 1))
     exm.grouped_mm(xd, wd, off.cuda(), y=y)
     equal(y, plain_mm(x, w, off, src)[0], "mm into wide rows")
+
+
+# (counts, N, K): 16-row blocks and 64 x 64 blocks (few tiles), 128 x 128 and 256 x 256 tiles in
+# each direction, split and whole sums over the rows; ragged edges everywhere; odd row lengths,
+# few and many rows per expert.
+FORMS = [([3, 0, 9, 1], 72, 136), ([100, 0, 37, 201], 200, 264), ([130, 0, 1000, 1, 600], 904, 136),
+         ([130, 0, 1000, 1, 600], 136, 904), ([1, 4199], 4104, 72), ([4200], 72, 4104), ([0, 1600], 2824, 2824),
+         ([200, 0, 190], 41, 77), ([200, 0, 190], 40, 77), ([9, 200, 2], 41, 80), ([700, 690], 523, 129), ([1, 2], 41, 77),
+         ([0, 2500], 130, 1001)]
+
+
+@gpu
+@pytest.mark.parametrize("counts,N,K", FORMS)
+@pytest.mark.parametrize("dtype,out", [(BF16, FP32), (FP16, FP16)])
+def test_every_form_with_a_gather_nan_neighbours_and_bad_indices(counts, N, K, dtype, out):
+    """Operands inside wider tensors of NaN, rows before the first and behind the last segment,
+    x gathered through an index with two entries outside it; outputs into wider tensors."""
+    print(f"forms counts={counts} N={N} K={K} {dtype} -> {out}", flush=True)
+    gen = torch.Generator().manual_seed(N * 7 + K)
+    E, grouped = len(counts), sum(counts)
+    lead, rows, xr = 4, grouped + 4 + 3, grouped // 2 + 1
+    off = offsets_of(counts) + lead
+    x, w, dy = whole(gen, (xr, K), -1, 2), whole(gen, (E, N, K), -1, 2), whole(gen, (rows, N), -1, 2)
+    idx = torch.randint(0, 2 * xr, (rows,), generator=gen).to(torch.int32)
+    src = idx.long() // 2
+    bad = [lead, lead + grouped - 1] if grouped > 3 else []
+    idx[bad] = torch.tensor([-1, 2 * xr], dtype=torch.int32)[:len(bad)]
+    odd = 1 if K % 8 else 8
+    xw, xd = strided(x, dtype, odd, 8)
+    _, dyd = strided(dy, dtype, 1 if N % 8 else 8, 8)
+    dyd[:lead], dyd[lead + grouped:] = float("nan"), float("nan")
+    _, wd = strided(w, dtype, odd, 8)
+    offd, idxd = off.cuda(), idx.cuda()
+    xz = torch.cat([x, torch.zeros((1, K), dtype=torch.float64)])     # a bad index: zeros
+    src[bad] = xr
+    ref_y, ref_dx, ref_dw = plain_mm(xz, w, off, src)[0], plain_dgrad(dy, w, off)[0], plain_wgrad(dy, xz, off, src)[0]
+    inner = slice(lead, lead + grouped)
+    for pad in (8, 3):
+        yw, y = strided(torch.zeros((rows, N)), out, pad, 8, 7.0)
+        y.fill_(7.0)
+        exm.grouped_mm(xd, wd, offd, row_index=idxd, row_div=2, out_dtype=out, y=y)
+        equal(y[inner], ref_y[inner], "mm")
+        y[inner] = 7.0
+        assert bool((yw == 7).all()), "mm wrote outside its rows or columns"
+        dxw, dx = strided(torch.zeros((rows, K)), out, pad, 8, 7.0)
+        dx.fill_(7.0)
+        exm.grouped_mm_dgrad(dyd, wd, offd, out_dtype=out, dx=dx)
+        equal(dx[inner], ref_dx[inner], "dgrad")
+        dx[inner] = 7.0
+        assert bool((dxw == 7).all()), "dgrad wrote outside its rows or columns"
+        dww, dw = strided(torch.zeros((E, N, K)), out, pad, 8, 7.0)
+        exm.grouped_mm_wgrad(dyd, xd, offd, row_index=idxd, row_div=2, out_dtype=out, dw=dw)
+        equal(dw, ref_dw, "wgrad")
+        dw.fill_(7.0)
+        assert bool((dww == 7).all()), "wgrad wrote outside its columns"
+
+
+@gpu
+@pytest.mark.parametrize("counts,N,K", [([100, 0, 37, 203], 200, 264), ([130, 1, 1000, 601], 136, 904), ([200, 0, 192], 41, 77),
+                                        ([2, 4198], 72, 4104)])
+def test_token_gradients_of_every_form(counts, N, K):
+    """The gradient of x summed per token (k = 4), with ungrouped rows and an index outside."""
+    print(f"token gradients counts={counts} N={N} K={K}", flush=True)
+    gen = torch.Generator().manual_seed(K)
+    rows, E, k = sum(counts), len(counts), 4
+    off = offsets_of(counts)
+    off[-1] -= 1                                                       # the last row is ungrouped
+    w, dy = whole(gen, (E, N, K), -1, 2), whole(gen, (rows, N), -1, 2)
+    f2s = torch.randperm(rows, generator=gen).to(torch.int32)
+    f2s[5] = rows
+    dyd = cuda(dy, BF16)
+    dyd[-1] = float("nan")
+    got = exm.grouped_mm_dgrad(dyd, cuda(w, BF16), off.cuda(), flat_to_sorted=f2s.cuda(), k=k, out_dtype=FP32)
+    per_row = torch.cat([plain_dgrad(dy, w, off)[0], torch.zeros((1, K), dtype=torch.float64)])
+    equal(got, per_row[f2s.long()].view(-1, k, K).sum(1), "dgrad")
+
+
+@gpu
+def test_no_rows_and_no_routing():
+    """No rows at all: nothing is written but the zeros of a gradient of W; a routing that gives
+    every row to nobody does the same."""
+    w, off = torch.ones((2, 40, 72), dtype=BF16, device="cuda"), torch.zeros(3, dtype=torch.int32, device="cuda")
+    none, some = torch.empty((0, 72), dtype=BF16, device="cuda"), torch.ones((50, 72), dtype=BF16, device="cuda")
+    assert exm.grouped_mm(none, w, off).shape == (0, 40)
+    assert exm.grouped_mm_dgrad(none[:, :40], w, off).shape == (0, 72)
+    for x in (none, some):
+        dy = torch.full((len(x), 40), float("nan"), dtype=BF16, device="cuda")
+        dw = torch.full((2, 40, 72), 5.0, device="cuda")
+        exm.grouped_mm_wgrad(dy, x, off, dw=dw)
+        assert bool((dw == 0).all())
+    y = torch.full((50, 40), 5.0, dtype=BF16, device="cuda")
+    exm.grouped_mm(some, w, off, y=y)
+    assert bool((y == 5).all())
+    dx = exm.grouped_mm_dgrad(y, w, off, flat_to_sorted=torch.arange(50, dtype=torch.int32, device="cuda"), k=5)
+    assert dx.shape == (10, 72) and bool((dx == 0).all())
+
+
+@gpu
+def test_two_calls_at_once():
+    """Two streams, each with outputs and a workspace of its own, at the same time."""
+    gen = torch.Generator().manual_seed(12)
+    T, k, E, N, K = 150, 4, 6, 131, 203
+    ids, off, order, f2s = routed(gen, T, k, E)
+    x, w, dy = torch.randn((T, K), generator=gen), torch.randn((E, N, K), generator=gen), torch.randn((T * k, N), generator=gen)
+    xd, wd, dyd, offd, sf, fs = cuda(x, BF16), cuda(w, BF16), cuda(dy, BF16), off.cuda(), order.cuda(), f2s.cuda()
+    need = max(exm.grouped_mm_workspace_bytes(op, T * k, N, K, E, k) for op in range(3))
+
+    def run(scale, ws):
+        return (exm.grouped_mm(xd * scale, wd, offd, row_index=sf, row_div=k, workspace=ws),
+                exm.grouped_mm_dgrad(dyd * scale, wd, offd, flat_to_sorted=fs, k=k, workspace=ws),
+                exm.grouped_mm_wgrad(dyd * scale, xd, offd, row_index=sf, row_div=k, workspace=ws))
+
+    spaces = [exm.alloc_workspace(need) for _ in range(2)]
+    want = [[t.clone() for t in run(s, spaces[0])] for s in (1.0, 2.0)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[], []]
+    for _ in range(8):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(run(float(i + 1), spaces[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for out in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(out, want[i]))
 
 
 @gpu

@@ -95,6 +95,8 @@ def test_refusals():
     assert _call(wsb=need - 1) == exm.ERR_WORKSPACE and str(need) in exm.last_error()
     assert _call(ws=None) == exm.ERR_WORKSPACE
     assert _call(T=0) == exm.OK
+    for far in (dict(ldx=(1 << 24) + 8), dict(ldw=(1 << 24) + 8), dict(lda=(1 << 24) + 8, a_stride=1 << 30)):
+        assert _call(**far) == exm.ERR_UNSUPPORTED, far
     assert _call(T=1 << 22, N=1 << 20, ldy=1 << 20, b_stride=1 << 24) == exm.ERR_UNSUPPORTED
     assert exm.lora_workspace_bytes(4, 32, 60, 3, 16) == 0
 
@@ -135,6 +137,86 @@ def test_against_fp64(T, N, K, L, R, dtype):
     close(y, ref, bound, "added to y")
     none = (ids < 0) | (ranks[ids.clamp(min=0)] == 0)
     assert torch.equal(y.cpu()[none].double(), y0[none]), "a token without an adapter changed"
+
+
+# (T, N, K): 16 x 16 blocks, 64 x 64 blocks, 128 x 128 and 256 x 256 tiles, all ragged
+FORMS = [(70, 200, 136), (150, 2604, 136), (601, 3804, 72), (4100, 4004, 64)]
+
+
+@gpu
+@pytest.mark.parametrize("order", ["one", "runs", "mixed", "distinct"])
+@pytest.mark.parametrize("rank", [5, 16, 72, 128])
+@pytest.mark.parametrize("T,N,K", FORMS)
+def test_every_form(T, N, K, rank, order):
+    """Token orders and ranks on every form, operands inside wider tensors of NaN."""
+    print(f"lora forms T={T} N={N} K={K} rank={rank} order={order}", flush=True)
+    gen = torch.Generator().manual_seed(rank)
+    L, R = 24, (rank + 7) // 8 * 8
+    x, w = whole(gen, (T, K), -1, 2), whole(gen, (N, K), -1, 2)
+    a, b = whole(gen, (L, R, K), -1, 2), whole(gen, (L, N, R), -1, 2)
+    ids = {"one": torch.full((T,), 3), "runs": torch.arange(T) // 21 % (L + 2) - 1,
+           "mixed": torch.randint(-1, 4, (T,), generator=gen), "distinct": torch.arange(T) % L}[order]
+    ranks = torch.full((L,), rank)
+    ranks[1::5] = torch.tensor([0, 1, R, min(R, 17), 3])
+    an, bn = a.clone(), b.clone()
+    for i in range(L):
+        an[i, ranks[i]:], bn[i, :, ranks[i]:] = float("nan"), float("nan")
+    xw = torch.full((T, K + 24), float("nan"), dtype=BF16, device="cuda")
+    xd = xw[:, 8:8 + K]
+    xd.copy_(x)
+    ww = torch.full((N, K + 8), float("nan"), dtype=BF16, device="cuda")
+    ww[:, :K].copy_(w)
+    bank = exm.LoraBank(an.to(BF16).cuda(), bn.to(BF16).cuda(), ranks=ranks.to(torch.int32).cuda())
+    idd = ids.to(torch.int32).cuda()
+    base, add = x @ w.t(), torch.zeros((T, N), dtype=torch.float64)
+    for i in range(L):
+        rows = ids == i
+        if bool(rows.any()) and int(ranks[i]):
+            r = int(ranks[i])
+            add[rows] = (x[rows] @ a[i, :r].t()) @ b[i, :, :r].t()
+    for pad in (8, 3):
+        yw = torch.full((T + 2, N + pad), 9.0, dtype=BF16, device="cuda")
+        y = yw[1:T + 1, pad // 2:pad // 2 + N]
+        exm.lora_linear(xd, ww[:, :K], bank, idd, y=y)
+        assert torch.equal(y.cpu(), (base + add).to(BF16)), "with w"
+        y.copy_(base)
+        y0 = y.cpu().double()
+        exm.lora_linear(xd, None, bank, idd, y=y)
+        assert torch.equal(y.cpu(), (y0 + add).to(BF16)), "added to y"
+        y.fill_(9.0)
+        assert bool((yw == 9).all()), "wrote outside its rows or columns"
+
+
+@gpu
+@pytest.mark.parametrize("T,N,K", [(150, 2604, 520), (601, 3804, 136), (1030, 2064, 1000)])
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+def test_long_batches_against_fp64(T, N, K, dtype):
+    print(f"lora long T={T} N={N} K={K} {dtype}", flush=True)
+    gen = torch.Generator().manual_seed(T)
+    L, R = 7, 40
+    x, w = normal(gen, (T, K), dtype), normal(gen, (N, K), dtype, 0.1)
+    a, b = normal(gen, (L, R, K), dtype, 0.1), normal(gen, (L, N, R), dtype, 0.1)
+    ranks, scales = torch.tensor([40, 0, 8, 33, 16, 24, 7]), torch.rand(L, generator=gen) * 3 - 1
+    ids = torch.randint(-1, L, (T,), generator=gen)
+    y = exm.lora_linear(x.to(dtype).cuda(), w.to(dtype).cuda(), device_bank(a, b, ranks, scales, dtype), ids.to(torch.int32).cuda())
+    close(y, *plain(x, w, a, b, ids, ranks, scales.float().double()), "with w")
+
+
+@gpu
+def test_rows_far_apart():
+    """Row strides of 2^24 elements, where no 32-bit offset spans the tokens."""
+    gen = torch.Generator().manual_seed(3)
+    T, N, K, L, R, ld = 101, 4 * 1664, 64, 3, 16, 1 << 24
+    x, w = whole(gen, (T, K), -1, 2), whole(gen, (N, K), -1, 2)
+    a, b = whole(gen, (L, R, K), -1, 2), whole(gen, (L, N, R), -1, 2)
+    ids = torch.arange(T) % (L + 1) - 1
+    xd = torch.empty((T - 1) * ld + K, dtype=BF16, device="cuda").as_strided((T, K), (ld, 1))
+    xd.copy_(x)
+    ref, _ = plain(x, w, a, b, ids, torch.full((L,), R), torch.ones(L))
+    for n in (N, 1000):       # 64 x 64 and 16 x 16 blocks
+        bank = exm.LoraBank(a.to(BF16).cuda(), b[:, :n].contiguous().to(BF16).cuda())
+        y = exm.lora_linear(xd, w[:n].to(BF16).cuda(), bank, ids.to(torch.int32).cuda())
+        assert torch.equal(y.cpu(), ref[:, :n].to(BF16))
 
 
 @gpu

@@ -305,27 +305,28 @@ __device__ __forceinline__ void skinny_product_any(const uint16_t* __restrict__ 
   }
 }
 
-// Sum over the waves in wave order: part [NW][TQ TP][64] in LDS; block b (= j TP + i) of the
-// sums ends in wave b (b < NW).
+// Sum over the waves in wave order: part [NW][TQ TP][64] in LDS. Wave w < TP gets those of
+// row block w, v[j] of column block j.
 template <int TP, int TQ, int NW>
-__device__ __forceinline__ f32x4 skinny_reduce(f32x4 (*part)[TQ * TP][64], const f32x4 (&acc)[TQ][TP], int wave, int lane) {
-  static_assert(TQ * TP <= NW, "a wave per block of sums");
+__device__ __forceinline__ void skinny_reduce(f32x4 (*part)[TQ * TP][64], const f32x4 (&acc)[TQ][TP], int wave, int lane,
+                                              f32x4 (&v)[TQ]) {
+  static_assert(TP <= NW, "a wave per row block");
 #pragma unroll
   for (int j = 0; j < TQ; j++)
 #pragma unroll
     for (int i = 0; i < TP; i++) part[wave][j * TP + i][lane] = acc[j][i];
   __syncthreads();
-  f32x4 v = {0.f, 0.f, 0.f, 0.f};
-  if (wave < TQ * TP) {
-    v = part[0][wave][lane];
+  if (wave >= TP) return;
+#pragma unroll
+  for (int j = 0; j < TQ; j++) {
+    v[j] = part[0][j * TP + wave][lane];
 #pragma unroll
     for (int w = 1; w < NW; w++) {
-      const f32x4 q = part[w][wave][lane];
+      const f32x4 q = part[w][j * TP + wave][lane];
 #pragma unroll
-      for (int e = 0; e < 4; e++) v[e] += q[e];
+      for (int e = 0; e < 4; e++) v[j][e] += q[e];
     }
   }
-  return v;
 }
 
 // Workgroup b of a launch of n runs on XCD b % 8 (round-robin dispatch). This gives each

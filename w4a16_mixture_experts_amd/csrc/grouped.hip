@@ -378,17 +378,18 @@ __global__ __launch_bounds__(64 * WP * WQ, OCC) void grouped_wide_kernel(Grouped
       [](int, int, auto&) {}, [&](int p) { return MODE == kWG ? p : t.seg0 + p; });
 }
 
-// The forward product for few rows per expert: 16 TP rows x 16 columns per workgroup, the
-// waves split K and W streams through once (gemm_wide.h, narrow_product). Bound by reading W.
-template <class ET, int TP, int NW, int D, bool ALIGNED>
+// The forward product for few rows per expert, or few tiles: 16 TP rows x 16 TQ columns per
+// workgroup, the waves split K (gemm_wide.h, narrow_product). TP = TQ = 1 is bound by reading
+// W, which streams through once; 4 x 4 blocks shorten the loop of small products.
+template <class ET, int TP, int TQ, int NW, int D, bool ALIGNED>
 __global__ __launch_bounds__(64 * NW) void grouped_narrow_kernel(GroupedArgs a, int q_tiles) {
-  constexpr int kPart = ALIGNED ? 16 * (TP + 1) * D : TP * 64 * 8;   // (elements; the sums at least)
-  __shared__ __attribute__((aligned(16))) uint16_t s_a[NW][kPart], s_b[NW][ALIGNED ? kPart : 8];
-  static_assert(sizeof(f32x4) * TP * 64 <= sizeof(s_a[0]), "the sums fit into the slices' part");
+  constexpr int kPart = ALIGNED ? 16 * (TP + TQ) * D : TP * TQ * 64 * 4;   // (elements; the sums at least)
+  __shared__ __attribute__((aligned(16))) uint16_t s_a[2][NW][kPart];        // two slices a wave
+  static_assert(sizeof(f32x4) * TP * TQ * 64 * NW <= sizeof(s_a), "the sums fit into the slices' part");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   RowTile r;
   if (!resolve_rows<16 * TP, 16>(a.offsets, a.rows, a.E, q_tiles, blockIdx.x, r)) return;
-  const int n0 = 16 * r.qt, n = n0 + (lane & 15);
+  const int n0 = 16 * TQ * r.qt;
   const uint32_t dmul = 0xFFFFFFFFu / (uint32_t)a.row_div;
   // row i of the tile: its row of x, or -1
   auto source = [&](int i) {
@@ -401,54 +402,65 @@ __global__ __launch_bounds__(64 * NW) void grouped_narrow_kernel(GroupedArgs a, 
     }
     return s < a.x_rows ? s : -1;
   };
-  f32x4 acc[1][TP];
+  f32x4 acc[TQ][TP];
 #pragma unroll
-  for (int i = 0; i < TP; i++) acc[0][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int j = 0; j < TQ; j++)
+#pragma unroll
+    for (int i = 0; i < TP; i++) acc[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
   const uint16_t* w = a.b + (size_t)r.e * a.b_stride;
   if constexpr (ALIGNED) {
-    NarrowRows<16 * TP, D> op_x;
-    NarrowRows<16, D> op_w;
-    op_w.init(make_buf(w + (size_t)n0 * a.ldb, 2 * ((size_t)(min(16, a.N - n0) - 1) * a.ldb + a.K)), a.K, lane,
+    using OpX = NarrowRows<16 * TP, D>;
+    using OpW = NarrowRows<16 * TQ, D>;
+    OpX op_x;
+    OpW op_w;
+    op_w.init(make_buf(w + (size_t)n0 * a.ldb, 2 * ((size_t)(min(16 * TQ, a.N - n0) - 1) * a.ldb + a.len_b)), a.K, lane,
               [&](int i) { return n0 + i < a.N ? (uint32_t)(i * a.ldb * 2) : kNowhere; });
-    op_x.init(make_buf(a.a, 2 * ((size_t)(a.x_rows - 1) * a.lda + a.K)), a.K, lane, [&](int i) {
+    op_x.init(make_buf(a.a, 2 * ((size_t)(a.x_rows - 1) * a.lda + a.len_a)), a.K, lane, [&](int i) {
       const int s = source(i);
       return s < 0 ? kNowhere : (uint32_t)((size_t)s * a.lda * 2);
     });
-    narrow_product<ET, TP, 1, NW, D>(op_x, op_w, a.K, wave, lane, s_a[wave], s_b[wave], acc);
+    narrow_product<ET, TP, TQ, NW, D>(op_x, op_w, a.K, wave, lane, s_a[0][wave], s_a[1][wave], acc);
   } else {
-    size_t xrow[TP];
-    const size_t wrow[1] = {(size_t)(n < a.N ? n : a.N - 1) * a.ldb};
+    size_t xrow[TP], wrow[TQ];
     bool zero[TP];
+#pragma unroll
+    for (int j = 0; j < TQ; j++) wrow[j] = (size_t)min(n0 + 16 * j + (lane & 15), a.N - 1) * a.ldb;
 #pragma unroll
     for (int i = 0; i < TP; i++) {
       const int s = source(16 * i + (lane & 15));
       zero[i] = s < 0;
       xrow[i] = zero[i] ? 0 : (size_t)s * a.lda;
     }
-    skinny_product_any<ET, TP, 1, NW>(a.a, xrow, w, wrow, a.K, wave, lane, acc);
+    skinny_product_any<ET, TP, TQ, NW>(a.a, xrow, w, wrow, a.K, wave, lane, acc);
 #pragma unroll
     for (int i = 0; i < TP; i++)
-      if (zero[i]) acc[0][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < TQ; j++)
+        if (zero[i]) acc[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
   __syncthreads();
-  const f32x4 v = skinny_reduce<TP, 1, NW>(reinterpret_cast<f32x4(*)[TP][64]>(&s_a[0][0]), acc, wave, lane);
-  const int p = r.p0 + 16 * wave + (lane & 15), q = n0 + 4 * (lane >> 4);
-  if (wave < TP && p < r.p1 && q < a.N)
-    store4<ET>(a.out, (size_t)(r.seg0 + p) * a.ldo + q, a.out_f32, a.vec, a.N - q, v);
+  f32x4 v[TQ];
+  skinny_reduce<TP, TQ, NW>(reinterpret_cast<f32x4(*)[TQ * TP][64]>(&s_a[0][0][0]), acc, wave, lane, v);
+  const int p = r.p0 + 16 * wave + (lane & 15);
+  if (wave >= TP || p >= r.p1) return;
+#pragma unroll
+  for (int j = 0; j < TQ; j++) {
+    const int q = n0 + 16 * j + 4 * (lane >> 4);
+    if (q < a.N) store4<ET>(a.out, (size_t)(r.seg0 + p) * a.ldo + q, a.out_f32, a.vec, a.N - q, v[j]);
+  }
 }
 
-// The gradient of x for few rows per expert: 16 rows x 64 columns per workgroup, the waves
-// split N and W streams through once.
-template <class ET, int NW>
+// The gradient of x in the same way: 16 TP rows x 64 columns per workgroup, the waves split N.
+template <class ET, int TP, int NW>
 __global__ __launch_bounds__(64 * NW) void grouped_narrow_dgrad_kernel(GroupedArgs a, int q_tiles) {
-  constexpr int D = 32;
-  using OpX = NarrowRows<16, D>;
+  constexpr int D = 32, kPart = 16 * TP * D + 64 * D;
+  using OpX = NarrowRows<16 * TP, D>;
   using OpW = NarrowCols<D>;
-  __shared__ __attribute__((aligned(16))) uint16_t s_a[NW][OpX::kElems + OpW::kElems], s_b[NW][OpX::kElems + OpW::kElems];
-  static_assert(sizeof(f32x4) * 4 * 64 <= sizeof(s_a[0]), "the sums fit into the slices' part");
+  __shared__ __attribute__((aligned(16))) uint16_t s_a[2][NW][kPart];   // two slices a wave
+  static_assert(sizeof(f32x4) * TP * 4 * 64 * NW <= sizeof(s_a), "the sums fit into the slices' part");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   RowTile r;
-  if (!resolve_rows<16, 16>(a.offsets, a.rows, a.E, q_tiles, blockIdx.x, r)) return;
+  if (!resolve_rows<16 * TP, 16>(a.offsets, a.rows, a.E, q_tiles, blockIdx.x, r)) return;
   const int q0 = 64 * r.qt, p0 = r.seg0 + r.p0, cnt = r.p1 - r.p0;
   OpX op_x;
   OpW op_w;
@@ -456,15 +468,22 @@ __global__ __launch_bounds__(64 * NW) void grouped_narrow_dgrad_kernel(GroupedAr
             2 * (uint32_t)a.ldb, a.N, a.len_b - q0, lane);
   op_x.init(make_buf(a.a + (size_t)p0 * a.lda, 2 * ((size_t)(cnt - 1) * a.lda + a.len_a)), a.N, lane,
             [&](int i) { return i < cnt ? (uint32_t)(i * a.lda * 2) : kNowhere; });
-  f32x4 acc[4][1];
+  f32x4 acc[4][TP];
 #pragma unroll
-  for (int j = 0; j < 4; j++) acc[j][0] = f32x4{0.f, 0.f, 0.f, 0.f};
-  narrow_product<ET, 1, 4, NW, D>(op_x, op_w, a.N, wave, lane, s_a[wave], s_b[wave], acc);
+  for (int j = 0; j < 4; j++)
+#pragma unroll
+    for (int i = 0; i < TP; i++) acc[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  narrow_product<ET, TP, 4, NW, D>(op_x, op_w, a.N, wave, lane, s_a[0][wave], s_a[1][wave], acc);
   __syncthreads();
-  const f32x4 v = skinny_reduce<1, 4, NW>(reinterpret_cast<f32x4(*)[4][64]>(&s_a[0][0]), acc, wave, lane);
-  const int q = q0 + 16 * wave + 4 * (lane >> 4);
-  if (wave < 4 && (lane & 15) < cnt && q < a.K)
-    store4<ET>(a.out, (size_t)(p0 + (lane & 15)) * a.ldo + q, a.out_f32, a.vec, a.K - q, v);
+  f32x4 v[4];
+  skinny_reduce<TP, 4, NW>(reinterpret_cast<f32x4(*)[4 * TP][64]>(&s_a[0][0][0]), acc, wave, lane, v);
+  const int p = 16 * wave + (lane & 15);
+  if (wave >= TP || p >= cnt) return;
+#pragma unroll
+  for (int j = 0; j < 4; j++) {
+    const int q = q0 + 16 * j + 4 * (lane >> 4);
+    if (q < a.K) store4<ET>(a.out, (size_t)(p0 + p) * a.ldo + q, a.out_f32, a.vec, a.K - q, v[j]);
+  }
 }
 
 // dx[t, :] = sum_j rows[flat_to_sorted[t k + j], :] in slot order, rounded once. Entries
@@ -580,7 +599,7 @@ constexpr int kNarrowRowsAny = 128;   // see kNarrowRows
 
 // Operands whose rows are no multiple of 16 bytes long are copied with padded rows first, so
 // that the products run on their aligned forms (one pass over the operand against loads
-// through registers in the product: gradient of x, 1384 rows, N = 7827, K = 384: XX -> YY us).
+// through registers in the product: gradient of x, 1384 rows, N = 7827, K = 384: 510 -> 94 us).
 // Not for the forward product's few rows per expert, which have a form of their own.
 GroupedWorkspace grouped_workspace(int op, int rows, int N, int K, int E, int k) {
   GroupedWorkspace w{0, 0, 0};
@@ -652,27 +671,23 @@ static bool large_tiles(int rows, int Q, int E) {
   return rows / E >= 256 && (long long)(rows / 256) * ceil_div(Q, 256) >= 256;
 }
 
-template <class ET, int TP, int NW, int D, bool ALIGNED>
+template <class ET, int TP, int TQ, int NW, int D, bool ALIGNED>
 static hipError_t launch_narrow(const GroupedArgs& a, hipStream_t s) {
   const long long max_p = a.rows / (16 * TP) + (a.E < a.rows ? a.E : a.rows);
-  const int qt = ceil_div(a.N, 16);
+  const int qt = ceil_div(a.N, 16 * TQ);
   if (max_p * qt * (64 * NW) > kMaxThreads) return hipErrorInvalidConfiguration;
   ProfScope prof("grouped_mm", s);
-  EXMOE_LAUNCH(prof, (grouped_narrow_kernel<ET, TP, NW, D, ALIGNED>), dim3((unsigned)(max_p * qt)), dim3(64 * NW), 0, s, a, qt);
+  EXMOE_LAUNCH(prof, (grouped_narrow_kernel<ET, TP, TQ, NW, D, ALIGNED>), dim3((unsigned)(max_p * qt)), dim3(64 * NW), 0, s, a, qt);
   return hipGetLastError();
 }
 
-// Rows per expert up to which the forward product runs on 16-row blocks (narrow) instead of
-// 128-row tiles. Measured on 64 experts of 2048 x 2048, us: 2 rows per expert 83 / 117,
-// 8 rows 97 / 128, 16 rows 127 / 130. Operands of any alignment, 13 experts of 517 x 1003: 10
-// rows 11 / 39, 39 rows 21 / 42, 60 rows 28 / 44, 630 rows 193 / 61.
-template <class ET, int NW>
+template <class ET, int TP, int NW>
 static hipError_t launch_narrow_dgrad(const GroupedArgs& a, hipStream_t s) {
-  const long long max_p = a.rows / 16 + (a.E < a.rows ? a.E : a.rows);
+  const long long max_p = a.rows / (16 * TP) + (a.E < a.rows ? a.E : a.rows);
   const int qt = ceil_div(a.K, 64);
   if (max_p * qt * (64 * NW) > kMaxThreads) return hipErrorInvalidConfiguration;
   ProfScope prof("grouped_dgrad", s);
-  EXMOE_LAUNCH(prof, (grouped_narrow_dgrad_kernel<ET, NW>), dim3((unsigned)(max_p * qt)), dim3(64 * NW), 0, s, a, qt);
+  EXMOE_LAUNCH(prof, (grouped_narrow_dgrad_kernel<ET, TP, NW>), dim3((unsigned)(max_p * qt)), dim3(64 * NW), 0, s, a, qt);
   return hipGetLastError();
 }
 
@@ -689,17 +704,25 @@ static bool narrow_dgrad(const GroupedArgs& a) {
 // of 517 x 1003: 10 rows 11 / 39, 39 rows 21 / 42, 60 rows 28 / 44, 630 rows 193 / 61.
 constexpr int kNarrowRows = 16;
 
+// Fewer 128 x 128 tiles than half the CUs: 64 x 64 blocks whose waves split the reduction (500
+// rows, E = 4, N = 1024, K = 2048: 25.5 -> 14.7 us, the gradient of x of 1000 rows, N = 2048,
+// K = 384 28.0 -> 18.6 us; with 154 and 207 tiles 21.3 -> 20.2 and 33.8 -> 37.7 us).
+static bool few_tiles(int rows, int Q, int E) {
+  return (rows / 128 + (long long)(E < rows ? E : rows)) * ceil_div(Q, 128) < 128;
+}
+
 template <class ET>
 static hipError_t mm_type(const GroupedArgs& a, hipStream_t s) {
   const bool al = op_aligned(a.a, a.lda, 0, a.len_a) && op_aligned(a.b, a.ldb, a.b_stride, a.len_b);
   if (!al) {
-    if (a.rows <= kNarrowRowsAny * (long long)a.E) return launch_narrow<ET, 1, 8, 64, false>(a, s);
+    if (a.rows <= kNarrowRowsAny * (long long)a.E) return launch_narrow<ET, 1, 1, 8, 64, false>(a, s);
     return launch_rows<ET, kMM, 128, 128, 2, 2, false>(a, "grouped_mm", s);
   }
   if (a.rows <= kNarrowRows * (long long)a.E && op_span(a.x_rows, a.lda, a.K) && op_span(16, a.ldb, a.K))
-    return launch_narrow<ET, 1, 4, 64, true>(a, s);
+    return launch_narrow<ET, 1, 1, 4, 64, true>(a, s);
   if (!op_span(a.x_rows, a.lda, a.len_a) || !op_span(a.N, a.ldb, a.len_b))
     return launch_rows<ET, kMM, 128, 128, 2, 2, true>(a, "grouped_mm", s);
+  if (few_tiles(a.rows, a.N, a.E)) return launch_narrow<ET, 4, 4, 4, 32, true>(a, s);
   if (large_tiles(a.rows, a.N, a.E)) return launch_wide<ET, kMM, 4, 2, 2, 4, 64, 2>(a, "grouped_mm", s);
   return launch_wide<ET, kMM, 2, 2, 2, 2, 64, 2>(a, "grouped_mm", s);
 }
@@ -721,9 +744,16 @@ static hipError_t pack_weights(GroupedArgs& a, hipStream_t s) {
   return e;
 }
 
+// Whether the products after the copies fit into a launch (checked before anything runs).
+static bool packed_fits(const GroupedArgs& a, int Q) {
+  return (a.rows / 128 + (long long)(a.E < a.rows ? a.E : a.rows)) * ceil_div(Q, 128) * 256 <= kMaxThreads &&
+         (!a.flat_to_sorted || (long long)(a.rows / a.k) * a.K <= kMaxThreads);
+}
+
 hipError_t launch_grouped_mm(const GroupedArgs& given, hipStream_t s) {
   GroupedArgs a = given;
   hipError_t e = hipSuccess;
+  if ((a.pack_a || a.pack_b) && !packed_fits(a, a.N)) return hipErrorInvalidConfiguration;
   if (a.pack_a) {
     if ((e = pack_a_rows(a, a.K, true, s)) != hipSuccess) return e;
     a.x_rows = a.rows;
@@ -749,7 +779,8 @@ static hipError_t dgrad_type(const GroupedArgs& a, hipStream_t s) {
   if (!al) e = launch_rows<ET, kDG, 128, 128, 2, 2, false>(r, "grouped_dgrad", s);
   else if (!op_span(a.rows, a.lda, a.len_a) || !op_span(a.N, a.ldb, a.len_b))
     e = launch_rows<ET, kDG, 128, 128, 2, 2, true>(r, "grouped_dgrad", s);
-  else if (narrow_dgrad(a)) e = launch_narrow_dgrad<ET, 8>(r, s);
+  else if (narrow_dgrad(a)) e = launch_narrow_dgrad<ET, 1, 8>(r, s);
+  else if (few_tiles(a.rows, a.K, a.E)) e = launch_narrow_dgrad<ET, 4, 4>(r, s);
   else if (large_tiles(a.rows, a.K, a.E)) e = launch_wide<ET, kDG, 4, 2, 2, 4, 64, 2>(r, "grouped_dgrad", s);
   else e = launch_wide<ET, kDG, 2, 2, 2, 2, 64, 2>(r, "grouped_dgrad", s);
   if (e != hipSuccess || !a.flat_to_sorted) return e;
@@ -770,6 +801,7 @@ static hipError_t dgrad_type(const GroupedArgs& a, hipStream_t s) {
 hipError_t launch_grouped_dgrad(const GroupedArgs& given, hipStream_t s) {
   GroupedArgs a = given;
   hipError_t e = hipSuccess;
+  if ((a.pack_a || a.pack_b) && !packed_fits(a, a.K)) return hipErrorInvalidConfiguration;
   if (a.pack_a && (e = pack_a_rows(a, a.N, false, s)) != hipSuccess) return e;
   if (a.pack_b && (e = pack_weights(a, s)) != hipSuccess) return e;
   return a.fp16 ? dgrad_type<ElemFP16>(a, s) : dgrad_type<ElemBF16>(a, s);
@@ -820,6 +852,8 @@ static hipError_t wgrad_type(const GroupedArgs& a, hipStream_t s) {
 hipError_t launch_grouped_wgrad(const GroupedArgs& given, hipStream_t s) {
   GroupedArgs a = given;
   hipError_t e = hipSuccess;
+  if ((a.pack_a || a.pack_b) && (long long)a.E * ceil_div(a.N, 128) * ceil_div(a.K, 128) * wgrad_splits(a.rows, a.N, a.K, a.E) * 256 > kMaxThreads)
+    return hipErrorInvalidConfiguration;
   if (a.rows > 0 && a.pack_a && (e = pack_a_rows(a, a.N, false, s)) != hipSuccess) return e;
   if (a.rows > 0 && a.pack_b) {
     e = pack_rows(a.b, a.ldb, 0, a.K, a.rows, 1, a.x_rows, a.row_index, a.row_div, nullptr, a.pack_b, s);

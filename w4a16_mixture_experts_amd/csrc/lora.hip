@@ -204,6 +204,65 @@ struct ExpandBlock {
   }
 };
 
+// The same by one wave for TQ blocks of 16 columns: kBatch (adapter, 16 ranks) pairs at a time,
+// whose loads run together; the first of them are issued before the pass over W.
+template <class ET, int TQ>
+struct ExpandWave {
+  static constexpr int kBatch = 4;
+  int id, y;
+  size_t group;
+  uint32_t left;
+  int ad, rank, next;        // the walk: ranks from `next` on of adapter `ad`
+  int got[kBatch];           // adapter of each pair, or -1
+  bf16x8 bv[kBatch][TQ], vv[kBatch];
+  float mul[kBatch];
+
+  __device__ __forceinline__ void start(const LoraArgs& a, int t0, int lane) {
+    const int t = t0 + (lane & 15);
+    const int2 info = t < a.T ? a.info[t] : make_int2(-1, 0);
+    id = info.x;
+    y = info.y;
+    group = (size_t)min(t0 / 16, (a.T - 1) / 16) * a.rank_blocks;
+    left = (uint32_t)__ballot(info.y > 0) & 0xFFFFu;
+    ad = rank = next = 0;
+  }
+  __device__ __forceinline__ void load(const LoraArgs& a, int n0, int lane) {
+#pragma unroll
+    for (int u = 0; u < kBatch; u++) {
+      if (next >= rank && left) {
+        const int lead = __ffs((int)left) - 1;
+        ad = __builtin_amdgcn_readlane(id, lead);
+        rank = __builtin_amdgcn_readlane(y, lead);
+        left &= ~(uint32_t)__ballot(id == ad);
+        next = 0;
+      }
+      const bool have = next < rank;
+      got[u] = have ? ad : -1;
+      const size_t blk = group + (have ? next / 16 : 0);
+#pragma unroll
+      for (int j = 0; j < TQ; j++)
+        bv[u][j] = load_b(a, have ? ad : 0, have ? rank : 0, n0 + 16 * j + (lane & 15), next + 8 * ((lane >> 4) & 1));
+      vv[u] = *reinterpret_cast<const bf16x8*>(a.hl + 512 * blk + 8 * lane);   // (tokens of other adapters: dropped)
+      mul[u] = a.mul[16 * blk + (lane & 15)];
+      next += 16;
+    }
+  }
+  __device__ __forceinline__ bool more() const { return left || next < rank; }
+  __device__ __forceinline__ void add(f32x4 (&acc)[TQ]) {
+#pragma unroll
+    for (int u = 0; u < kBatch; u++) {
+#pragma unroll
+      for (int j = 0; j < TQ; j++) {
+        const f32x4 d = ET::mfma(bv[u][j], vv[u], f32x4{0.f, 0.f, 0.f, 0.f});
+        if (got[u] >= 0 && id == got[u]) {
+#pragma unroll
+          for (int q = 0; q < 4; q++) acc[j][q] += mul[u] * d[q];
+        }
+      }
+    }
+  }
+};
+
 // The same for a block of 32 tokens and TQ blocks of 32 columns on 32 x 32 x 16 MFMA: two per
 // adapter and 16 ranks (8 ranks each: hi in lanes 0..31, lo in lanes 32..63).
 template <class ET, int TQ, int TP>
@@ -298,8 +357,50 @@ __global__ __launch_bounds__(64 * NW) void lora_skinny_kernel(LoraArgs a) {
 #pragma unroll
   for (int i = 0; i < TP; i++) part[i].add(a, n0, lane, acc[0][i]);
   __syncthreads();
-  const f32x4 v = skinny_reduce<TP, 1, NW>(reinterpret_cast<f32x4(*)[TP][64]>(&s_a[0][0]), acc, wave, lane);
-  if (wave < TP) lora_store<ET>(a, t0 + 16 * wave + (lane & 15), n0 + 4 * (lane >> 4), v);
+  f32x4 v[1];
+  skinny_reduce<TP, 1, NW>(reinterpret_cast<f32x4(*)[TP][64]>(&s_a[0][0]), acc, wave, lane, v);
+  if (wave < TP) lora_store<ET>(a, t0 + 16 * wave + (lane & 15), n0 + 4 * (lane >> 4), v[0]);
+}
+
+// More tokens, still too few for the pipelined tiles: 64 tokens x 64 columns per workgroup,
+// the waves split K and the rank blocks of the adapters.
+template <class ET>
+__global__ __launch_bounds__(256) void lora_mid_kernel(LoraArgs a, int t_tiles) {
+  constexpr int TP = 4, TQ = 4, NW = 4, D = 64, kPart = 16 * (TP + TQ) * D;
+  __shared__ __attribute__((aligned(16))) uint16_t s_a[2][NW][kPart];   // two slices a wave
+  static_assert(sizeof(f32x4) * TP * TQ * 64 * NW <= sizeof(s_a), "the sums fit into the slices' part");
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // (the blocks of one column block on one XCD: W is read into one L2)
+  const int idx = xcd_contiguous(blockIdx.x, gridDim.x);
+  const int n0 = idx / t_tiles * 16 * TQ, t0 = idx % t_tiles * 16 * TP;
+  ExpandWave<ET, TQ> part;   // (of the 16 tokens whose sums this wave joins)
+  static_assert(TP == NW, "a wave per 16 tokens");
+  part.start(a, t0 + 16 * wave, lane);
+  part.load(a, n0, lane);
+  f32x4 acc[TQ][TP];
+#pragma unroll
+  for (int i = 0; i < TP; i++)
+#pragma unroll
+    for (int j = 0; j < TQ; j++) acc[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  if (a.w) {
+    NarrowRows<16 * TP, D> op_x;
+    NarrowRows<16 * TQ, D> op_w;
+    op_x.init(make_buf(a.x + (size_t)t0 * a.ldx, 2 * ((size_t)(min(16 * TP, a.T - t0) - 1) * a.ldx + a.K)), a.K, lane,
+              [&](int i) { return t0 + i < a.T ? (uint32_t)(i * a.ldx * 2) : kNowhere; });
+    op_w.init(make_buf(a.w + (size_t)n0 * a.ldw, 2 * ((size_t)(min(16 * TQ, a.N - n0) - 1) * a.ldw + a.K)), a.K, lane,
+              [&](int i) { return n0 + i < a.N ? (uint32_t)(i * a.ldw * 2) : kNowhere; });
+    narrow_product<ET, TP, TQ, NW, D>(op_x, op_w, a.K, wave, lane, s_a[0][wave], s_a[1][wave], acc);
+  }
+  __syncthreads();
+  f32x4 v[TQ];
+  skinny_reduce<TP, TQ, NW>(reinterpret_cast<f32x4(*)[TQ * TP][64]>(&s_a[0][0][0]), acc, wave, lane, v);
+  part.add(v);
+  while (part.more()) {
+    part.load(a, n0, lane);
+    part.add(v);
+  }
+#pragma unroll
+  for (int j = 0; j < TQ; j++) lora_store<ET>(a, t0 + 16 * wave + (lane & 15), n0 + 16 * j + 4 * (lane >> 4), v[j]);
 }
 
 // One to sixteen tokens with few 16-rank blocks among their adapters (at most NB): both
@@ -519,20 +620,31 @@ static hipError_t launch_lora(const LoraArgs& a, hipStream_t s) {
     return launch_token<ET, 4, 5>(a, s);
   }
   {
-    // (with many tokens, most of 16 share an adapter: four workgroups walk them instead of 16)
     ProfScope prof("lora_shrink", s);
-    EXMOE_LAUNCH(prof, (lora_shrink_kernel<ET, 4, 64>), dim3((a.T + 15) / 16, a.T > 256 ? std::min(distinct, 4) : distinct, a.rank_blocks),
+    EXMOE_LAUNCH(prof, (lora_shrink_kernel<ET, 4, 64>), dim3((a.T + 15) / 16, a.T > 256 ? std::min(distinct, 8) : distinct, a.rank_blocks),
                  dim3(256), 0, s, a);
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const bool span = 2 * ((size_t)(a.T - 1) * a.ldx + a.K) < kMaxSpan && 2 * ((size_t)(a.N - 1) * a.ldw + a.K) < kMaxSpan;
-  // Few-token blocks against pipelined tiles, 2048 x 2048, ranks to 64, us: 256 tokens of 256
-  // requests 43 / 103, of 8 requests 33 / 41; 512 tokens of 512 requests 77 / 109, of 8 requests
-  // 52 / 38; 1024 tokens of 512 requests 117 / 86, of 8 requests 94 / 40.
-  if (a.w && span && a.T > 512) {
+  // Pipelined 128 x 128 tiles against 64 x 64 blocks, one of which a compute unit holds: beyond
+  // two rounds of those. K = 2048, ranks to 64, us: 1024 tokens of 512 requests, N = 2048 (512
+  // blocks) 86 / 65, of 8 requests 40 / 35; 300 tokens of 20 requests, N = 5632 (440) 40 / 36; 600
+  // tokens of 20 requests, N = 5632 (880) 41 / 56; 555 tokens, N = 3712, K = 7472 (522) 107 / 120.
+  const long long blocks = (long long)((a.T + 63) / 64) * ((a.N + 63) / 64);
+  if (a.w && span && a.T > 64 && blocks > 512) {
     if ((long long)((a.T + 255) / 256) * ((a.N + 255) / 256) >= 256) return launch_lora_wide<ET, 4, 2, 2, 4, 2>(a, s);
     return launch_lora_wide<ET, 2, 2, 2, 2, 2>(a, s);
+  }
+  // 64 x 64 blocks against 16 x 16, where they reach enough compute units, us: 128 tokens of 128
+  // requests, N = K = 2048 (64 blocks) 40 / 27, with N = 5632 (176) 29 / 47; 94 tokens, N = 5664
+  // (178) 25 / 40; 256 tokens of 256 requests, N = K = 2048 (128) 43 / 43, of 8 requests 25 / 34; 142
+  // tokens, N = 192 (9) 39 / 20.
+  if (a.T > 64 && blocks >= 100) {
+    const int tt = (a.T + 63) / 64;
+    ProfScope prof("lora_linear", s);
+    EXMOE_LAUNCH(prof, lora_mid_kernel<ET>, dim3((a.N + 63) / 64 * tt), dim3(256), 0, s, a, tt);
+    return hipGetLastError();
   }
   return launch_skinny<ET, 1, 8, 64>(a, s);
 }
