@@ -276,7 +276,6 @@ struct TileOut {
   void* ptr;
   size_t base, ld;
   bool f32, vec;   // vec: rows can be stored 16 bytes at a time
-  bool stream;     // stores bypass the caches
 };
 
 // One tile: rows p0.. (those below plim exist), columns q0.. (below Q) of the output, summed
@@ -445,7 +444,7 @@ __device__ __forceinline__ void wide_tile(const OpP& op_p, const OpQ& op_q, int 
   // Lane l holds p = l % 32 and q = 8 g + 4 (l / 32) + 0..3 (registers 4 g..4 g + 3) of a block:
   // each wave turns a row block at a time through its own part of LDS, so that a row leaves
   // in pieces of 16 bytes a lane, 32 TQ outputs together (16-byte chunks swizzled by the row,
-  // so that 16 rows of a write hit distinct banks). Streamed stores bypass the caches: a gradient of
+  // so that 16 rows of a write hit distinct banks). The stores bypass the caches: a gradient of
   // W of 1 GiB left in 289 us instead of 485 us (2048 tokens, 64 experts of 2048 x 2048, fp32).
 #pragma unroll
   for (int i = 0; i < TP; i++)
@@ -487,8 +486,7 @@ __device__ __forceinline__ void wide_tile(const OpP& op_p, const OpQ& op_q, int 
         if (pb + row < plim && q < Q) {
           char* dst = static_cast<char*>(out.ptr) + (out.base + (size_t)out_row(pb + row) * out.ld + q) * SZ;
           if (out.vec && q + 16 / SZ <= Q) {
-            if (out.stream) __builtin_nontemporal_store(__builtin_bit_cast(i32x4, v), reinterpret_cast<i32x4*>(dst));
-            else *reinterpret_cast<uint4*>(dst) = v;
+            __builtin_nontemporal_store(__builtin_bit_cast(i32x4, v), reinterpret_cast<i32x4*>(dst));
           } else {
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll

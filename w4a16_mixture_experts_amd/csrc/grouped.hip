@@ -144,9 +144,9 @@ __device__ __forceinline__ bool place_tile(const GroupedArgs& a, int p_tiles, in
 // Where a tile's outputs go: the caller's matrix, or the partial sums [split][E][N][K].
 template <int MODE>
 __device__ __forceinline__ TileOut tile_out(const GroupedArgs& a, const TilePlace& t, int splits) {
-  TileOut o{a.out, 0, a.ldo, a.out_f32 != 0, a.vec != 0, true};
+  TileOut o{a.out, 0, a.ldo, a.out_f32 != 0, a.vec != 0};
   if (MODE == kWG) {
-    if (splits > 1) o = TileOut{a.ws, ((size_t)t.split * a.E + t.e) * a.N * a.K, (size_t)a.K, true, a.K % 4 == 0, false};
+    if (splits > 1) o = TileOut{a.ws, ((size_t)t.split * a.E + t.e) * a.N * a.K, (size_t)a.K, true, a.K % 4 == 0};
     else o.base = (size_t)t.e * a.o_stride;
   }
   return o;

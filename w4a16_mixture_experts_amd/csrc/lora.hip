@@ -579,7 +579,7 @@ __global__ __launch_bounds__(64 * WP * WQ, OCC) void lora_wide_kernel(LoraArgs a
             [&](int i) { return q0 + i < a.N ? (uint32_t)((size_t)(q0 + i) * a.ldw * 2) : kNowhere; });
   const int n0 = q0 + 32 * TQ * (wave % WQ);
   wide_tile<ET, TP, TQ, WP, WQ, 64, false>(
-      op_p, op_q, a.K, p0, a.T, q0, a.N, TileOut{a.y, 0, a.ldy, false, a.vec16 != 0, true}, [](int) { return 0; },
+      op_p, op_q, a.K, p0, a.T, q0, a.N, TileOut{a.y, 0, a.ldy, false, a.vec16 != 0}, [](int) { return 0; },
       [](int) { return 0u; }, [&](int i, int t, auto& acc) { lora_expand32<ET, TQ, TP>(a, t, n0, lane, acc, i); },
       [](int p) { return p; });
 }
