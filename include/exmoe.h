@@ -359,7 +359,8 @@ int exmoe_moe_forward_cached(const exmoe_bf16* x, const int32_t* topk_ids, const
  * (to nearest even) when the output is 16 bits wide.
  *
  * Sizes: any rows >= 0, N, K >= 1 (multiples of 8 with 16-byte aligned rows run on wider
- * loads), 1 <= E <= 256; empty segments are allowed anywhere (exmoe_grouped_mm_wgrad
+ * loads; other row lengths are copied into the workspace with padded rows where that pays),
+ * 1 <= E <= 256; empty segments are allowed anywhere (exmoe_grouped_mm_wgrad
  * writes zeros for them). ld* are elements between rows, *_stride elements between
  * experts; the last axis is contiguous. Pointers need the alignment of their elements only
  * (workspace: 16 bytes). Operands share `dtype` (bf16 or fp16); out_dtype is that type or
@@ -407,10 +408,10 @@ int exmoe_grouped_mm_wgrad(const void* dy, size_t lddy, const void* x, size_t ld
  *
  * x [T, K], w [N, K], y [T, N] and the bank are bf16 or all fp16 (dtype), last axis
  * contiguous, ld* elements between rows. K and rank_max are multiples of 8, rank_max <= 128,
- * rows of x, w, a and b 16-byte aligned (ld and strides multiples of 8, ld <= 2^24); N is any size. The
- * bank's adapters lie a_stride / b_stride elements apart; ranks int32 [adapters] (clamped to
- * [0, rank_max]; what a and b hold past an adapter's rank is not used) and scales fp32
- * [adapters] are device arrays or NULL (rank_max, 1). y must not overlap the inputs.
+ * rows of x, w, a and b 16-byte aligned (ld and strides multiples of 8, ld <= 2^24); N is any
+ * size. The bank's adapters lie a_stride / b_stride elements apart; ranks int32 [adapters]
+ * (clamped to [0, rank_max]; what a and b hold past an adapter's rank is not used) and scales
+ * fp32 [adapters] are device arrays or NULL (rank_max, 1). y must not overlap the inputs.
  * Workspace: exmoe_lora_workspace_bytes bytes, no initialization, not kept; calls that
  * overlap in time must not share one. Equal calls give equal bits.
  * ---------------------------------------------------------------------------------- */
@@ -438,7 +439,8 @@ int exmoe_lora_linear(const void* x, size_t ldx, const void* w, size_t ldw, cons
  * synchronizes the recorded events and returns the accumulated milliseconds and launch
  * count of one kernel by name: "route_logits", "route_token", "route_sel", "topk",
  * "group", "decode_gateup", "decode_down", "decode_fused", "combine", "xsum",
- * "prefill_gateup", "prefill_down". Process-global. The events bracket the launch as the
+ * "prefill_gateup", "prefill_down", "grouped_mm", "grouped_dgrad", "grouped_wgrad",
+ * "pack_rows", "token_sum", "split_sum", "lora_shrink", "lora_linear". Process-global. The events bracket the launch as the
  * stream processes it, so a launch that waits for the host is counted with that wait.
  * ---------------------------------------------------------------------------------- */
 int exmoe_profile_enable(int on);

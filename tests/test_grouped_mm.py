@@ -485,6 +485,30 @@ def test_token_gradients_of_every_form(counts, N, K):
 
 
 @gpu
+def test_infinite_rows_far_apart():
+    """Few summed rows 2^27 elements apart, the first of them infinite: positions past the last
+    row are zeros times zeros, not zeros times the first row."""
+    inf, ld = float("inf"), 1 << 27
+    buf = torch.empty(7 * ld + 64, dtype=BF16, device="cuda")
+    rows8 = buf.as_strided((8, 64), (ld, 1))
+    rows8.fill_(1.0)
+    rows8[0] = inf
+    near = torch.ones((8, 64), dtype=BF16, device="cuda")
+    off = torch.tensor([0, 8], dtype=torch.int32, device="cuda")
+    dx = exm.grouped_mm_dgrad(near[:, :8], rows8.unsqueeze(0), off, out_dtype=FP32)
+    assert bool((dx == inf).all())
+    many = torch.ones((400, 8), dtype=BF16, device="cuda")
+    dx = exm.grouped_mm_dgrad(many, rows8.unsqueeze(0), torch.tensor([0, 400], dtype=torch.int32, device="cuda"), out_dtype=FP32)
+    assert bool((dx == inf).all())
+    assert bool((exm.grouped_mm_wgrad(rows8, near, off) == inf).all())
+    assert bool((exm.grouped_mm_wgrad(near, rows8, off) == inf).all())
+    one = buf.as_strided((1, 64), (1 << 31, 1))       # one row: its stride means nothing
+    off1 = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    assert bool((exm.grouped_mm_wgrad(one, near[:1], off1) == inf).all())
+    assert bool((exm.grouped_mm_wgrad(near[:1], one, off1) == inf).all())
+
+
+@gpu
 def test_no_rows_and_no_routing():
     """No rows at all: nothing is written but the zeros of a gradient of W; a routing that gives
     every row to nobody does the same."""

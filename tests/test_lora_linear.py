@@ -213,6 +213,10 @@ def test_rows_far_apart():
     xd = torch.empty((T - 1) * ld + K, dtype=BF16, device="cuda").as_strided((T, K), (ld, 1))
     xd.copy_(x)
     ref, _ = plain(x, w, a, b, ids, torch.full((L,), R), torch.ones(L))
+    last = torch.empty(1 << 28, dtype=BF16, device="cuda").as_strided((1, K), (1 << 27, 1))   # one token: its stride means nothing
+    last.copy_(x[:1])
+    bank = exm.LoraBank(a.to(BF16).cuda(), b.to(BF16).cuda())
+    assert torch.equal(exm.lora_linear(last, w.to(BF16).cuda(), bank, ids[:1].to(torch.int32).cuda()).cpu(), ref[:1].to(BF16))
     for n in (N, 1000):       # 64 x 64 and 16 x 16 blocks
         bank = exm.LoraBank(a.to(BF16).cuda(), b[:, :n].contiguous().to(BF16).cuda())
         y = exm.lora_linear(xd, w[:n].to(BF16).cuda(), bank, ids.to(torch.int32).cuda())

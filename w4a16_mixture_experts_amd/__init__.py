@@ -410,7 +410,7 @@ def _rows_ld(name: str, t, ndim: int = 2) -> int:
         raise ValueError(f"{name} must be a GPU tensor")
     if stride[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name}: the last axis must be contiguous")
-    return stride[-2] if shape[-2] > 1 else max(stride[-2], shape[-1])
+    return stride[-2] if shape[-2] > 1 else shape[-1]   # (the stride of a single row means nothing)
 
 
 def _expert_stride(t, ld: int) -> int:

@@ -660,6 +660,9 @@ static bool op_aligned(const void* p, size_t ld, size_t stride, int len) {
 
 // Whether an operand of n rows, ld apart, len long, can be addressed with 32-bit offsets.
 static bool op_span(size_t n, size_t ld, int len) { return n == 0 || 2 * ((n - 1) * ld + len) < kMaxSpan; }
+// The same where the n rows are the summed axis: a slice's rows past the end (up to 63) have
+// to lie past the buffer too, not wrap around into it.
+static bool sum_span(size_t n, size_t ld, int len) { return ld < kMaxSpan && op_span(n + 64, ld, len); }
 
 // Tiles of 256 x 256 on 8 waves (one workgroup per compute unit) move half the bytes per
 // product of 128 x 128 tiles on 4 waves (two per unit, so that one's start and end hide
@@ -777,7 +780,7 @@ static hipError_t dgrad_type(const GroupedArgs& a, hipStream_t s) {
   }
   hipError_t e;
   if (!al) e = launch_rows<ET, kDG, 128, 128, 2, 2, false>(r, "grouped_dgrad", s);
-  else if (!op_span(a.rows, a.lda, a.len_a) || !op_span(a.N, a.ldb, a.len_b))
+  else if (!op_span(a.rows, a.lda, a.len_a) || !sum_span(a.N, a.ldb, a.len_b))
     e = launch_rows<ET, kDG, 128, 128, 2, 2, true>(r, "grouped_dgrad", s);
   else if (narrow_dgrad(a)) e = launch_narrow_dgrad<ET, 1, 8>(r, s);
   else if (few_tiles(a.rows, a.K, a.E)) e = launch_narrow_dgrad<ET, 4, 4>(r, s);
@@ -827,7 +830,7 @@ static hipError_t wgrad_type(const GroupedArgs& a, hipStream_t s) {
   hipError_t e;
   if (!op_aligned(a.a, a.lda, 0, a.len_a) || !op_aligned(a.b, a.ldb, 0, a.len_b))
     e = launch_weights<128, 128, 256>(a, s, splits, grouped_kernel<ET, kWG, 128, 128, 2, 2, false>);
-  else if (!op_span(a.rows, a.lda, a.len_a) || !op_span(a.x_rows, a.ldb, a.len_b))
+  else if (!sum_span(a.rows, a.lda, a.len_a) || !op_span(a.x_rows, a.ldb, a.len_b))
     e = launch_weights<128, 128, 256>(a, s, splits, grouped_kernel<ET, kWG, 128, 128, 2, 2, true>);
   else if (a.rows / a.E >= 768 && splits == 1 && (long long)a.E * ceil_div(a.N, 256) * ceil_div(a.K, 256) >= 256)
     e = launch_weights_wide<ET, 4, 2, 2, 4, 64, 2>(a, s, splits);
