@@ -409,11 +409,14 @@ def test_offsets_past_32_bits():
     equal(y, plain_mm(x, w, off, src)[0], "mm into wide rows")
 
 
-# (counts, N, K): 16-row blocks and 64 x 64 blocks (few tiles), 128 x 128 and 256 x 256 tiles in
+TALL = [250, 0, 1, 700, 321, 320, 319, 33, 640, 257, 256, 288, 32, 322, 99, 161]   # about 250 on average
+
+# (counts, N, K): 16-row blocks and 64 x 64 blocks (few tiles), tiles of 128, 256 and 320 rows in
 # each direction, split and whole sums over the rows; ragged edges everywhere; odd row lengths,
 # few and many rows per expert.
 FORMS = [([3, 0, 9, 1], 72, 136), ([100, 0, 37, 201], 200, 264), ([130, 0, 1000, 1, 600], 904, 136),
          ([130, 0, 1000, 1, 600], 136, 904), ([1, 4199], 4104, 72), ([4200], 72, 4104), ([0, 1600], 2824, 2824),
+         (TALL, 4616, 72), (TALL, 72, 4616),
          ([200, 0, 190], 41, 77), ([200, 0, 190], 40, 77), ([9, 200, 2], 41, 80), ([700, 690], 523, 129), ([1, 2], 41, 77),
          ([0, 2500], 130, 1001)]
 

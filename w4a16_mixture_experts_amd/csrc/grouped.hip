@@ -664,14 +664,24 @@ static bool op_span(size_t n, size_t ld, int len) { return n == 0 || 2 * ((n - 1
 // to lie past the buffer too, not wrap around into it.
 static bool sum_span(size_t n, size_t ld, int len) { return ld < kMaxSpan && op_span(n + 64, ld, len); }
 
-// Tiles of 256 x 256 on 8 waves (one workgroup per compute unit) move half the bytes per
-// product of 128 x 128 tiles on 4 waves (two per unit, so that one's start and end hide
-// behind the other's loop). Measured, large / small: 4096 tokens, 8 experts of 14336 x 4096
-// (1024 rows each) 879 / 1096 us; 64 experts of 2048 x 2048 with 256 rows each 202 / 217 us,
-// with 256 on average but skewed 215 / 211 us. Large from 256 rows per expert on, when that
-// still gives every compute unit a tile.
-static bool large_tiles(int rows, int Q, int E) {
-  return rows / E >= 256 && (long long)(rows / 256) * ceil_div(Q, 256) >= 256;
+// Rows of the tiles: 256 x 256 on 8 waves (one workgroup per compute unit) moves half the bytes
+// per product of 128 x 128 on 4 waves (two per unit, so that one's start and end hide behind
+// the other's loop). 320 x 256 keeps most experts in one tile where their rows scatter around a
+// little less than 256 to 320: an expert of 257 rows costs two tiles of 256, which read its W
+// twice. Measured on 64 experts of 2048 x 2048, rows per expert on average, evenly routed /
+// skewed, us:
+//         96          128         160         200         256         288    320    375
+//   128   135 / 145   157 / 164   170 / 170   177 / 191   217 / 211
+//   256   137 / 168   142 / 167   146 / 168   148 / 172   201 / 214   219    223    232
+//   320                                       150 / 183   164 / 193   190    223    241
+// The gradient of x, 200 rows: 208 / 165 / 173 on 128, 256, 320; 256 rows, skewed: 245 / 232 on
+// 256, 320. From 512 rows on 256 and 320 are within 5% of each other; 8 experts of 14336 x 4096
+// with 1024 rows each: 1096 / 879 / 864 on 128, 256, 320; one of 8192 x 8192 846 / 924 on 256, 320.
+// The large tiles need to give every compute unit one.
+static int tile_rows(int rows, int Q, int E) {
+  const int each = rows / E;
+  if (each < 160 || (long long)(rows / 256) * ceil_div(Q, 256) < 256) return 128;
+  return each > 256 * 9 / 10 && each <= 320 * 9 / 10 ? 320 : 256;
 }
 
 template <class ET, int TP, int TQ, int NW, int D, bool ALIGNED>
@@ -726,7 +736,9 @@ static hipError_t mm_type(const GroupedArgs& a, hipStream_t s) {
   if (!op_span(a.x_rows, a.lda, a.len_a) || !op_span(a.N, a.ldb, a.len_b))
     return launch_rows<ET, kMM, 128, 128, 2, 2, true>(a, "grouped_mm", s);
   if (few_tiles(a.rows, a.N, a.E)) return launch_narrow<ET, 4, 4, 4, 32, true>(a, s);
-  if (large_tiles(a.rows, a.N, a.E)) return launch_wide<ET, kMM, 4, 2, 2, 4, 64, 2>(a, "grouped_mm", s);
+  const int height = tile_rows(a.rows, a.N, a.E);
+  if (height == 320) return launch_wide<ET, kMM, 5, 2, 2, 4, 64, 2>(a, "grouped_mm", s);
+  if (height == 256) return launch_wide<ET, kMM, 4, 2, 2, 4, 64, 2>(a, "grouped_mm", s);
   return launch_wide<ET, kMM, 2, 2, 2, 2, 64, 2>(a, "grouped_mm", s);
 }
 
@@ -779,12 +791,14 @@ static hipError_t dgrad_type(const GroupedArgs& a, hipStream_t s) {
     r.out_f32 = 1;
   }
   hipError_t e;
+  const int height = tile_rows(a.rows, a.K, a.E);
   if (!al) e = launch_rows<ET, kDG, 128, 128, 2, 2, false>(r, "grouped_dgrad", s);
   else if (!op_span(a.rows, a.lda, a.len_a) || !sum_span(a.N, a.ldb, a.len_b))
     e = launch_rows<ET, kDG, 128, 128, 2, 2, true>(r, "grouped_dgrad", s);
   else if (narrow_dgrad(a)) e = launch_narrow_dgrad<ET, 1, 8>(r, s);
   else if (few_tiles(a.rows, a.K, a.E)) e = launch_narrow_dgrad<ET, 4, 4>(r, s);
-  else if (large_tiles(a.rows, a.K, a.E)) e = launch_wide<ET, kDG, 4, 2, 2, 4, 64, 2>(r, "grouped_dgrad", s);
+  else if (height == 320) e = launch_wide<ET, kDG, 5, 2, 2, 4, 64, 2>(r, "grouped_dgrad", s);
+  else if (height == 256) e = launch_wide<ET, kDG, 4, 2, 2, 4, 64, 2>(r, "grouped_dgrad", s);
   else e = launch_wide<ET, kDG, 2, 2, 2, 2, 64, 2>(r, "grouped_dgrad", s);
   if (e != hipSuccess || !a.flat_to_sorted) return e;
   const int T = a.rows / a.k;
