@@ -294,7 +294,8 @@ struct TileOut {
 // 256 x 256 tiles (4, 2, 2, 4, 64): 8192 x 8192 x 8192 bf16 in 829 us, 1.33 PFLOP/s; MFMA
 // busy 80% of the cycles at the about 1.5 GHz that the chip sustains under it, the rest is
 // waiting for copies at the barrier. Slices half as deep in four buffers: 909 us (twice the
-// barriers); four waves of 128 x 128: 922 us (nothing hides a lone wave's barrier).
+// barriers); four waves of 128 x 128: 922 us (nothing hides a lone wave's barrier); the lines of
+// the slice after next asked for into L2 a slice ahead: 876 us.
 template <class ET, int TP, int TQ, int WP, int WQ, int D, bool GATHER, class OpP, class OpQ, class LoadRow,
           class RowBytes, class Adjust, class OutRow>
 __device__ __forceinline__ void wide_tile(const OpP& op_p, const OpQ& op_q, int red, int p0, int plim, int q0, int Q,
