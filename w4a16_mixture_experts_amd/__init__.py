@@ -200,9 +200,15 @@ def unpack_expert(blob: np.ndarray, H: int, I: int):
 
 
 # ----------------------------------------------------------------------------- device calls
+_TORCH = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+    return _TORCH
 
 
 def _ptr(t) -> Optional[int]:
@@ -420,16 +426,16 @@ def _expert_stride(t, ld: int) -> int:
 def _int32(name: str, t, dev: int, numel: Optional[int] = None):
     if t is None:
         return None
-    if t.dtype is not _torch().int32 or t.get_device() != dev or not t.is_contiguous():
+    if t.dtype is not (_TORCH or _torch()).int32 or t.get_device() != dev or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor on GPU {dev}")
     if numel is not None and t.numel() != numel:
         raise ValueError(f"{name} must have {numel} entries (got {t.numel()})")
     return t.data_ptr()
 
 
-def _result(name: str, out, shape, dtype, dev: int):
+def _result(name: str, out, shape, dtype, dev: int, like):
     if out is None:
-        return _torch().empty(shape, dtype=dtype, device=f"cuda:{dev}")
+        return like.new_empty(shape, dtype=dtype)
     if out.shape != shape or out.dtype is not dtype or out.get_device() != dev:
         raise ValueError(f"{name} must be {tuple(shape)} {dtype} on GPU {dev}")
     return out
@@ -449,8 +455,8 @@ def _scratch(workspace, need, dev: int):
 
 def _run_on(dev: int, fn, *args):
     """Calls a C entry point on GPU dev, on that device's current stream."""
-    torch = _torch()
-    if dev == torch.cuda.current_device():
+    torch = _TORCH or _torch()
+    if dev == torch._C._cuda_getDevice():
         st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
@@ -484,7 +490,7 @@ def grouped_mm(x, w, offsets, row_index=None, row_div: int = 1, out_dtype=None, 
         raise ValueError(f"x has {x_cols} columns, w takes {K}")
     rows = x_rows if row_index is None else row_index.numel()
     out_dtype = dtype if out_dtype is None else out_dtype
-    y = _result("y", y, (rows, N), out_dtype, dev)
+    y = _result("y", y, (rows, N), out_dtype, dev, x)
     ws, ws_bytes, _keep = _scratch(workspace, lambda: grouped_mm_workspace_bytes(GROUPED_MM, rows, N, K, E), dev)
     _run_on(dev, _lib.exmoe_grouped_mm, x.data_ptr(), ldx, x_rows, _int32("row_index", row_index, dev), row_div,
             _int32("offsets", offsets, dev, E + 1), w.data_ptr(), ldw, _expert_stride(w, ldw), rows, N, K, E,
@@ -505,7 +511,7 @@ def grouped_mm_dgrad(dy, w, offsets, flat_to_sorted=None, k: int = 1, out_dtype=
     if flat_to_sorted is not None and (k < 1 or rows % k):
         raise ValueError(f"dy's {rows} rows are no multiple of k = {k}")
     out_dtype = dtype if out_dtype is None else out_dtype
-    dx = _result("dx", dx, (rows if flat_to_sorted is None else rows // k, K), out_dtype, dev)
+    dx = _result("dx", dx, (rows if flat_to_sorted is None else rows // k, K), out_dtype, dev, dy)
     ws, ws_bytes, _keep = _scratch(
         workspace, lambda: grouped_mm_workspace_bytes(GROUPED_DGRAD, rows, N, K, E, 0 if flat_to_sorted is None else k), dev)
     _run_on(dev, _lib.exmoe_grouped_mm_dgrad, dy.data_ptr(), lddy, _int32("offsets", offsets, dev, E + 1), w.data_ptr(),
@@ -526,7 +532,7 @@ def grouped_mm_wgrad(dy, x, offsets, row_index=None, row_div: int = 1, out_dtype
     if row_index is None and x_rows < rows:
         raise ValueError(f"x has {x_rows} rows, dy has {rows}")
     out_dtype = _torch().float32 if out_dtype is None else out_dtype
-    dw = _result("dw", dw, (E, N, K), out_dtype, dev)
+    dw = _result("dw", dw, (E, N, K), out_dtype, dev, x)
     lddw = _rows_ld("dw", dw, 3)
     ws, ws_bytes, _keep = _scratch(workspace, lambda: grouped_mm_workspace_bytes(GROUPED_WGRAD, rows, N, K, E), dev)
     _run_on(dev, _lib.exmoe_grouped_mm_wgrad, dy.data_ptr(), lddy, x.data_ptr(), ldx, x_rows,
@@ -580,7 +586,7 @@ def lora_linear(x, w, bank: LoraBank, ids, y=None, workspace=None):
         _same("w", w, dtype, dev)
         if w.shape != (N, K):
             raise ValueError(f"w must be {(N, K)} (got {tuple(w.shape)})")
-    y = _result("y", y, (T, N), dtype, dev)
+    y = _result("y", y, (T, N), dtype, dev, x)
     ws, ws_bytes, _keep = _scratch(workspace, lambda: lora_workspace_bytes(T, N, K, bank.c.adapters, bank.c.rank_max), dev)
     _run_on(dev, _lib.exmoe_lora_linear, x.data_ptr(), ldx, wp, ldw, bank.ref, _int32("ids", ids, dev, T), T, N, K,
             _dtype_code(dtype), y.data_ptr(), _rows_ld("y", y), ws, ws_bytes)

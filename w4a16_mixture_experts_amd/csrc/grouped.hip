@@ -580,7 +580,7 @@ __global__ __launch_bounds__(256) void split_sum_kernel(const float* __restrict_
 
 // ------------------------------------------------------------------------------------ host
 static inline int ceil_div(int a, int b) { return (int)(((long long)a + b - 1) / b); }
-constexpr long long kMaxThreads = 0xFFFFFFFFll;   // of one launch; larger calls are refused
+constexpr long long kMaxThreads = 0xFFFFFF00ll;   // of one launch, in whole workgroups; larger calls are refused
 
 // Parts into which the sum over an expert's rows is split: enough workgroups for the chip
 // where an expert's gradient has few tiles, at least four 64-row slices per part.
