@@ -414,7 +414,8 @@ TALL = [250, 0, 1, 700, 321, 320, 319, 33, 640, 257, 256, 288, 32, 322, 99, 161]
 # (counts, N, K): 16-row blocks and 64 x 64 blocks (few tiles), tiles of 128, 256 and 320 rows in
 # each direction, split and whole sums over the rows; ragged edges everywhere; odd row lengths,
 # few and many rows per expert.
-FORMS = [([3, 0, 9, 1], 72, 136), ([100, 0, 37, 201], 200, 264), ([130, 0, 1000, 1, 600], 904, 136),
+FORMS = [([3, 0, 9, 1], 72, 136), ([100, 0, 37, 201], 200, 264),
+         ([100, 0, 37, 201], 840, 264), ([100, 0, 37, 201], 264, 840), ([130, 0, 1000, 1, 600], 904, 136),
          ([130, 0, 1000, 1, 600], 136, 904), ([1, 4199], 4104, 72), ([4200], 72, 4104), ([0, 1600], 2824, 2824),
          (TALL, 4616, 72), (TALL, 72, 4616),
          ([200, 0, 190], 41, 77), ([200, 0, 190], 40, 77), ([9, 200, 2], 41, 80), ([700, 690], 523, 129), ([1, 2], 41, 77),
@@ -468,7 +469,8 @@ def test_every_form_with_a_gather_nan_neighbours_and_bad_indices(counts, N, K, d
 
 
 @gpu
-@pytest.mark.parametrize("counts,N,K", [([100, 0, 37, 203], 200, 264), ([130, 1, 1000, 601], 136, 904), ([200, 0, 192], 41, 77),
+@pytest.mark.parametrize("counts,N,K", [([100, 0, 37, 203], 200, 264), ([100, 0, 37, 203], 264, 840),
+                                        ([130, 1, 1000, 601], 136, 904), ([200, 0, 192], 41, 77),
                                         ([2, 4198], 72, 4104)])
 def test_token_gradients_of_every_form(counts, N, K):
     """The gradient of x summed per token (k = 4), with ungrouped rows and an index outside."""

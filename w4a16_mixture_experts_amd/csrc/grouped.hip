@@ -723,6 +723,13 @@ constexpr int kNarrowRows = 16;
 static bool few_tiles(int rows, int Q, int E) {
   return (rows / 128 + (long long)(E < rows ? E : rows)) * ceil_div(Q, 128) < 128;
 }
+// Of those, too few 64 x 64 blocks: 16-row blocks (blocks of 64 x 64, us on 64 x 64 / 16 rows:
+// forward 18, K = 6496, 34 / 16; 38, K = 2176, 12.6 / 8.7; 56, K = 2048, 12.1 / 8.5; 96, K = 1024,
+// 9.9 / 11.1; 176, K = 2048, 14.7 / 19.3; gradient of x 21, N = 4224, 27 / 16; 56, N = 2048, 14.8 /
+// 11.1; 304, N = 512, 13.6 / 18.2).
+static bool few_blocks(int rows, int Q, int E) {
+  return (rows / 64 + (long long)(E < rows ? E : rows)) * ceil_div(Q, 64) < 80;
+}
 
 template <class ET>
 static hipError_t mm_type(const GroupedArgs& a, hipStream_t s) {
@@ -735,7 +742,8 @@ static hipError_t mm_type(const GroupedArgs& a, hipStream_t s) {
     return launch_narrow<ET, 1, 1, 4, 64, true>(a, s);
   if (!op_span(a.x_rows, a.lda, a.len_a) || !op_span(a.N, a.ldb, a.len_b))
     return launch_rows<ET, kMM, 128, 128, 2, 2, true>(a, "grouped_mm", s);
-  if (few_tiles(a.rows, a.N, a.E)) return launch_narrow<ET, 4, 4, 4, 32, true>(a, s);
+  if (few_tiles(a.rows, a.N, a.E))
+    return few_blocks(a.rows, a.N, a.E) ? launch_narrow<ET, 1, 1, 4, 64, true>(a, s) : launch_narrow<ET, 4, 4, 4, 32, true>(a, s);
   const int height = tile_rows(a.rows, a.N, a.E);
   if (height == 320) return launch_wide<ET, kMM, 5, 2, 2, 4, 64, 2>(a, "grouped_mm", s);
   if (height == 256) return launch_wide<ET, kMM, 4, 2, 2, 4, 64, 2>(a, "grouped_mm", s);
@@ -796,7 +804,8 @@ static hipError_t dgrad_type(const GroupedArgs& a, hipStream_t s) {
   else if (!op_span(a.rows, a.lda, a.len_a) || !sum_span(a.N, a.ldb, a.len_b))
     e = launch_rows<ET, kDG, 128, 128, 2, 2, true>(r, "grouped_dgrad", s);
   else if (narrow_dgrad(a)) e = launch_narrow_dgrad<ET, 1, 8>(r, s);
-  else if (few_tiles(a.rows, a.K, a.E)) e = launch_narrow_dgrad<ET, 4, 4>(r, s);
+  else if (few_tiles(a.rows, a.K, a.E))
+    e = few_blocks(a.rows, a.K, a.E) ? launch_narrow_dgrad<ET, 1, 8>(r, s) : launch_narrow_dgrad<ET, 4, 4>(r, s);
   else if (height == 320) e = launch_wide<ET, kDG, 5, 2, 2, 4, 64, 2>(r, "grouped_dgrad", s);
   else if (height == 256) e = launch_wide<ET, kDG, 4, 2, 2, 4, 64, 2>(r, "grouped_dgrad", s);
   else e = launch_wide<ET, kDG, 2, 2, 2, 2, 64, 2>(r, "grouped_dgrad", s);
