@@ -480,13 +480,25 @@ __device__ __forceinline__ void wide_tile(const OpP& op_p, const OpQ& op_q, int 
             *reinterpret_cast<uint2*>(p) = make_uint2(ET::pack2(c[4 * g], c[4 * g + 1]), ET::pack2(c[4 * g + 2], c[4 * g + 3]));
         }
       const int pb = p0 + block_p(i);
+      if (!out.vec) {   // (uniform) rows that start anywhere: neighbouring lanes write neighbouring elements
+#pragma unroll 2
+        for (int e = 0; e < 32 * kCols / 64; e++) {   // (unrolled further, its addresses push sums out of the registers)
+          const int row = (64 * e + lane) / kCols, col = (64 * e + lane) % kCols, q = qw + col;
+          if (pb + row < plim && q < Q) {
+            const size_t o = out.base + (size_t)out_row(pb + row) * out.ld + q;
+            if constexpr (F32) static_cast<uint32_t*>(out.ptr)[o] = *reinterpret_cast<const uint32_t*>(at(row, col * SZ));
+            else static_cast<uint16_t*>(out.ptr)[o] = *reinterpret_cast<const uint16_t*>(at(row, col * SZ));
+          }
+        }
+        continue;
+      }
 #pragma unroll
       for (int r = 0; r < 32; r += kRows) {
         const int row = r + lane / kLanes, col = (lane % kLanes) * (16 / SZ), q = qw + col;
         const uint4 v = *reinterpret_cast<const uint4*>(at(row, col * SZ));
         if (pb + row < plim && q < Q) {
           char* dst = static_cast<char*>(out.ptr) + (out.base + (size_t)out_row(pb + row) * out.ld + q) * SZ;
-          if (out.vec && q + 16 / SZ <= Q) {
+          if (q + 16 / SZ <= Q) {
             __builtin_nontemporal_store(__builtin_bit_cast(i32x4, v), reinterpret_cast<i32x4*>(dst));
           } else {
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
