@@ -139,8 +139,8 @@ def test_against_fp64(T, N, K, L, R, dtype):
     assert torch.equal(y.cpu()[none].double(), y0[none]), "a token without an adapter changed"
 
 
-# (T, N, K): 16 x 16 blocks, 64 x 64 blocks, 128 x 128 and 256 x 256 tiles, all ragged
-FORMS = [(70, 200, 136), (150, 2604, 136), (601, 3804, 72), (4100, 4004, 64)]
+# (T, N, K): blocks of 16, 32 and 64, 128 x 128 and 256 x 256 tiles, all ragged
+FORMS = [(70, 200, 136), (150, 700, 136), (150, 2604, 136), (601, 3804, 72), (4100, 4004, 64)]
 
 
 @gpu

@@ -362,11 +362,11 @@ __global__ __launch_bounds__(64 * NW) void lora_skinny_kernel(LoraArgs a) {
   if (wave < TP) lora_store<ET>(a, t0 + 16 * wave + (lane & 15), n0 + 4 * (lane >> 4), v[0]);
 }
 
-// More tokens, still too few for the pipelined tiles: 64 tokens x 64 columns per workgroup,
-// the waves split K and the rank blocks of the adapters.
-template <class ET>
+// More tokens, still too few for the pipelined tiles: 16 TP tokens x 16 TQ columns per workgroup,
+// the waves split K; a wave adds the adapters of the 16 tokens whose sums it joins.
+template <class ET, int TP, int TQ>
 __global__ __launch_bounds__(256) void lora_mid_kernel(LoraArgs a, int t_tiles) {
-  constexpr int TP = 4, TQ = 4, NW = 4, D = 64, kPart = 16 * (TP + TQ) * D;
+  constexpr int NW = 4, D = 64, kPart = 16 * (TP + TQ) * D;
   __shared__ __attribute__((aligned(16))) uint16_t s_a[2][NW][kPart];   // two slices a wave
   static_assert(sizeof(f32x4) * TP * TQ * 64 * NW <= sizeof(s_a), "the sums fit into the slices' part");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -374,9 +374,11 @@ __global__ __launch_bounds__(256) void lora_mid_kernel(LoraArgs a, int t_tiles) 
   const int idx = xcd_contiguous(blockIdx.x, gridDim.x);
   const int n0 = idx / t_tiles * 16 * TQ, t0 = idx % t_tiles * 16 * TP;
   ExpandWave<ET, TQ> part;   // (of the 16 tokens whose sums this wave joins)
-  static_assert(TP == NW, "a wave per 16 tokens");
-  part.start(a, t0 + 16 * wave, lane);
-  part.load(a, n0, lane);
+  static_assert(TP <= NW, "a wave per 16 tokens");
+  if (wave < TP) {
+    part.start(a, t0 + 16 * wave, lane);
+    part.load(a, n0, lane);
+  }
   f32x4 acc[TQ][TP];
 #pragma unroll
   for (int i = 0; i < TP; i++)
@@ -394,6 +396,7 @@ __global__ __launch_bounds__(256) void lora_mid_kernel(LoraArgs a, int t_tiles) 
   __syncthreads();
   f32x4 v[TQ];
   skinny_reduce<TP, TQ, NW>(reinterpret_cast<f32x4(*)[TQ * TP][64]>(&s_a[0][0][0]), acc, wave, lane, v);
+  if (wave >= TP) return;
   part.add(v);
   while (part.more()) {
     part.load(a, n0, lane);
@@ -595,6 +598,13 @@ static hipError_t launch_skinny(const LoraArgs& a, hipStream_t s) {
                dim3(64 * NW), 0, s, a);
   return hipGetLastError();
 }
+template <class ET, int TP, int TQ>
+static hipError_t launch_mid(const LoraArgs& a, hipStream_t s) {
+  const int tt = (a.T + 16 * TP - 1) / (16 * TP);
+  ProfScope prof("lora_linear", s);
+  EXMOE_LAUNCH(prof, (lora_mid_kernel<ET, TP, TQ>), dim3((a.N + 16 * TQ - 1) / (16 * TQ) * tt), dim3(256), 0, s, a, tt);
+  return hipGetLastError();
+}
 template <class ET, int NB, int NW>
 static hipError_t launch_token(const LoraArgs& a, hipStream_t s) {
   ProfScope prof("lora_linear", s);
@@ -636,16 +646,14 @@ static hipError_t launch_lora(const LoraArgs& a, hipStream_t s) {
     if ((long long)((a.T + 255) / 256) * ((a.N + 255) / 256) >= 256) return launch_lora_wide<ET, 4, 2, 2, 4, 2>(a, s);
     return launch_lora_wide<ET, 2, 2, 2, 2, 2>(a, s);
   }
-  // 64 x 64 blocks against 16 x 16, where they reach enough compute units, us: 128 tokens of 128
-  // requests, N = K = 2048 (64 blocks) 40 / 27, with N = 5632 (176) 29 / 47; 94 tokens, N = 5664
-  // (178) 25 / 40; 256 tokens of 256 requests, N = K = 2048 (128) 43 / 43, of 8 requests 25 / 34; 142
-  // tokens, N = 192 (9) 39 / 20.
-  if (a.T > 64 && blocks >= 100) {
-    const int tt = (a.T + 63) / 64;
-    ProfScope prof("lora_linear", s);
-    EXMOE_LAUNCH(prof, lora_mid_kernel<ET>, dim3((a.N + 63) / 64 * tt), dim3(256), 0, s, a, tt);
-    return hipGetLastError();
-  }
+  // 64 x 64 blocks, then 32 x 32, against 16 x 16, where at least 100 of them share the chip, us:
+  // 128 tokens of 128 requests, N = 5632 (176 of 64 x 64) 29 / 47; 94 tokens, N = 5664 (178) 25 / 40;
+  // 64 tokens, N = 6400 (100), of 64 requests 40 / 42, of 4 requests 22 / 31; 40 tokens of 4, N = 8192
+  // (128) 28 / 45, of 40, N = 6400 (100) 38 / 33; 256 tokens of 8 requests, N = 2048 (128) 25 / 34; 128
+  // of 128 requests, N = 2048 (64) 40 / 27. 32 x 32: 155 tokens, N = 848 (135) 31 / 39; 3896 tokens,
+  // N = 64 (244) 21 / 29; 100 tokens of 8 requests, N = 2048 (256) 15 / 20, 128 of 128 28 / 27.
+  if (a.T > 32 && blocks >= 100) return launch_mid<ET, 4, 4>(a, s);
+  if (a.T > 64 && (long long)((a.T + 31) / 32) * ((a.N + 31) / 32) >= 100) return launch_mid<ET, 2, 2>(a, s);
   return launch_skinny<ET, 1, 8, 64>(a, s);
 }
 
