@@ -291,6 +291,23 @@ def test_strides_and_alignments(front, back, N, K):
 
 
 @gpu
+@pytest.mark.parametrize("counts", [[300, 0, 210], [20, 3, 44]])
+@pytest.mark.parametrize("front,back", [(1, 7), (3, 2)])
+def test_misaligned_rows_of_whole_length(counts, front, back):
+    """Row lengths that are multiples of 8 at addresses that are not, few and many rows."""
+    print(f"misaligned counts={counts} front={front} back={back}", flush=True)
+    gen = torch.Generator().manual_seed(14)
+    E, rows, N, K = 3, sum(counts), 144, 136
+    off, src = offsets_of(counts), torch.arange(sum(counts))
+    x, w, dy = whole(gen, (rows, K)), whole(gen, (E, N, K)), whole(gen, (rows, N))
+    xd, dyd, wd = (strided(t, FP16, front, back)[1] for t in (x, dy, w))
+    offd = off.cuda()
+    equal(exm.grouped_mm(xd, wd, offd, out_dtype=FP32), plain_mm(x, w, off, src)[0], "mm")
+    equal(exm.grouped_mm_dgrad(dyd, wd, offd, out_dtype=FP32), plain_dgrad(dy, w, off)[0], "dgrad")
+    equal(exm.grouped_mm_wgrad(dyd, xd, offd), plain_wgrad(dy, x, off, src)[0], "wgrad")
+
+
+@gpu
 def test_rows_outside_the_segments():
     """Offsets that start after row 0 and end before the last: those rows stay as they were,
     what they hold reaches no output, and experts without rows may hold anything."""
@@ -418,7 +435,7 @@ FORMS = [([3, 0, 9, 1], 72, 136), ([100, 0, 37, 201], 200, 264),
          ([100, 0, 37, 201], 840, 264), ([100, 0, 37, 201], 264, 840), ([130, 0, 1000, 1, 600], 904, 136),
          ([130, 0, 1000, 1, 600], 136, 904), ([1, 4199], 4104, 72), ([4200], 72, 4104), ([0, 1600], 2824, 2824),
          (TALL, 4616, 72), (TALL, 72, 4616),
-         ([200, 0, 190], 41, 77), ([200, 0, 190], 40, 77), ([9, 200, 2], 41, 80), ([700, 690], 523, 129), ([1, 2], 41, 77),
+         ([200, 0, 190], 41, 77), ([200, 0, 190], 40, 77), ([30, 0, 90], 200, 77), ([9, 200, 2], 41, 80), ([700, 690], 523, 129), ([1, 2], 41, 77),
          ([0, 2500], 130, 1001)]
 
 

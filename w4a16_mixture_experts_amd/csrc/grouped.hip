@@ -595,18 +595,21 @@ static int wgrad_splits(int rows, int N, int K, int E) {
 
 static inline int pad8(int n) { return (n + 7) & ~7; }
 static inline size_t align16(size_t n) { return (n + 15) & ~(size_t)15; }
-constexpr int kNarrowRowsAny = 128;   // see kNarrowRows
+// Rows per expert from which the forward product copies operands with odd row lengths. Without
+// and with copies, us: 22 experts of 3831 x 641, 16 rows 73 / 93, 30 rows 108 / 95, 41 rows 142 /
+// 96, 84 rows 262 / 104; 13 experts of 517 x 1003, 31 rows 19 / 23, 39 rows 22 / 24, 60 rows 27 / 24.
+constexpr int kPackRows = 32;
 
 // Operands whose rows are no multiple of 16 bytes long are copied with padded rows first, so
 // that the products run on their aligned forms (one pass over the operand against loads
 // through registers in the product: gradient of x, 1384 rows, N = 7827, K = 384: 510 -> 94 us).
-// Not for the forward product's few rows per expert, which have a form of their own.
+// Not for the forward product's few rows per expert, which read W once or twice anyway.
 GroupedWorkspace grouped_workspace(int op, int rows, int N, int K, int E, int k) {
   GroupedWorkspace w{0, 0, 0};
   const size_t rows_n = align16((size_t)rows * pad8(N) * 2), rows_k = align16((size_t)rows * pad8(K) * 2),
                weights = align16((size_t)E * N * pad8(K) * 2);
   if (op == EXMOE_GROUPED_MM) {
-    if (K % 8 && rows > kNarrowRowsAny * (long long)E) w.pack_a = rows_k, w.pack_b = weights;
+    if (K % 8 && rows > kPackRows * (long long)E) w.pack_a = rows_k, w.pack_b = weights;
   } else if (op == EXMOE_GROUPED_DGRAD) {
     if (k > 0) w.sums = align16((size_t)rows * K * 4);
     if (N % 8) w.pack_a = rows_n;
@@ -715,7 +718,7 @@ static bool narrow_dgrad(const GroupedArgs& a) {
 // 128-row tiles. Measured on 64 experts of 2048 x 2048, us: 2 rows per expert 83 / 117,
 // 8 rows 97 / 128, 16 rows 127 / 130, 32 rows 182 / 131. Operands of any alignment, 13 experts
 // of 517 x 1003: 10 rows 11 / 39, 39 rows 21 / 42, 60 rows 28 / 44, 630 rows 193 / 61.
-constexpr int kNarrowRows = 16;
+constexpr int kNarrowRows = 16, kNarrowRowsAny = 128;
 
 // Fewer 128 x 128 tiles than half the CUs: 64 x 64 blocks whose waves split the reduction (500
 // rows, E = 4, N = 1024, K = 2048: 25.5 -> 14.7 us, the gradient of x of 1000 rows, N = 2048,
