@@ -203,6 +203,24 @@ def test_long_batches_against_fp64(T, N, K, dtype):
 
 
 @gpu
+@pytest.mark.parametrize("T,R", [(1, 8), (16, 128), (17, 24), (300, 40), (700, 128)])
+def test_workspaces_are_enough(T, R):
+    """A workspace of exactly the bytes asked for: what lies behind it stays as it was."""
+    gen = torch.Generator().manual_seed(T)
+    N, K, L = 3804, 72, 7
+    x, w = whole(gen, (T, K), -1, 2), whole(gen, (N, K), -1, 2)
+    a, b = whole(gen, (L, R, K), -1, 2), whole(gen, (L, N, R), -1, 2)
+    ids = torch.randint(-1, L, (T,), generator=gen)
+    need = exm.lora_workspace_bytes(T, N, K, L, R)
+    buf = torch.full((need + 256,), 0xAB, dtype=torch.uint8, device="cuda")
+    y = exm.lora_linear(x.to(BF16).cuda(), w.to(BF16).cuda(), exm.LoraBank(a.to(BF16).cuda(), b.to(BF16).cuda()),
+                        ids.to(torch.int32).cuda(), workspace=buf[:need])
+    ref, _ = plain(x, w, a, b, ids, torch.full((L,), R), torch.ones(L))
+    assert torch.equal(y.cpu(), ref.to(BF16))
+    assert bool((buf[need:] == 0xAB).all())
+
+
+@gpu
 def test_rows_far_apart():
     """Row strides of 2^24 elements, where no 32-bit offset spans the tokens."""
     gen = torch.Generator().manual_seed(3)
