@@ -402,9 +402,11 @@ int exmoe_grouped_mm_wgrad(const void* dy, size_t lddy, const void* x, size_t ld
  *   y[t, n] = sum_k x[t, k] w[n, k] + scale_a sum_{r < rank_a} b_a[n, r] v[t, r]
  *   v[t, r] = sum_k x[t, k] a_a[r, k],  a = adapter_ids[t]
  *   (w NULL: y[t, n] += the second term; tokens without an adapter are left as they are).
- * An id outside [0, adapters) is a token without an adapter. v is held in 32 bits (as two
- * 16-bit halves for the product with b_a), sums are fp32, y is rounded once. Where v or an
- * element of b_a is infinite, that output is infinite or NaN.
+ * An id outside [0, adapters) is a token without an adapter. v is held in 32 bits: for the
+ * product with b_a as four 16-bit terms, which lose nothing of a bf16 call's v; in fp16 ranks
+ * down to 2^-38 of the largest |v| among their 16 (r / 16 alike) are kept whole, smaller ones to
+ * 2^-62 of that largest. Sums are fp32, y is rounded once. Where v, scale_a v or an element of
+ * b_a is infinite, that output is infinite or NaN.
  *
  * x [T, K], w [N, K], y [T, N] and the bank are bf16 or all fp16 (dtype), last axis
  * contiguous, ld* elements between rows. K and rank_max are multiples of 8, rank_max <= 128,

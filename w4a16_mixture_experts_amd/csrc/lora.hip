@@ -11,9 +11,12 @@
 //   main    the tiles of x W^T; then, per 16 tokens, one short MFMA chain per adapter among
 //           them adds B_a v to the accumulators of that adapter's tokens.
 // v has 32 bits but B_a v runs on 16-bit MFMA: 16 ranks of a token's v are scaled by a power
-// of two into [-2, 2] and split into hi + lo, two 16-bit values whose sum is v to 2^-16 (bf16)
-// or 2^-22 (fp16) of it; both halves multiply the same B_a in one MFMA (16 summed positions
-// hi, 16 lo). The power of two and the adapter's scale are applied in fp32 to the result.
+// of two and split into four 16-bit terms (SplitV); two of them multiply the same B_a in one
+// MFMA of 32 summed positions (16 ranks each), the other two in a second one. The power of two
+// and the adapter's scale are applied in fp32 to the result. (Two terms alone are off by 2^-16
+// of v in bf16 and lose ranks far below the token's largest in fp16. The second MFMA and its
+// operand cost: 2048 tokens of 8 requests, rank 64, 4096 x 4096, 80.0 -> 82.6 us for the main
+// launch; 64 tokens of 64 requests, 2048 x 2048, 9.9 -> 10.6; one token, rank 16, 5.4 -> 5.5.)
 #include <algorithm>
 
 #include "exmoe.h"
@@ -38,7 +41,7 @@ struct LoraArgs {
   int vec8, vec16;            // rows of y can be stored 8 / 16 bytes at a time
   int rank_blocks;            // ceil(rank_max / 16)
   // by groups of 16 tokens and blocks of 16 ranks (group g, block b: index g rank_blocks + b):
-  uint16_t* hl;               // [index][2][2][16][8]: hi, lo; ranks 0..7, 8..15; token; rank (fragment order)
+  uint16_t* terms;            // [index][4][2][16][8]: term; ranks 0..7, 8..15; token; rank (fragment order)
   float* mul;                 // [index][16]: scale_a times the power of two taken out of a token's v
   int2* info;                 // [T]: the token's adapter (-1: none) and its rank
 };
@@ -64,23 +67,47 @@ __device__ __forceinline__ int nth_adapter(int id, int j) {
   return -1;
 }
 
-// A token's v of 16 ranks, scaled by a power of two and split: m is the largest |v| of the 16.
+// A token's v of 16 ranks as four 16-bit terms: m, the largest |v| of the 16, is scaled into
+// [2^kTop, 2^(kTop + 1)), and v down = t0 + t1 + (t2 + t3) / kRest, each term what the ones before
+// leave, rounded to nearest (every difference is exact).
+//   bf16: three terms hold the 24 bits, in fp32's own range of exponents: nothing is lost.
+//   fp16: t0 + t1 are off by 2^-22 of the value or, where t1 is subnormal, by 2^-25; t2 and t3 take
+//   that 2^23 times larger (at most 2^15) and are off by 2^-25 of it. Nothing is lost of ranks down
+//   to 2^-38 of the largest, below that at most 2^-62 of the largest.
+template <class ET>
 struct SplitV {
-  float down, up;   // 1 / 2^e and 2^e with the largest |v| / 2^e in [1, 2); 1 where nothing finite and normal is there
+  static constexpr bool kBF16 = std::is_same_v<ET, ElemBF16>;
+  static constexpr uint32_t kTop = kBF16 ? 1 : 14;
+  static constexpr float kRest = kBF16 ? 1.f : 8388608.f;
+  float down, up;   // the power of two and its inverse; 1 where nothing finite and normal is there
   __device__ __forceinline__ explicit SplitV(float m) {
     const uint32_t eb = __float_as_uint(m) >> 23;
-    const bool scale = eb >= 1 && eb <= 253;
-    down = scale ? __uint_as_float((254 - eb) << 23) : 1.f;
-    up = scale ? __uint_as_float(eb << 23) : 1.f;
+    const bool scale = eb > kTop && eb <= 254;
+    down = scale ? __uint_as_float((254 + kTop - eb) << 23) : 1.f;
+    up = scale ? __uint_as_float((eb - kTop) << 23) : 1.f;
   }
-  template <class ET>
-  __device__ __forceinline__ void split(float v, uint16_t& hi, uint16_t& lo) const {
-    const float n = v * down;
-    hi = ET::from_f32(n);
-    const float rest = n - ET::to_f32(hi);
-    lo = __builtin_isfinite(rest) ? ET::from_f32(rest) : (uint16_t)0;
+  // term i to out[256 i]
+  __device__ __forceinline__ void split(float v, uint16_t* out) const {
+    float r = v * down;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const uint16_t t = kBF16 && i == 3 ? 0 : ET::from_f32(r);   // (after three bf16 terms nothing is left)
+      out[256 * i] = t;
+      r -= ET::to_f32(t);
+      if (i == 0 && !__builtin_isfinite(r)) r = 0.f;   // (an infinite or NaN v: the first term has it)
+      if (i == 1) r *= kRest;
+    }
   }
 };
+
+// B v of 16 ranks: v0 holds the terms 0 and 1, v1 the terms 2 and 3.
+template <class ET>
+__device__ __forceinline__ f32x4 times_v(bf16x8 b, bf16x8 v0, bf16x8 v1) {
+  f32x4 d = ET::mfma(b, v1, f32x4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+  for (int q = 0; q < 4; q++) d[q] *= 1.f / SplitV<ET>::kRest;
+  return ET::mfma(b, v0, d);
+}
 
 // Workgroup (16 tokens, the y-th adapter among them and every gridDim.y-th after it, 16
 // ranks): the waves split K and their sums are added in wave order.
@@ -121,10 +148,9 @@ __global__ __launch_bounds__(64 * NW) void lora_shrink_kernel(LoraArgs a) {
     m = fmaxf(m, __uint_as_float(dpp_u32<0x122>(__float_as_uint(m))));
     m = fmaxf(m, __uint_as_float(dpp_u32<0x124>(__float_as_uint(m))));
     m = fmaxf(m, __uint_as_float(dpp_u32<0x128>(__float_as_uint(m))));
-    const SplitV sv(m);
+    const SplitV<ET> sv(m);
     const size_t block = (size_t)blockIdx.x * a.rank_blocks + blockIdx.z;
-    uint16_t* out = a.hl + 512 * block + 128 * ((tid >> 3) & 1) + 8 * (tid >> 4) + (tid & 7);
-    sv.split<ET>(v, out[0], out[256]);
+    sv.split(v, a.terms + 1024 * block + 128 * ((tid >> 3) & 1) + 8 * (tid >> 4) + (tid & 7));
     if ((tid & 15) == 0) a.mul[16 * block + (tid >> 4)] = sv.up * (a.scales ? a.scales[ad] : 1.f);
   }
 }
@@ -146,7 +172,7 @@ __device__ __forceinline__ bf16x8 load_b(const LoraArgs& a, int ad, int rank, in
 // The adapters' parts of one block of 16 tokens and 16 columns from n0 that this wave adds:
 // those of the adapters wave + m NW (m < kSlots) among the tokens, in token order. The first
 // 64 ranks of their B are loaded when they are found, ahead of the pass over K; add() runs
-// one MFMA (hi and lo) per adapter and 16 ranks, kept for the lanes of the adapter's own tokens.
+// two MFMAs (the terms of v) per adapter and 16 ranks, kept for the lanes of the adapter's own tokens.
 template <class ET, int NW>
 struct ExpandBlock {
   static constexpr int kSlots = 16 / NW;
@@ -182,18 +208,19 @@ struct ExpandBlock {
 #pragma unroll
     for (int m = 0; m < kSlots; m++) {
       for (int r0 = 0; r0 < rank[m]; r0 += 64) {
-        bf16x8 vv[4];
+        bf16x8 v0[4], v1[4];
         float mul[4];
 #pragma unroll
         for (int u = 0; u < 4; u++) {
           const size_t blk = group + (r0 + 16 * u < rank[m] ? r0 / 16 + u : 0);
-          vv[u] = *reinterpret_cast<const bf16x8*>(a.hl + 512 * blk + 8 * lane);   // (tokens of other adapters: dropped)
+          v0[u] = *reinterpret_cast<const bf16x8*>(a.terms + 1024 * blk + 8 * lane);   // (tokens of other adapters: dropped)
+          v1[u] = *reinterpret_cast<const bf16x8*>(a.terms + 1024 * blk + 512 + 8 * lane);
           mul[u] = a.mul[16 * blk + (lane & 15)];
           if (r0) bv[m][u] = load_b(a, ad[m], rank[m], n0 + (lane & 15), r0 + 16 * u + 8 * ((lane >> 4) & 1));
         }
 #pragma unroll
         for (int u = 0; u < 4; u++) {
-          const f32x4 d = ET::mfma(bv[m][u], vv[u], f32x4{0.f, 0.f, 0.f, 0.f});
+          const f32x4 d = times_v<ET>(bv[m][u], v0[u], v1[u]);
           if (id == ad[m] && r0 + 16 * u < rank[m]) {
 #pragma unroll
             for (int q = 0; q < 4; q++) acc[q] += mul[u] * d[q];
@@ -214,7 +241,7 @@ struct ExpandWave {
   uint32_t left;
   int ad, rank, next;        // the walk: ranks from `next` on of adapter `ad`
   int got[kBatch];           // adapter of each pair, or -1
-  bf16x8 bv[kBatch][TQ], vv[kBatch];
+  bf16x8 bv[kBatch][TQ], v0[kBatch], v1[kBatch];
   float mul[kBatch];
 
   __device__ __forceinline__ void start(const LoraArgs& a, int t0, int lane) {
@@ -242,7 +269,8 @@ struct ExpandWave {
 #pragma unroll
       for (int j = 0; j < TQ; j++)
         bv[u][j] = load_b(a, have ? ad : 0, have ? rank : 0, n0 + 16 * j + (lane & 15), next + 8 * ((lane >> 4) & 1));
-      vv[u] = *reinterpret_cast<const bf16x8*>(a.hl + 512 * blk + 8 * lane);   // (tokens of other adapters: dropped)
+      v0[u] = *reinterpret_cast<const bf16x8*>(a.terms + 1024 * blk + 8 * lane);   // (tokens of other adapters: dropped)
+      v1[u] = *reinterpret_cast<const bf16x8*>(a.terms + 1024 * blk + 512 + 8 * lane);
       mul[u] = a.mul[16 * blk + (lane & 15)];
       next += 16;
     }
@@ -253,7 +281,7 @@ struct ExpandWave {
     for (int u = 0; u < kBatch; u++) {
 #pragma unroll
       for (int j = 0; j < TQ; j++) {
-        const f32x4 d = ET::mfma(bv[u][j], vv[u], f32x4{0.f, 0.f, 0.f, 0.f});
+        const f32x4 d = times_v<ET>(bv[u][j], v0[u], v1[u]);
         if (got[u] >= 0 && id == got[u]) {
 #pragma unroll
           for (int q = 0; q < 4; q++) acc[j][q] += mul[u] * d[q];
@@ -263,8 +291,8 @@ struct ExpandWave {
   }
 };
 
-// The same for a block of 32 tokens and TQ blocks of 32 columns on 32 x 32 x 16 MFMA: two per
-// adapter and 16 ranks (8 ranks each: hi in lanes 0..31, lo in lanes 32..63).
+// The same for a block of 32 tokens and TQ blocks of 32 columns on 32 x 32 x 16 MFMA: four per
+// adapter and 16 ranks (8 ranks and two terms of v each, one in lanes 0..31, one in 32..63).
 template <class ET, int TQ, int TP>
 __device__ __forceinline__ void lora_expand32(const LoraArgs& a, int t, int n0, int lane, f32x16 (&acc)[TQ][TP], int i) {
   const int2 info = t < a.T ? a.info[t] : make_int2(-1, 0);
@@ -277,15 +305,17 @@ __device__ __forceinline__ void lora_expand32(const LoraArgs& a, int t, int n0, 
     left &= ~(uint32_t)__ballot(id == ad);
     // two blocks of 16 ranks a turn, their loads together
     for (int rb = 0; 16 * rb < rank; rb += 2) {
-      bf16x8 v[2][2], bv[2][TQ][2];
+      bf16x8 v[2][2][2], bv[2][TQ][2];   // v: [16 ranks][terms 0, 1 or 2, 3][8 ranks]
       float mul[2];
 #pragma unroll
       for (int u = 0; u < 2; u++) {
         const bool in = 16 * (rb + u) < rank;
         const size_t blk = group + (in ? rb + u : 0);
-        const uint16_t* p = a.hl + 512 * blk + 256 * (lane >> 5) + 8 * (lane & 15);
-        v[u][0] = *reinterpret_cast<const bf16x8*>(p);   // (tokens of other adapters: dropped)
-        v[u][1] = *reinterpret_cast<const bf16x8*>(p + 128);
+        const uint16_t* p = a.terms + 1024 * blk + 256 * (lane >> 5) + 8 * (lane & 15);
+#pragma unroll
+        for (int m = 0; m < 2; m++)
+#pragma unroll
+          for (int h = 0; h < 2; h++) v[u][m][h] = *reinterpret_cast<const bf16x8*>(p + 512 * m + 128 * h);   // (tokens of other adapters: dropped)
         mul[u] = a.mul[16 * blk + (lane & 15)];
 #pragma unroll
         for (int j = 0; j < TQ; j++)
@@ -300,8 +330,12 @@ __device__ __forceinline__ void lora_expand32(const LoraArgs& a, int t, int n0, 
           f32x16 d;
 #pragma unroll
           for (int q = 0; q < 16; q++) d[q] = 0.f;
-          d = mfma32(ET{}, bv[u][j][0], v[u][0], d);
-          d = mfma32(ET{}, bv[u][j][1], v[u][1], d);
+          d = mfma32(ET{}, bv[u][j][0], v[u][1][0], d);
+          d = mfma32(ET{}, bv[u][j][1], v[u][1][1], d);
+#pragma unroll
+          for (int q = 0; q < 16; q++) d[q] *= 1.f / SplitV<ET>::kRest;
+          d = mfma32(ET{}, bv[u][j][0], v[u][0][0], d);
+          d = mfma32(ET{}, bv[u][j][1], v[u][0][1], d);
           if (id == ad) {
 #pragma unroll
             for (int q = 0; q < 16; q++) acc[j][i][q] += mul[u] * d[q];
@@ -415,7 +449,7 @@ __global__ __launch_bounds__(64 * NW) void lora_token_kernel(LoraArgs a) {
   constexpr int D = 64, kPart = 16 * (2 + NB) * D, kCopies = 2 * (2 + NB);
   __shared__ __attribute__((aligned(16))) uint16_t s_a[NW][kPart], s_b[NW][kPart];
   static_assert(sizeof(f32x4) * (1 + NB) * 64 <= sizeof(s_a[0]), "the sums fit into the slices' part");
-  __shared__ __attribute__((aligned(16))) uint16_t s_hl[NB][512];
+  __shared__ __attribute__((aligned(16))) uint16_t s_terms[NB][1024];
   __shared__ float s_mul[NB][16];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n0 = blockIdx.x * 16, t = lane & 15, n = n0 + (lane & 15);
@@ -542,11 +576,11 @@ __global__ __launch_bounds__(64 * NW) void lora_token_kernel(LoraArgs a) {
     }
     m = fmaxf(m, __shfl_xor(m, 16, 64));
     m = fmaxf(m, __shfl_xor(m, 32, 64));
-    const SplitV sv(m);
-    // (fragment order: hi or lo, ranks 0..7 or 8..15, token, rank)
-    uint16_t* out = &s_hl[b][128 * (lane >> 5) + 8 * t + 4 * ((lane >> 4) & 1)];
+    const SplitV<ET> sv(m);
+    // (fragment order: term, ranks 0..7 or 8..15, token, rank)
+    uint16_t* out = &s_terms[b][128 * (lane >> 5) + 8 * t + 4 * ((lane >> 4) & 1)];
 #pragma unroll
-    for (int q = 0; q < 4; q++) sv.split<ET>(v[q], out[q], out[256 + q]);
+    for (int q = 0; q < 4; q++) sv.split(v[q], out + q);
     if (lane < 16) s_mul[b][t] = sv.up;
   }
   __syncthreads();
@@ -554,7 +588,8 @@ __global__ __launch_bounds__(64 * NW) void lora_token_kernel(LoraArgs a) {
 #pragma unroll
   for (int b = 0; b < NB; b++) {
     if (!brank[b]) continue;
-    const f32x4 d = ET::mfma(bv[b], *reinterpret_cast<const bf16x8*>(&s_hl[b][8 * lane]), f32x4{0.f, 0.f, 0.f, 0.f});
+    const f32x4 d = times_v<ET>(bv[b], *reinterpret_cast<const bf16x8*>(&s_terms[b][8 * lane]),
+                                *reinterpret_cast<const bf16x8*>(&s_terms[b][512 + 8 * lane]));
     if (id == bad[b]) {
       const float mul = s_mul[b][t] * scale[b];
 #pragma unroll
@@ -684,7 +719,7 @@ using namespace exmoe;
 
 extern "C" size_t exmoe_lora_workspace_bytes(int T, int N, int K, int adapters, int rank_max) {
   if (lora_shape(T, N, K, adapters, rank_max)) return 0;
-  return lora_blocks(T, rank_max) * (1024 + 64) + (size_t)T * 8;
+  return lora_blocks(T, rank_max) * (2048 + 64) + (size_t)T * 8;
 }
 
 extern "C" int exmoe_lora_linear(const void* x, size_t ldx, const void* w, size_t ldw, const exmoe_lora_bank* bank,
@@ -718,8 +753,8 @@ extern "C" int exmoe_lora_linear(const void* x, size_t ldx, const void* w, size_
   a.scales = bank->scales; a.ids = adapter_ids; a.adapters = bank->adapters; a.rank_max = bank->rank_max; a.T = T;
   a.N = N; a.K = K; a.y = static_cast<uint16_t*>(y); a.vec8 = (uintptr_t)y % 8 == 0 && ldy % 4 == 0;
   a.vec16 = aligned16(y) && ldy % 8 == 0; a.rank_blocks = (bank->rank_max + 15) / 16;
-  a.hl = static_cast<uint16_t*>(workspace);
-  a.mul = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + lora_blocks(T, bank->rank_max) * 1024);
+  a.terms = static_cast<uint16_t*>(workspace);
+  a.mul = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + lora_blocks(T, bank->rank_max) * 2048);
   a.info = reinterpret_cast<int2*>(a.mul + lora_blocks(T, bank->rank_max) * 16);
   const hipError_t e = dtype == EXMOE_DTYPE_FP16 ? launch_lora<ElemFP16>(a, stream) : launch_lora<ElemBF16>(a, stream);
   return e == hipSuccess ? EXMOE_OK : hip_error(e, "exmoe_lora_linear");
