@@ -361,7 +361,8 @@ int exmoe_moe_forward_cached(const exmoe_bf16* x, const int32_t* topk_ids, const
  * Sizes: any rows >= 0, N, K >= 1 (multiples of 8 with 16-byte aligned rows run on wider
  * loads; other row lengths are copied into the workspace with padded rows where that pays),
  * 1 <= E <= 256; empty segments are allowed anywhere (exmoe_grouped_mm_wgrad
- * writes zeros for them). ld* are elements between rows, *_stride elements between
+ * writes zeros for them). Calls whose output tiles or copies need more than 2^32 threads in
+ * one launch return EXMOE_ERR_UNSUPPORTED. ld* are elements between rows, *_stride elements between
  * experts; the last axis is contiguous. Pointers need the alignment of their elements only
  * (workspace: 16 bytes). Operands share `dtype` (bf16 or fp16); out_dtype is that type or
  * fp32. Outputs must not overlap inputs.

@@ -582,6 +582,13 @@ __global__ __launch_bounds__(256) void split_sum_kernel(const float* __restrict_
 static inline int ceil_div(int a, int b) { return (int)(((long long)a + b - 1) / b); }
 constexpr long long kMaxThreads = 0xFFFFFF00ll;   // of one launch, in whole workgroups; larger calls are refused
 
+// Tiles of BP rows, at most, into which the experts' rows fall.
+static long long row_tiles(int rows, int E, int bp) { return rows / bp + (E < rows ? E : rows); }
+// Whether the bp x bq tiles of rows x Q outputs, one workgroup of that many threads each, are one launch.
+static bool tiles_fit(int rows, int Q, int E, int bp, int bq, int threads) {
+  return row_tiles(rows, E, bp) * ceil_div(Q, bq) * threads <= kMaxThreads;
+}
+
 // Parts into which the sum over an expert's rows is split: enough workgroups for the chip
 // where an expert's gradient has few tiles, at least four 64-row slices per part.
 static int wgrad_splits(int rows, int N, int K, int E) {
@@ -623,11 +630,12 @@ GroupedWorkspace grouped_workspace(int op, int rows, int N, int K, int E, int k)
   return w;
 }
 
+static size_t pack_threads(int rows, int len) { return (size_t)rows * (pad8(len) / 8); }   // of one group
+
 static hipError_t pack_rows(const uint16_t* src, size_t ld, size_t stride, int len, int rows, int groups, int src_rows,
                             const int32_t* row_index, int row_div, const int32_t* offsets, uint16_t* dst, hipStream_t s) {
   const int pad = pad8(len);
-  const size_t n = (size_t)rows * (pad / 8);
-  if (n > (size_t)kMaxThreads) return hipErrorInvalidConfiguration;
+  const size_t n = pack_threads(rows, len);
   ProfScope prof("pack_rows", s);
   EXMOE_LAUNCH(prof, pack_rows_kernel, dim3((unsigned)((n + 255) / 256), groups), dim3(256), 0, s, src, ld, stride, len, rows,
                src_rows, row_index, row_div, offsets, dst, pad);
@@ -636,9 +644,8 @@ static hipError_t pack_rows(const uint16_t* src, size_t ld, size_t stride, int l
 
 template <class ET, int MODE, int BP, int BQ, int WP, int WQ, bool ALIGNED>
 static hipError_t launch_rows(const GroupedArgs& a, const char* name, hipStream_t s) {
-  const long long max_p = a.rows / BP + (a.E < a.rows ? a.E : a.rows);
+  const long long max_p = row_tiles(a.rows, a.E, BP);
   const int qt = ceil_div(MODE == kMM ? a.N : a.K, BQ);
-  if (max_p * qt * (64 * WP * WQ) > kMaxThreads) return hipErrorInvalidConfiguration;
   ProfScope prof(name, s);
   EXMOE_LAUNCH(prof, (grouped_kernel<ET, MODE, BP, BQ, WP, WQ, ALIGNED>), dim3((unsigned)(max_p * qt)),
                dim3(64 * WP * WQ), 0, s, a, 0, qt, 1);
@@ -648,9 +655,8 @@ static hipError_t launch_rows(const GroupedArgs& a, const char* name, hipStream_
 template <class ET, int MODE, int TP, int TQ, int WP, int WQ, int D, int OCC>
 static hipError_t launch_wide(const GroupedArgs& a, const char* name, hipStream_t s) {
   constexpr int BP = 32 * TP * WP, BQ = 32 * TQ * WQ;
-  const long long max_p = a.rows / BP + (a.E < a.rows ? a.E : a.rows);
+  const long long max_p = row_tiles(a.rows, a.E, BP);
   const int qt = ceil_div(MODE == kMM ? a.N : a.K, BQ);
-  if (max_p * qt * (64 * WP * WQ) > kMaxThreads) return hipErrorInvalidConfiguration;
   ProfScope prof(name, s);
   EXMOE_LAUNCH(prof, (grouped_wide_kernel<ET, MODE, TP, TQ, WP, WQ, D, OCC>), dim3((unsigned)(max_p * qt)),
                dim3(64 * WP * WQ), 0, s, a, 0, qt, 1);
@@ -689,9 +695,8 @@ static int tile_rows(int rows, int Q, int E) {
 
 template <class ET, int TP, int TQ, int NW, int D, bool ALIGNED>
 static hipError_t launch_narrow(const GroupedArgs& a, hipStream_t s) {
-  const long long max_p = a.rows / (16 * TP) + (a.E < a.rows ? a.E : a.rows);
+  const long long max_p = row_tiles(a.rows, a.E, 16 * TP);
   const int qt = ceil_div(a.N, 16 * TQ);
-  if (max_p * qt * (64 * NW) > kMaxThreads) return hipErrorInvalidConfiguration;
   ProfScope prof("grouped_mm", s);
   EXMOE_LAUNCH(prof, (grouped_narrow_kernel<ET, TP, TQ, NW, D, ALIGNED>), dim3((unsigned)(max_p * qt)), dim3(64 * NW), 0, s, a, qt);
   return hipGetLastError();
@@ -699,9 +704,8 @@ static hipError_t launch_narrow(const GroupedArgs& a, hipStream_t s) {
 
 template <class ET, int TP, int NW>
 static hipError_t launch_narrow_dgrad(const GroupedArgs& a, hipStream_t s) {
-  const long long max_p = a.rows / (16 * TP) + (a.E < a.rows ? a.E : a.rows);
+  const long long max_p = row_tiles(a.rows, a.E, 16 * TP);
   const int qt = ceil_div(a.K, 64);
-  if (max_p * qt * (64 * NW) > kMaxThreads) return hipErrorInvalidConfiguration;
   ProfScope prof("grouped_dgrad", s);
   EXMOE_LAUNCH(prof, (grouped_narrow_dgrad_kernel<ET, TP, NW>), dim3((unsigned)(max_p * qt)), dim3(64 * NW), 0, s, a, qt);
   return hipGetLastError();
@@ -718,6 +722,7 @@ static bool narrow_dgrad(const GroupedArgs& a) {
 // 128-row tiles. Measured on 64 experts of 2048 x 2048, us: 2 rows per expert 83 / 117,
 // 8 rows 97 / 128, 16 rows 127 / 130, 32 rows 182 / 131. Operands of any alignment, 13 experts
 // of 517 x 1003: 10 rows 11 / 39, 39 rows 21 / 42, 60 rows 28 / 44, 630 rows 193 / 61.
+// (Where 16 x 16 blocks are more than one launch holds, 128 x 128 tiles may still fit.)
 constexpr int kNarrowRows = 16, kNarrowRowsAny = 128;
 
 // Fewer 128 x 128 tiles than half the CUs: 64 x 64 blocks whose waves split the reduction (500
@@ -738,10 +743,11 @@ template <class ET>
 static hipError_t mm_type(const GroupedArgs& a, hipStream_t s) {
   const bool al = op_aligned(a.a, a.lda, 0, a.len_a) && op_aligned(a.b, a.ldb, a.b_stride, a.len_b);
   if (!al) {
-    if (a.rows <= kNarrowRowsAny * (long long)a.E) return launch_narrow<ET, 1, 1, 8, 64, false>(a, s);
+    if (a.rows <= kNarrowRowsAny * (long long)a.E && tiles_fit(a.rows, a.N, a.E, 16, 16, 512)) return launch_narrow<ET, 1, 1, 8, 64, false>(a, s);
     return launch_rows<ET, kMM, 128, 128, 2, 2, false>(a, "grouped_mm", s);
   }
-  if (a.rows <= kNarrowRows * (long long)a.E && op_span(a.x_rows, a.lda, a.K) && op_span(16, a.ldb, a.K))
+  if (a.rows <= kNarrowRows * (long long)a.E && op_span(a.x_rows, a.lda, a.K) && op_span(16, a.ldb, a.K) &&
+      tiles_fit(a.rows, a.N, a.E, 16, 16, 256))
     return launch_narrow<ET, 1, 1, 4, 64, true>(a, s);
   if (!op_span(a.x_rows, a.lda, a.len_a) || !op_span(a.N, a.ldb, a.len_b))
     return launch_rows<ET, kMM, 128, 128, 2, 2, true>(a, "grouped_mm", s);
@@ -753,8 +759,7 @@ static hipError_t mm_type(const GroupedArgs& a, hipStream_t s) {
   return launch_wide<ET, kMM, 2, 2, 2, 2, 64, 2>(a, "grouped_mm", s);
 }
 
-// Copies the operands that need it; a then describes the copies. A launch that is too large
-// is refused before: the copies' sizes are bounded by the products' own.
+// Copies the operands that need it; a then describes the copies.
 static hipError_t pack_a_rows(GroupedArgs& a, int len, bool gather, hipStream_t s) {
   hipError_t e = pack_rows(a.a, a.lda, 0, len, a.rows, 1, gather ? a.x_rows : a.rows, gather ? a.row_index : nullptr,
                            a.row_div, nullptr, a.pack_a, s);
@@ -770,16 +775,9 @@ static hipError_t pack_weights(GroupedArgs& a, hipStream_t s) {
   return e;
 }
 
-// Whether the products after the copies fit into a launch (checked before anything runs).
-static bool packed_fits(const GroupedArgs& a, int Q) {
-  return (a.rows / 128 + (long long)(a.E < a.rows ? a.E : a.rows)) * ceil_div(Q, 128) * 256 <= kMaxThreads &&
-         (!a.flat_to_sorted || (long long)(a.rows / a.k) * a.K <= kMaxThreads);
-}
-
 hipError_t launch_grouped_mm(const GroupedArgs& given, hipStream_t s) {
   GroupedArgs a = given;
   hipError_t e = hipSuccess;
-  if ((a.pack_a || a.pack_b) && !packed_fits(a, a.N)) return hipErrorInvalidConfiguration;
   if (a.pack_a) {
     if ((e = pack_a_rows(a, a.K, true, s)) != hipSuccess) return e;
     a.x_rows = a.rows;
@@ -795,7 +793,6 @@ static hipError_t dgrad_type(const GroupedArgs& a, hipStream_t s) {
   const bool al = op_aligned(a.a, a.lda, 0, a.len_a) && op_aligned(a.b, a.ldb, a.b_stride, a.len_b);
   GroupedArgs r = a;
   if (a.flat_to_sorted) {
-    if ((long long)(a.rows / a.k) * a.K > kMaxThreads) return hipErrorInvalidConfiguration;
     r.out = a.ws;
     r.vec = a.K % 4 == 0;
     r.ldo = (size_t)a.K;
@@ -830,7 +827,6 @@ static hipError_t dgrad_type(const GroupedArgs& a, hipStream_t s) {
 hipError_t launch_grouped_dgrad(const GroupedArgs& given, hipStream_t s) {
   GroupedArgs a = given;
   hipError_t e = hipSuccess;
-  if ((a.pack_a || a.pack_b) && !packed_fits(a, a.K)) return hipErrorInvalidConfiguration;
   if (a.pack_a && (e = pack_a_rows(a, a.N, false, s)) != hipSuccess) return e;
   if (a.pack_b && (e = pack_weights(a, s)) != hipSuccess) return e;
   return a.fp16 ? dgrad_type<ElemFP16>(a, s) : dgrad_type<ElemBF16>(a, s);
@@ -840,7 +836,6 @@ template <int BP, int BQ, int THREADS, class F>
 static hipError_t launch_weights(const GroupedArgs& a, hipStream_t s, int splits, F kernel) {
   const int pt = ceil_div(a.N, BP), qt = ceil_div(a.K, BQ);
   const long long grid = (long long)pt * qt * a.E * splits;
-  if (grid * THREADS > kMaxThreads) return hipErrorInvalidConfiguration;
   ProfScope prof("grouped_wgrad", s);
   EXMOE_LAUNCH(prof, kernel, dim3((unsigned)grid), dim3(THREADS), 0, s, a, pt, qt, splits);
   return hipGetLastError();
@@ -881,8 +876,6 @@ static hipError_t wgrad_type(const GroupedArgs& a, hipStream_t s) {
 hipError_t launch_grouped_wgrad(const GroupedArgs& given, hipStream_t s) {
   GroupedArgs a = given;
   hipError_t e = hipSuccess;
-  if ((a.pack_a || a.pack_b) && (long long)a.E * ceil_div(a.N, 128) * ceil_div(a.K, 128) * wgrad_splits(a.rows, a.N, a.K, a.E) * 256 > kMaxThreads)
-    return hipErrorInvalidConfiguration;
   if (a.rows > 0 && a.pack_a && (e = pack_a_rows(a, a.N, false, s)) != hipSuccess) return e;
   if (a.rows > 0 && a.pack_b) {
     e = pack_rows(a.b, a.ldb, 0, a.K, a.rows, 1, a.x_rows, a.row_index, a.row_div, nullptr, a.pack_b, s);
@@ -894,6 +887,23 @@ hipError_t launch_grouped_wgrad(const GroupedArgs& given, hipStream_t s) {
     a.row_div = 1;
   }
   return a.fp16 ? wgrad_type<ElemFP16>(a, s) : wgrad_type<ElemBF16>(a, s);
+}
+
+// Whether each launch of a call holds its threads: the copies, the products' last resort (128 x
+// 128 tiles, and 256 x 256 on twice the threads) and the sums. Checked before anything runs.
+static bool call_fits(int op, int rows, int N, int K, int E, int k, const GroupedWorkspace& need) {
+  const size_t most = (size_t)kMaxThreads;
+  if (op == EXMOE_GROUPED_WGRAD) {
+    const long long wide = (long long)E * ceil_div(N, 256) * ceil_div(K, 256) * 512,
+                    tiles = (long long)E * ceil_div(N, 128) * ceil_div(K, 128) * wgrad_splits(rows, N, K, E) * 256;
+    return wide <= kMaxThreads && tiles <= kMaxThreads && (!need.pack_a || pack_threads(rows, N) <= most) &&
+           (!need.pack_b || pack_threads(rows, K) <= most);
+  }
+  const int Q = op == EXMOE_GROUPED_MM ? N : K;
+  if (!tiles_fit(rows, Q, E, 128, 128, 256) || !tiles_fit(rows, Q, E, 256, 256, 512)) return false;
+  if (need.pack_a && pack_threads(rows, op == EXMOE_GROUPED_MM ? K : N) > most) return false;
+  if (need.pack_b && pack_threads(N, K) > most) return false;
+  return k == 0 || (size_t)(rows / k) * (K % 4 == 0 ? K / 4 : K) <= most;
 }
 
 }  // namespace exmoe
@@ -940,11 +950,11 @@ static int check_ws(size_t need, const void* ws, size_t ws_bytes) {
   return EXMOE_OK;
 }
 
-static int launched(hipError_t e, const char* what) {
-  if (e == hipSuccess) return EXMOE_OK;
-  if (e == hipErrorInvalidConfiguration) return set_error(EXMOE_ERR_UNSUPPORTED, "%s: too many output tiles for one launch", what);
-  return hip_error(e, what);
+static int check_size(bool fits, const char* what) {
+  return fits ? EXMOE_OK : set_error(EXMOE_ERR_UNSUPPORTED, "%s: more output tiles or copied elements than one launch holds", what);
 }
+
+static int launched(hipError_t e, const char* what) { return e == hipSuccess ? EXMOE_OK : hip_error(e, what); }
 
 // Whether rows of outputs can be stored 16 bytes at a time.
 static int vec_store(const void* p, size_t ld, size_t stride, int out_f32) {
@@ -991,6 +1001,7 @@ extern "C" int exmoe_grouped_mm(const void* x, size_t ldx, int x_rows, const int
   EXMOE_TRY(check_int32("row_index", row_index, true));
   EXMOE_TRY(check_int32("expert_offsets", expert_offsets, false));
   const GroupedWorkspace need = grouped_workspace(EXMOE_GROUPED_MM, rows, N, K, E, 0);
+  EXMOE_TRY(check_size(call_fits(EXMOE_GROUPED_MM, rows, N, K, E, 0, need), "exmoe_grouped_mm"));
   EXMOE_TRY(check_ws(need.total(), workspace, ws_bytes));
   GroupedArgs a{};
   a.a = static_cast<const uint16_t*>(x); a.b = static_cast<const uint16_t*>(w); a.lda = ldx; a.ldb = ldw;
@@ -1017,6 +1028,7 @@ extern "C" int exmoe_grouped_mm_dgrad(const void* dy, size_t lddy, const int32_t
   EXMOE_TRY(check_int32("expert_offsets", expert_offsets, false));
   EXMOE_TRY(check_int32("flat_to_sorted", flat_to_sorted, true));
   const GroupedWorkspace need = grouped_workspace(EXMOE_GROUPED_DGRAD, rows, N, K, E, flat_to_sorted ? k : 0);
+  EXMOE_TRY(check_size(call_fits(EXMOE_GROUPED_DGRAD, rows, N, K, E, flat_to_sorted ? k : 0, need), "exmoe_grouped_mm_dgrad"));
   EXMOE_TRY(check_ws(need.total(), workspace, ws_bytes));
   GroupedArgs a{};
   a.a = static_cast<const uint16_t*>(dy); a.b = static_cast<const uint16_t*>(w); a.lda = lddy; a.ldb = ldw;
@@ -1046,6 +1058,7 @@ extern "C" int exmoe_grouped_mm_wgrad(const void* dy, size_t lddy, const void* x
   EXMOE_TRY(check_int32("row_index", row_index, true));
   EXMOE_TRY(check_int32("expert_offsets", expert_offsets, false));
   const GroupedWorkspace need = grouped_workspace(EXMOE_GROUPED_WGRAD, rows, N, K, E, 0);
+  EXMOE_TRY(check_size(call_fits(EXMOE_GROUPED_WGRAD, rows, N, K, E, 0, need), "exmoe_grouped_mm_wgrad"));
   EXMOE_TRY(check_ws(need.total(), workspace, ws_bytes));
   GroupedArgs a{};
   a.a = static_cast<const uint16_t*>(dy); a.b = static_cast<const uint16_t*>(x); a.lda = lddy; a.ldb = ldx;
