@@ -365,7 +365,8 @@ int exmoe_moe_forward_cached(const exmoe_bf16* x, const int32_t* topk_ids, const
  * one launch return EXMOE_ERR_UNSUPPORTED. ld* are elements between rows, *_stride elements between
  * experts; the last axis is contiguous. Pointers need the alignment of their elements only
  * (workspace: 16 bytes). Operands share `dtype` (bf16 or fp16); out_dtype is that type or
- * fp32. Outputs must not overlap inputs.
+ * fp32. An output or workspace that shares bytes with another operand is refused (it may lie
+ * between another's rows).
  * Offsets are read on the device and clamped to [0, rows]. Rows of y and dx outside every
  * segment are left as they are; with flat_to_sorted every token is written, and an entry
  * outside the segments (-1 of an ungrouped row) adds nothing. A row_index that leads
@@ -414,7 +415,8 @@ int exmoe_grouped_mm_wgrad(const void* dy, size_t lddy, const void* x, size_t ld
  * rows of x, w, a and b 16-byte aligned (ld and strides multiples of 8, ld <= 2^24); N is any
  * size. The bank's adapters lie a_stride / b_stride elements apart; ranks int32 [adapters]
  * (clamped to [0, rank_max]; what a and b hold past an adapter's rank is not used) and scales
- * fp32 [adapters] are device arrays or NULL (rank_max, 1). y must not overlap the inputs.
+ * fp32 [adapters] are device arrays or NULL (rank_max, 1). A y or workspace that shares bytes
+ * with another operand is refused (it may lie between another's rows).
  * Workspace: exmoe_lora_workspace_bytes bytes, no initialization, not kept; calls that
  * overlap in time must not share one. Equal calls give equal bits.
  * ---------------------------------------------------------------------------------- */

@@ -11,6 +11,7 @@
 
 #include "exmoe.h"
 #include "gemm_wide.h"
+#include "overlap.h"
 
 namespace exmoe {
 
@@ -1003,6 +1004,11 @@ extern "C" int exmoe_grouped_mm(const void* x, size_t ldx, int x_rows, const int
   const GroupedWorkspace need = grouped_workspace(EXMOE_GROUPED_MM, rows, N, K, E, 0);
   EXMOE_TRY(check_size(call_fits(EXMOE_GROUPED_MM, rows, N, K, E, 0, need), "exmoe_grouped_mm"));
   EXMOE_TRY(check_ws(need.total(), workspace, ws_bytes));
+  const MemRows mx = mem_matrix("x", x, row_index ? x_rows : rows, ldx, K, 2), mw = mem_matrices("w", w, E, w_stride, N, ldw, K, 2),
+                mi = mem_flat("row_index", row_index, (size_t)rows * 4), mo = mem_flat("expert_offsets", expert_offsets, (E + 1) * 4),
+                my = mem_matrix("y", y, rows, ldy, N, ob);
+  EXMOE_TRY(check_apart(my, {mx, mw, mi, mo}));
+  EXMOE_TRY(check_apart(mem_flat("workspace", workspace, need.total()), {mx, mw, mi, mo, my}));
   GroupedArgs a{};
   a.a = static_cast<const uint16_t*>(x); a.b = static_cast<const uint16_t*>(w); a.lda = ldx; a.ldb = ldw;
   a.b_stride = w_stride; a.offsets = expert_offsets; a.row_index = row_index; a.row_div = row_div; a.x_rows = x_rows;
@@ -1030,6 +1036,12 @@ extern "C" int exmoe_grouped_mm_dgrad(const void* dy, size_t lddy, const int32_t
   const GroupedWorkspace need = grouped_workspace(EXMOE_GROUPED_DGRAD, rows, N, K, E, flat_to_sorted ? k : 0);
   EXMOE_TRY(check_size(call_fits(EXMOE_GROUPED_DGRAD, rows, N, K, E, flat_to_sorted ? k : 0, need), "exmoe_grouped_mm_dgrad"));
   EXMOE_TRY(check_ws(need.total(), workspace, ws_bytes));
+  const MemRows md = mem_matrix("dy", dy, rows, lddy, N, 2), mw = mem_matrices("w", w, E, w_stride, N, ldw, K, 2),
+                mi = mem_flat("flat_to_sorted", flat_to_sorted, (size_t)rows * 4),
+                mo = mem_flat("expert_offsets", expert_offsets, (E + 1) * 4),
+                mx = mem_matrix("dx", dx, flat_to_sorted ? rows / k : rows, lddx, K, ob);
+  EXMOE_TRY(check_apart(mx, {md, mw, mi, mo}));
+  EXMOE_TRY(check_apart(mem_flat("workspace", workspace, need.total()), {md, mw, mi, mo, mx}));
   GroupedArgs a{};
   a.a = static_cast<const uint16_t*>(dy); a.b = static_cast<const uint16_t*>(w); a.lda = lddy; a.ldb = ldw;
   a.b_stride = w_stride; a.offsets = expert_offsets; a.row_div = 1; a.x_rows = rows; a.rows = rows; a.N = N; a.K = K;
@@ -1060,6 +1072,11 @@ extern "C" int exmoe_grouped_mm_wgrad(const void* dy, size_t lddy, const void* x
   const GroupedWorkspace need = grouped_workspace(EXMOE_GROUPED_WGRAD, rows, N, K, E, 0);
   EXMOE_TRY(check_size(call_fits(EXMOE_GROUPED_WGRAD, rows, N, K, E, 0, need), "exmoe_grouped_mm_wgrad"));
   EXMOE_TRY(check_ws(need.total(), workspace, ws_bytes));
+  const MemRows md = mem_matrix("dy", dy, rows, lddy, N, 2), mx = mem_matrix("x", x, rows == 0 ? 0 : row_index ? x_rows : rows, ldx, K, 2),
+                mi = mem_flat("row_index", row_index, (size_t)rows * 4), mo = mem_flat("expert_offsets", expert_offsets, (E + 1) * 4),
+                mw = mem_matrices("dw", dw, E, dw_stride, N, lddw, K, ob);
+  EXMOE_TRY(check_apart(mw, {md, mx, mi, mo}));
+  EXMOE_TRY(check_apart(mem_flat("workspace", workspace, need.total()), {md, mx, mi, mo, mw}));
   GroupedArgs a{};
   a.a = static_cast<const uint16_t*>(dy); a.b = static_cast<const uint16_t*>(x); a.lda = lddy; a.ldb = ldx;
   a.offsets = expert_offsets; a.row_index = row_index; a.row_div = row_div; a.x_rows = x_rows; a.rows = rows; a.N = N;

@@ -21,6 +21,7 @@
 
 #include "exmoe.h"
 #include "gemm_wide.h"
+#include "overlap.h"
 
 namespace exmoe {
 
@@ -746,6 +747,14 @@ extern "C" int exmoe_lora_linear(const void* x, size_t ldx, const void* w, size_
   if (!workspace || ws_bytes < need)
     return set_error(EXMOE_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace ? ws_bytes : 0);
   if (!aligned16(workspace)) return set_error(EXMOE_ERR_INVALID_ARGUMENT, "workspace must be 16-byte aligned");
+  const size_t L = (size_t)bank->adapters, R = (size_t)bank->rank_max;
+  const MemRows mx = mem_matrix("x", x, T, ldx, K, 2), mw = mem_matrix("w", w, N, ldw, K, 2),
+                ma = mem_matrices("bank->a", bank->a, L, bank->a_stride, R, bank->lda, K, 2),
+                mb = mem_matrices("bank->b", bank->b, L, bank->b_stride, N, bank->ldb, R, 2),
+                mr = mem_flat("bank->ranks", bank->ranks, L * 4), ms = mem_flat("bank->scales", bank->scales, L * 4),
+                mi = mem_flat("adapter_ids", adapter_ids, (size_t)T * 4), my = mem_matrix("y", y, T, ldy, N, 2);
+  if ((st = check_apart(my, {mx, mw, ma, mb, mr, ms, mi}))) return st;
+  if ((st = check_apart(mem_flat("workspace", workspace, need), {mx, mw, ma, mb, mr, ms, mi, my}))) return st;
   LoraArgs a{};
   a.x = static_cast<const uint16_t*>(x); a.w = static_cast<const uint16_t*>(w); a.ldx = ldx; a.ldw = ldw; a.ldy = ldy;
   a.a = static_cast<const uint16_t*>(bank->a); a.b = static_cast<const uint16_t*>(bank->b); a.lda = bank->lda;
