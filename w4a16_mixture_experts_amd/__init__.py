@@ -470,6 +470,12 @@ def _same(name: str, t, dtype, dev: int):
         raise ValueError(f"{name} must be {dtype} on GPU {dev}")
 
 
+def _no_gradient():
+    if _torch().is_grad_enabled():
+        raise ValueError("a tensor requires a gradient, and this call records none: pass it detached or call under "
+                         "torch.no_grad() (an autograd function around grouped_mm calls grouped_mm_dgrad and grouped_mm_wgrad)")
+
+
 def grouped_mm_workspace_bytes(op: int, rows: int, N: int, K: int, E: int, k: int = 0) -> int:
     return _lib.exmoe_grouped_mm_workspace_bytes(op, rows, N, K, E, k)
 
@@ -480,7 +486,10 @@ def grouped_mm(x, w, offsets, row_index=None, row_div: int = 1, out_dtype=None, 
     x [x_rows, K], w [E, N, K] (both bf16 or both fp16, last axis contiguous), offsets int32
     [E + 1]; row_index int32 [rows] with src(s) = row_index[s] // row_div (sorted_flat and k
     of a routed batch), or None for src(s) = s. Returns y [rows, N] in out_dtype (x's type
-    or fp32); its rows outside every segment are left as they are."""
+    or fp32); its rows outside every segment are left as they are. Records no gradient: tensors
+    that require one are refused unless gradients are off."""
+    if x.requires_grad or w.requires_grad or y is not None and y.requires_grad:
+        _no_gradient()
     ldx, ldw = _rows_ld("x", x), _rows_ld("w", w, 3)
     dev, dtype = x.get_device(), x.dtype
     _same("w", w, dtype, dev)
@@ -500,7 +509,10 @@ def grouped_mm(x, w, offsets, row_index=None, row_div: int = 1, out_dtype=None, 
 
 def grouped_mm_dgrad(dy, w, offsets, flat_to_sorted=None, k: int = 1, out_dtype=None, dx=None, workspace=None):
     """Gradient of grouped_mm with respect to x: dx[s, :] = dy[s, :] @ w[e] per row, or, with
-    flat_to_sorted int32 [T * k], summed over the k rows of each token (dx [T, K])."""
+    flat_to_sorted int32 [T * k], summed over the k rows of each token (dx [T, K]). Records no
+    gradient, as grouped_mm."""
+    if dy.requires_grad or w.requires_grad or dx is not None and dx.requires_grad:
+        _no_gradient()
     lddy, ldw = _rows_ld("dy", dy), _rows_ld("w", w, 3)
     dev, dtype = dy.get_device(), dy.dtype
     _same("w", w, dtype, dev)
@@ -522,7 +534,10 @@ def grouped_mm_dgrad(dy, w, offsets, flat_to_sorted=None, k: int = 1, out_dtype=
 
 def grouped_mm_wgrad(dy, x, offsets, row_index=None, row_div: int = 1, out_dtype=None, dw=None, workspace=None):
     """Gradient of grouped_mm with respect to w: dw[e] = sum over its rows of dy[s]^T x[src(s)],
-    zeros for an expert without rows. out_dtype defaults to fp32."""
+    zeros for an expert without rows. out_dtype defaults to fp32. Records no gradient, as
+    grouped_mm."""
+    if dy.requires_grad or x.requires_grad or dw is not None and dw.requires_grad:
+        _no_gradient()
     lddy, ldx = _rows_ld("dy", dy), _rows_ld("x", x)
     dev, dtype = dy.get_device(), dy.dtype
     _same("x", x, dtype, dev)
@@ -569,7 +584,11 @@ def lora_workspace_bytes(T: int, N: int, K: int, adapters: int, rank_max: int) -
 
 def lora_linear(x, w, bank: LoraBank, ids, y=None, workspace=None):
     """y[t] = w @ x[t] + scale * b[id] @ (a[id] @ x[t]) with id = ids[t] (int32 [T]; outside
-    [0, L): no adapter). w [N, K], or None: the adapters' part is added to y in place."""
+    [0, L): no adapter). w [N, K], or None: the adapters' part is added to y in place. Records no
+    gradient: tensors that require one are refused unless gradients are off."""
+    if (x.requires_grad or bank.a.requires_grad or bank.b.requires_grad or w is not None and w.requires_grad
+            or y is not None and y.requires_grad):
+        _no_gradient()
     ldx = _rows_ld("x", x)
     T, K = x.shape
     dev, dtype = x.get_device(), x.dtype
