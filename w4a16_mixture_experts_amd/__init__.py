@@ -419,10 +419,6 @@ def _rows_ld(name: str, t, ndim: int = 2) -> int:
     return stride[-2] if shape[-2] > 1 else shape[-1]   # (the stride of a single row means nothing)
 
 
-def _expert_stride(t, ld: int) -> int:
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * ld)
-
-
 def _int32(name: str, t, dev: int, numel: Optional[int] = None):
     if t is None:
         return None
@@ -502,7 +498,7 @@ def grouped_mm(x, w, offsets, row_index=None, row_div: int = 1, out_dtype=None, 
     y = _result("y", y, (rows, N), out_dtype, dev, x)
     ws, ws_bytes, _keep = _scratch(workspace, lambda: grouped_mm_workspace_bytes(GROUPED_MM, rows, N, K, E), dev)
     _run_on(dev, _lib.exmoe_grouped_mm, x.data_ptr(), ldx, x_rows, _int32("row_index", row_index, dev), row_div,
-            _int32("offsets", offsets, dev, E + 1), w.data_ptr(), ldw, _expert_stride(w, ldw), rows, N, K, E,
+            _int32("offsets", offsets, dev, E + 1), w.data_ptr(), ldw, w.stride(0), rows, N, K, E,
             _dtype_code(dtype), _dtype_code(out_dtype), y.data_ptr(), _rows_ld("y", y), ws, ws_bytes)
     return y
 
@@ -527,7 +523,7 @@ def grouped_mm_dgrad(dy, w, offsets, flat_to_sorted=None, k: int = 1, out_dtype=
     ws, ws_bytes, _keep = _scratch(
         workspace, lambda: grouped_mm_workspace_bytes(GROUPED_DGRAD, rows, N, K, E, 0 if flat_to_sorted is None else k), dev)
     _run_on(dev, _lib.exmoe_grouped_mm_dgrad, dy.data_ptr(), lddy, _int32("offsets", offsets, dev, E + 1), w.data_ptr(),
-            ldw, _expert_stride(w, ldw), _int32("flat_to_sorted", flat_to_sorted, dev, rows), k, rows, N, K, E,
+            ldw, w.stride(0), _int32("flat_to_sorted", flat_to_sorted, dev, rows), k, rows, N, K, E,
             _dtype_code(dtype), _dtype_code(out_dtype), dx.data_ptr(), _rows_ld("dx", dx), ws, ws_bytes)
     return dx
 
@@ -552,7 +548,7 @@ def grouped_mm_wgrad(dy, x, offsets, row_index=None, row_div: int = 1, out_dtype
     ws, ws_bytes, _keep = _scratch(workspace, lambda: grouped_mm_workspace_bytes(GROUPED_WGRAD, rows, N, K, E), dev)
     _run_on(dev, _lib.exmoe_grouped_mm_wgrad, dy.data_ptr(), lddy, x.data_ptr(), ldx, x_rows,
             _int32("row_index", row_index, dev, rows), row_div, _int32("offsets", offsets, dev, E + 1), rows, N, K, E,
-            _dtype_code(dtype), _dtype_code(out_dtype), dw.data_ptr(), lddw, _expert_stride(dw, lddw), ws, ws_bytes)
+            _dtype_code(dtype), _dtype_code(out_dtype), dw.data_ptr(), lddw, dw.stride(0), ws, ws_bytes)
     return dw
 
 
@@ -573,7 +569,7 @@ class LoraBank:
                                    or not scales.is_contiguous() or scales.numel() != L):
             raise ValueError(f"scales must be a contiguous float32 tensor of {L} on GPU {dev}")
         self.a, self.b, self.ranks, self.scales = a, b, ranks, scales      # kept alive
-        self.c = LoraBankC(a.data_ptr(), lda, _expert_stride(a, lda), b.data_ptr(), ldb, _expert_stride(b, ldb),
+        self.c = LoraBankC(a.data_ptr(), lda, a.stride(0), b.data_ptr(), ldb, b.stride(0),
                            _int32("ranks", ranks, dev, L), _ptr(scales), L, R)
         self.ref = ctypes.byref(self.c)
 

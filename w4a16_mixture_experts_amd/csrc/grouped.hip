@@ -931,6 +931,7 @@ static int check_matrix(const char* name, const void* p, size_t ld, int cols, in
   return EXMOE_OK;
 }
 
+// (the stride of a single expert means nothing)
 static int check_experts(const char* name, size_t ld, size_t stride, int N, int K, int E) {
   if (E > 1 && stride < (size_t)(N - 1) * ld + K)
     return set_error(EXMOE_ERR_INVALID_ARGUMENT, "%s: expert stride %zu smaller than a matrix", name, stride);
@@ -1011,7 +1012,7 @@ extern "C" int exmoe_grouped_mm(const void* x, size_t ldx, int x_rows, const int
   EXMOE_TRY(check_apart(mem_flat("workspace", workspace, need.total()), {mx, mw, mi, mo, my}));
   GroupedArgs a{};
   a.a = static_cast<const uint16_t*>(x); a.b = static_cast<const uint16_t*>(w); a.lda = ldx; a.ldb = ldw;
-  a.b_stride = w_stride; a.offsets = expert_offsets; a.row_index = row_index; a.row_div = row_div; a.x_rows = x_rows;
+  a.b_stride = E > 1 ? w_stride : 0; a.offsets = expert_offsets; a.row_index = row_index; a.row_div = row_div; a.x_rows = x_rows;
   a.rows = rows; a.N = N; a.K = K; a.E = E; a.out = y; a.ldo = ldy; a.fp16 = dtype == EXMOE_DTYPE_FP16;
   a.out_f32 = ob == 4; a.vec = vec_store(y, ldy, 0, a.out_f32); a.len_a = a.len_b = K;
   set_workspace(a, need, workspace);
@@ -1044,7 +1045,7 @@ extern "C" int exmoe_grouped_mm_dgrad(const void* dy, size_t lddy, const int32_t
   EXMOE_TRY(check_apart(mem_flat("workspace", workspace, need.total()), {md, mw, mi, mo, mx}));
   GroupedArgs a{};
   a.a = static_cast<const uint16_t*>(dy); a.b = static_cast<const uint16_t*>(w); a.lda = lddy; a.ldb = ldw;
-  a.b_stride = w_stride; a.offsets = expert_offsets; a.row_div = 1; a.x_rows = rows; a.rows = rows; a.N = N; a.K = K;
+  a.b_stride = E > 1 ? w_stride : 0; a.offsets = expert_offsets; a.row_div = 1; a.x_rows = rows; a.rows = rows; a.N = N; a.K = K;
   a.E = E; a.out = dx; a.ldo = lddx; a.fp16 = dtype == EXMOE_DTYPE_FP16; a.out_f32 = ob == 4;
   a.vec = vec_store(dx, lddx, 0, a.out_f32); a.flat_to_sorted = flat_to_sorted; a.k = k; a.len_a = N;
   a.len_b = K;
@@ -1080,8 +1081,8 @@ extern "C" int exmoe_grouped_mm_wgrad(const void* dy, size_t lddy, const void* x
   GroupedArgs a{};
   a.a = static_cast<const uint16_t*>(dy); a.b = static_cast<const uint16_t*>(x); a.lda = lddy; a.ldb = ldx;
   a.offsets = expert_offsets; a.row_index = row_index; a.row_div = row_div; a.x_rows = x_rows; a.rows = rows; a.N = N;
-  a.K = K; a.E = E; a.out = dw; a.ldo = lddw; a.o_stride = dw_stride; a.fp16 = dtype == EXMOE_DTYPE_FP16;
-  a.out_f32 = ob == 4; a.vec = vec_store(dw, lddw, dw_stride, a.out_f32); a.len_a = N; a.len_b = K;
+  a.K = K; a.E = E; a.out = dw; a.ldo = lddw; a.o_stride = E > 1 ? dw_stride : 0; a.fp16 = dtype == EXMOE_DTYPE_FP16;
+  a.out_f32 = ob == 4; a.vec = vec_store(dw, lddw, a.o_stride, a.out_f32); a.len_a = N; a.len_b = K;
   set_workspace(a, need, workspace);
   return launched(launch_grouped_wgrad(a, stream), "exmoe_grouped_mm_wgrad");
 }

@@ -734,9 +734,10 @@ extern "C" int exmoe_lora_linear(const void* x, size_t ldx, const void* w, size_
   if (T == 0) return EXMOE_OK;
   if ((st = check_rows16("x", x, ldx, 0, K))) return st;
   if (w && (st = check_rows16("w", w, ldw, 0, K))) return st;
-  if ((st = check_rows16("bank->a", bank->a, bank->lda, bank->a_stride, K))) return st;
-  if ((st = check_rows16("bank->b", bank->b, bank->ldb, bank->b_stride, bank->rank_max))) return st;
-  if (bank->adapters > 1 && (bank->a_stride < (size_t)(bank->rank_max - 1) * bank->lda + K ||
+  const bool many = bank->adapters > 1;   // (the stride of a single adapter means nothing)
+  if ((st = check_rows16("bank->a", bank->a, bank->lda, many ? bank->a_stride : 0, K))) return st;
+  if ((st = check_rows16("bank->b", bank->b, bank->ldb, many ? bank->b_stride : 0, bank->rank_max))) return st;
+  if (many && (bank->a_stride < (size_t)(bank->rank_max - 1) * bank->lda + K ||
                              bank->b_stride < (size_t)(N - 1) * bank->ldb + bank->rank_max))
     return set_error(EXMOE_ERR_INVALID_ARGUMENT, "bank: adapter stride smaller than an adapter's matrix");
   if (!y || (uintptr_t)y % 2) return set_error(EXMOE_ERR_INVALID_ARGUMENT, "y must be non-NULL and 2-byte aligned");
