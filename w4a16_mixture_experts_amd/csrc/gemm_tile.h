@@ -49,7 +49,7 @@ struct ElemFP16 {
 
 constexpr int kBK = 64;   // depth of one staged slice
 
-// Zero bytes: what a copy (16 of them) or load8_any (20) reads in place of elements past the
+// Zero bytes: what a copy (16 of them) or Any8 (20) reads in place of elements past the
 // summed axis (device globals start zeroed; never written).
 static __device__ __attribute__((aligned(16))) uint16_t g_zero16[16];
 
@@ -257,8 +257,8 @@ __device__ __forceinline__ void store4(void* out, size_t off, bool out_f32, bool
 }
 
 // ---- few rows, operands of any alignment: the waves of a workgroup split the summed axis in
-// 32-deep steps (wave w: steps w, w + NW, ...), each lane loads its fragments element by
-// element (row or column l % 16, positions 8 (l / 16) + 0..7).
+// 32-deep steps (wave w: steps w, w + NW, ...), each lane loads its fragments as the words
+// around their eight elements (Any8; row or column l % 16, positions 8 (l / 16) + 0..7).
 // xrow[i] / wrow[j]: element offset of the lane's row of each block in x / w.
 template <class ET, int TP, int TQ, int NW>
 __device__ __forceinline__ void skinny_product_any(const uint16_t* __restrict__ x, const size_t (&xrow)[TP],

@@ -53,12 +53,12 @@ template <int B, int NW, int D>
 struct WideRows {
   static constexpr int kChunks = D / 8, kRows = 64 / kChunks, kSlots = B / (kRows * NW);
   static constexpr int kReads = 1;   // LDS reads of a fragment
-  static_assert(B % (kRows * NW) == 0 && (D == 32 || (D == 64 && NW % 2 == 0) || (D == 128 && NW % 4 == 0)), "rows per slice");
+  static_assert(B % (kRows * NW) == 0 && (D == 32 || (D == 64 && NW % 2 == 0)), "rows per slice");
   buf_t buf;
   int red, wave, chunk;              // chunk: the lane's first summed position in a slice
   uint32_t voff[kSlots];
 
-  static __device__ __forceinline__ int swz(int row) { return D == 128 ? row & 15 : D == 64 ? (row >> 1) & 7 : (row >> 2) & 3; }
+  static __device__ __forceinline__ int swz(int row) { return D == 64 ? (row >> 1) & 7 : (row >> 2) & 3; }
   // row_off(i): byte offset of row i of the tile, or kNowhere for zeros
   template <class F>
   __device__ __forceinline__ void init(buf_t b, int red_, int wave_, int lane, F row_off) {
@@ -153,12 +153,12 @@ struct WideCols {
 template <int B, int D>
 struct NarrowRows {
   static constexpr int kChunks = D / 8, kRows = 64 / kChunks, kSlots = B / kRows, kElems = B * D;
-  static_assert((D == 32 || D == 64 || D == 128) && B % 16 == 0, "rows of a slice");
+  static_assert((D == 32 || D == 64) && B % 16 == 0, "rows of a slice");
   buf_t buf;
   int red, c0;               // c0: the lane's chunk in its first row
   uint32_t voff[kSlots];
 
-  static __device__ __forceinline__ int swz(int row) { return D == 128 ? row & 15 : D == 64 ? (row >> 1) & 7 : (row >> 2) & 3; }
+  static __device__ __forceinline__ int swz(int row) { return D == 64 ? (row >> 1) & 7 : (row >> 2) & 3; }
   // row_off(i): byte offset of row i, or kNowhere for zeros
   template <class F>
   __device__ __forceinline__ void init(buf_t b, int red_, int lane, F row_off) {

@@ -17,7 +17,7 @@ struct GroupedArgs {
   void* out;
   size_t ldo, o_stride;      // elements per output row, per expert (gradient of W)
   int fp16, out_f32;
-  int vec;                   // four consecutive outputs of a row can be stored at once
+  int vec;                   // 16-byte stores: the base and every row and expert of out are 16-byte aligned
   const int32_t* flat_to_sorted;   // gradient of x summed per token, or null
   int k;
   float* ws;                 // rows of the summed gradient, or the partial sums of W's

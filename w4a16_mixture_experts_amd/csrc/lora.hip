@@ -360,41 +360,31 @@ __device__ __forceinline__ void lora_store(const LoraArgs& a, int t, int n, f32x
   store4<ET>(a.y, (size_t)t * a.ldy + n, false, a.vec8, a.N - n, v);
 }
 
-// Few tokens: 16 TP tokens x 16 columns per workgroup, W streamed once per 16 TP tokens; the
-// waves split K, and the adapters among the tokens, before their sums are added.
-template <class ET, int TP, int NW, int D>
+// Few tokens: 16 tokens x 16 columns per workgroup, W streamed once per 16 tokens; the waves
+// split K, and the adapters among the tokens, before their sums are added.
+template <class ET, int NW, int D>
 __global__ __launch_bounds__(64 * NW) void lora_skinny_kernel(LoraArgs a) {
-  constexpr int kPart = 16 * (TP + 1) * D;
+  constexpr int kPart = 32 * D;
   __shared__ __attribute__((aligned(16))) uint16_t s_a[NW][kPart], s_b[NW][kPart];
-  static_assert(sizeof(f32x4) * TP * 64 <= sizeof(s_a[0]), "the sums fit into the slices' part");
+  static_assert(sizeof(f32x4) * 64 <= sizeof(s_a[0]), "the sums fit into the slices' part");
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int n0 = blockIdx.x * 16, t0 = blockIdx.y * 16 * TP;
-  f32x4 acc[1][TP];
-  int2 info[TP];
-  ExpandBlock<ET, NW> part[TP];
-#pragma unroll
-  for (int i = 0; i < TP; i++) {
-    const int t = t0 + 16 * i + (lane & 15);
-    info[i] = t < a.T ? a.info[t] : make_int2(-1, 0);
-    acc[0][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  }
-#pragma unroll
-  for (int i = 0; i < TP; i++) part[i].find(a, t0 + 16 * i, info[i], n0, wave, lane);
+  const int n0 = blockIdx.x * 16, t0 = blockIdx.y * 16, t = t0 + (lane & 15);
+  f32x4 acc[1][1] = {{{0.f, 0.f, 0.f, 0.f}}};
+  ExpandBlock<ET, NW> part;
+  part.find(a, t0, t < a.T ? a.info[t] : make_int2(-1, 0), n0, wave, lane);
   if (a.w) {
-    NarrowRows<16 * TP, D> op_x;
-    NarrowRows<16, D> op_w;
-    op_x.init(make_buf(a.x + (size_t)t0 * a.ldx, 2 * ((size_t)(min(16 * TP, a.T - t0) - 1) * a.ldx + a.K)), a.K, lane,
+    NarrowRows<16, D> op_x, op_w;
+    op_x.init(make_buf(a.x + (size_t)t0 * a.ldx, 2 * ((size_t)(min(16, a.T - t0) - 1) * a.ldx + a.K)), a.K, lane,
               [&](int i) { return t0 + i < a.T ? (uint32_t)(i * a.ldx * 2) : kNowhere; });
     op_w.init(make_buf(a.w + (size_t)n0 * a.ldw, 2 * ((size_t)(min(16, a.N - n0) - 1) * a.ldw + a.K)), a.K, lane,
               [&](int i) { return n0 + i < a.N ? (uint32_t)(i * a.ldw * 2) : kNowhere; });
-    narrow_product<ET, TP, 1, NW, D>(op_x, op_w, a.K, wave, lane, s_a[wave], s_b[wave], acc);
+    narrow_product<ET, 1, 1, NW, D>(op_x, op_w, a.K, wave, lane, s_a[wave], s_b[wave], acc);
   }
-#pragma unroll
-  for (int i = 0; i < TP; i++) part[i].add(a, n0, lane, acc[0][i]);
+  part.add(a, n0, lane, acc[0][0]);
   __syncthreads();
   f32x4 v[1];
-  skinny_reduce<TP, 1, NW>(reinterpret_cast<f32x4(*)[TP][64]>(&s_a[0][0]), acc, wave, lane, v);
-  if (wave < TP) lora_store<ET>(a, t0 + 16 * wave + (lane & 15), n0 + 4 * (lane >> 4), v[0]);
+  skinny_reduce<1, 1, NW>(reinterpret_cast<f32x4(*)[1][64]>(&s_a[0][0]), acc, wave, lane, v);
+  if (wave == 0) lora_store<ET>(a, t, n0 + 4 * (lane >> 4), v[0]);
 }
 
 // More tokens, still too few for the pipelined tiles: 16 TP tokens x 16 TQ columns per workgroup,
@@ -627,11 +617,10 @@ __global__ __launch_bounds__(64 * WP * WQ, OCC) void lora_wide_kernel(LoraArgs a
 // index blocks of 16 tokens and 16 ranks
 static inline size_t lora_blocks(int T, int rank_max) { return (size_t)((T + 15) / 16) * ((rank_max + 15) / 16); }
 
-template <class ET, int TP, int NW, int D>
+template <class ET, int NW, int D>
 static hipError_t launch_skinny(const LoraArgs& a, hipStream_t s) {
   ProfScope prof("lora_linear", s);
-  EXMOE_LAUNCH(prof, (lora_skinny_kernel<ET, TP, NW, D>), dim3((a.N + 15) / 16, (a.T + 16 * TP - 1) / (16 * TP)),
-               dim3(64 * NW), 0, s, a);
+  EXMOE_LAUNCH(prof, (lora_skinny_kernel<ET, NW, D>), dim3((a.N + 15) / 16, (a.T + 15) / 16), dim3(64 * NW), 0, s, a);
   return hipGetLastError();
 }
 template <class ET, int TP, int TQ>
@@ -690,7 +679,7 @@ static hipError_t launch_lora(const LoraArgs& a, hipStream_t s) {
   // N = 64 (244) 21 / 29; 100 tokens of 8 requests, N = 2048 (256) 15 / 20, 128 of 128 28 / 27.
   if (a.T > 32 && blocks >= 100) return launch_mid<ET, 4, 4>(a, s);
   if (a.T > 64 && (long long)((a.T + 31) / 32) * ((a.N + 31) / 32) >= 100) return launch_mid<ET, 2, 2>(a, s);
-  return launch_skinny<ET, 1, 8, 64>(a, s);
+  return launch_skinny<ET, 8, 64>(a, s);
 }
 
 static int lora_shape(int T, int N, int K, int adapters, int rank_max) {
