@@ -78,12 +78,12 @@ __device__ __forceinline__ int nth_adapter(int id, int j) {
 template <class ET>
 struct SplitV {
   static constexpr bool kBF16 = std::is_same_v<ET, ElemBF16>;
-  static constexpr uint32_t kTop = kBF16 ? 1 : 14;
+  static constexpr uint32_t kTop = kBF16 ? 0 : 14;
   static constexpr float kRest = kBF16 ? 1.f : 8388608.f;
   float down, up;   // the power of two and its inverse; 1 where nothing finite and normal is there
   __device__ __forceinline__ explicit SplitV(float m) {
     const uint32_t eb = __float_as_uint(m) >> 23;
-    const bool scale = eb > kTop && eb <= 254;
+    const bool scale = eb > kTop && eb <= (kBF16 ? 253 : 254);
     down = scale ? __uint_as_float((254 + kTop - eb) << 23) : 1.f;
     up = scale ? __uint_as_float((eb - kTop) << 23) : 1.f;
   }
