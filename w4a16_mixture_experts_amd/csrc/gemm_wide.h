@@ -291,6 +291,10 @@ struct TileOut {
 // row_bytes(value) makes its byte offset (or kNowhere); both for r < red only.
 // adjust(i, p, acc): changes the sums of row block i (lane's row p) before they are stored;
 // out_row(p): row of the output.
+// An output's whole sum (of its part, where a gradient of W is split) is one chain of MFMAs in an
+// fp32 accumulator: relative error against 64 bits over 8192 summed positions 5.7e-7 (mixed signs)
+// and 4.7e-7 (all positive), 65536 rows of a gradient of W 1.2e-6 and 7e-7; the installed BLAS in
+// fp32 9.5e-7, 1.3e-6, 3.5e-6 and 4.5e-6.
 // 256 x 256 tiles (4, 2, 2, 4, 64): 8192 x 8192 x 8192 bf16 in 829 us, 1.33 PFLOP/s; MFMA
 // busy 80% of the cycles at the about 1.5 GHz that the chip sustains under it, the rest is
 // waiting for copies at the barrier. Slices half as deep in four buffers: 909 us (twice the

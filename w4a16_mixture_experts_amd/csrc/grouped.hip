@@ -606,6 +606,7 @@ static inline size_t align16(size_t n) { return (n + 15) & ~(size_t)15; }
 // Rows per expert from which the forward product copies operands with odd row lengths. Without
 // and with copies, us: 22 experts of 3831 x 641, 16 rows 73 / 93, 30 rows 108 / 95, 41 rows 142 /
 // 96, 84 rows 262 / 104; 13 experts of 517 x 1003, 31 rows 19 / 23, 39 rows 22 / 24, 60 rows 27 / 24.
+// Skewed (Zipf), the 22 experts: 9 rows 56 / 91, 16 rows 73 / 92, 30 rows 107 / 97, 41 rows 138 / 96.
 constexpr int kPackRows = 32;
 
 // Operands whose rows are no multiple of 16 bytes long are copied with padded rows first, so
@@ -685,8 +686,9 @@ static bool sum_span(size_t n, size_t ld, int len) { return ld < kMaxSpan && op_
 //   256   137 / 168   142 / 167   146 / 168   148 / 172   201 / 214   219    223    232
 //   320                                       150 / 183   164 / 193   190    223    241
 // The gradient of x, 200 rows: 208 / 165 / 173 on 128, 256, 320; 256 rows, skewed: 245 / 232 on
-// 256, 320. From 512 rows on 256 and 320 are within 5% of each other; 8 experts of 14336 x 4096
-// with 1024 rows each: 1096 / 879 / 864 on 128, 256, 320; one of 8192 x 8192 846 / 924 on 256, 320.
+// 256, 320. From 512 rows on 256 and 320 are within 9% of each other, either way: 8 experts of
+// 14336 x 4096 with 1024 rows each 1096 / 879 / 864 on 128, 256, 320; one of 8192 x 8192 846 / 924 on
+// 256, 320.
 // The large tiles need to give every compute unit one.
 static int tile_rows(int rows, int Q, int E) {
   const int each = rows / E;
@@ -722,7 +724,10 @@ static bool narrow_dgrad(const GroupedArgs& a) {
 // Rows per expert up to which the forward product runs on 16-row blocks (narrow) instead of
 // 128-row tiles. Measured on 64 experts of 2048 x 2048, us: 2 rows per expert 83 / 117,
 // 8 rows 97 / 128, 16 rows 127 / 130, 32 rows 182 / 131. Operands of any alignment, 13 experts
-// of 517 x 1003: 10 rows 11 / 39, 39 rows 21 / 42, 60 rows 28 / 44, 630 rows 193 / 61.
+// of 517 x 1003: 10 rows 11 / 39, 39 rows 21 / 42, 60 rows 28 / 44, 630 rows 193 / 61. Skewed (Zipf),
+// 2048 x 2048: 64 experts, 2 rows on average 67 / 99, 8 rows 102 / 123, 16 rows 127 / 130; 128 experts,
+// 4 rows 146 / 155, 16 rows 246 / 196 (the largest expert's W is read once per 16 of its rows; the
+// host knows the average alone).
 // (Where 16 x 16 blocks are more than one launch holds, 128 x 128 tiles may still fit.)
 constexpr int kNarrowRows = 16, kNarrowRowsAny = 128;
 
