@@ -358,7 +358,7 @@ int exmoe_moe_forward_cached(const exmoe_bf16* x, const int32_t* topk_ids, const
  * when row_index is NULL. Products of 16-bit operands are summed in fp32 and rounded once
  * (to nearest even) when the output is 16 bits wide.
  *
- * Sizes: any rows >= 0, N, K >= 1 (multiples of 8 with 16-byte aligned rows run on wider
+ * Sizes: any rows up to 2^30, N and K from 1 to 2^24 (multiples of 8 with 16-byte aligned rows run on wider
  * loads; other row lengths are copied into the workspace with padded rows where that pays),
  * 1 <= E <= 256; empty segments are allowed anywhere (exmoe_grouped_mm_wgrad
  * writes zeros for them). Calls whose output tiles or copies need more than 2^32 threads in
@@ -412,8 +412,8 @@ int exmoe_grouped_mm_wgrad(const void* dy, size_t lddy, const void* x, size_t ld
  *
  * x [T, K], w [N, K], y [T, N] and the bank are bf16 or all fp16 (dtype), last axis
  * contiguous, ld* elements between rows. K and rank_max are multiples of 8, rank_max <= 128,
- * rows of x, w, a and b 16-byte aligned (ld and strides multiples of 8, ld <= 2^24); N is any
- * size. The bank's adapters lie a_stride / b_stride elements apart; ranks int32 [adapters]
+ * rows of x, w, a and b 16-byte aligned (ld and strides multiples of 8, ld <= 2^24); T <= 2^22, N
+ * (any size) and K <= 2^20, and T x N up to about 2^36 (EXMOE_ERR_UNSUPPORTED beyond). The bank's adapters lie a_stride / b_stride elements apart; ranks int32 [adapters]
  * (clamped to [0, rank_max]; what a and b hold past an adapter's rank is not used) and scales
  * fp32 [adapters] are device arrays or NULL (rank_max, 1). A y or workspace that shares bytes
  * with another operand is refused (it may lie between another's rows).

@@ -689,7 +689,8 @@ static int lora_shape(int T, int N, int K, int adapters, int rank_max) {
   if (adapters < 1) return set_error(EXMOE_ERR_INVALID_ARGUMENT, "adapters must be positive (got %d)", adapters);
   if (rank_max < 8 || rank_max % 8 || rank_max > kMaxRank)
     return set_error(EXMOE_ERR_INVALID_ARGUMENT, "rank_max must be a multiple of 8 in [8, 128] (got %d)", rank_max);
-  if ((long long)((T + 15) / 16) * ((N + 15) / 16) * 512 > 0xFFFFFFFFll)
+  // 64 x 64 blocks, which every large call can run on (16 x 16 and 32 x 32 blocks are for few)
+  if ((long long)((T + 63) / 64) * ((N + 63) / 64) * 256 > 0xFFFFFF00ll)
     return set_error(EXMOE_ERR_UNSUPPORTED, "T x N has too many output tiles for one launch");
   return EXMOE_OK;
 }
