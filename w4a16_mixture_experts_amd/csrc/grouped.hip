@@ -9,94 +9,15 @@
 // expert: a workgroup finds its expert and tile from a scan of the offsets (E <= 256).
 #include "grouped.h"
 
+#include "checks.h"
 #include "exmoe.h"
 #include "gemm_wide.h"
 #include "overlap.h"
+#include "row_tiles.h"
 
 namespace exmoe {
 
 enum { kMM = 0, kDG = 1, kWG = 2 };
-
-struct RowTile {
-  int e, seg0, cnt, p0, p1, qt;   // rows p0..p1 of the segment
-};
-
-__device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? lo : (v > hi ? hi : v); }
-
-// Inclusive sum over the lanes of a wave: row shifts inside 16 lanes, then the rows' totals.
-__device__ __forceinline__ int wave_scan(int v) {
-  auto step = [&](auto ctrl) __attribute__((always_inline)) {
-    v += __builtin_amdgcn_update_dpp(0, v, decltype(ctrl)::value, 0xF, 0xF, true);   // row_shr: zeros shifted in
-  };
-  step(std::integral_constant<int, 0x111>{});
-  step(std::integral_constant<int, 0x112>{});
-  step(std::integral_constant<int, 0x114>{});
-  step(std::integral_constant<int, 0x118>{});
-  const int t0 = __builtin_amdgcn_readlane(v, 15), t1 = __builtin_amdgcn_readlane(v, 31),
-            t2 = __builtin_amdgcn_readlane(v, 47);
-  const int row = (int)lane_id() >> 4;
-  return v + (row > 0 ? t0 : 0) + (row > 1 ? t1 : 0) + (row > 2 ? t2 : 0);
-}
-
-// Tile of workgroup b among ceil(count_e / BP) x q_tiles tiles per expert. Every wave finds
-// it by itself (no barrier): lane l holds experts 4 l .. 4 l + 3.
-template <int BP, int BLOCK = 32>
-__device__ __forceinline__ bool resolve_rows(const int32_t* __restrict__ offsets, int rows, int E, int q_tiles, int b,
-                                             RowTile& t) {
-  const int lane = (int)lane_id();
-  int o[5], v[4], run = 0;
-#pragma unroll
-  for (int q = 0; q < 5; q++) {
-    const int e = lane * 4 + q;
-    o[q] = offsets[e <= E ? e : E];
-  }
-#pragma unroll
-  for (int q = 0; q < 5; q++) o[q] = clampi(o[q], 0, rows);
-#pragma unroll
-  for (int q = 0; q < 4; q++) {
-    const int c = lane * 4 + q < E ? o[q + 1] - o[q] : 0;
-    v[q] = c > 0 ? (c + BP - 1) / BP : 0;
-    run += v[q];
-  }
-  const int incl = wave_scan(run);
-  const int total = __builtin_amdgcn_readlane(incl, 63) * q_tiles;
-  if (b >= total) return false;
-  const int idx = xcd_contiguous(b, total);
-  // the first lane whose experts end past the tile, then the expert of the four
-  const int own = __ffsll((long long)__ballot(incl * q_tiles > idx)) - 1;
-  int start = __builtin_amdgcn_readlane(incl - run, own), seg0 = 0, end = 0, e = 0;
-  bool found = false;
-#pragma unroll
-  for (int q = 0; q < 4; q++) {
-    const int vq = __builtin_amdgcn_readlane(v[q], own);
-    if (!found && (start + vq) * q_tiles > idx) {
-      found = true;
-      e = own * 4 + q;
-      seg0 = __builtin_amdgcn_readlane(o[q], own);
-      end = __builtin_amdgcn_readlane(o[q + 1], own);
-    }
-    if (!found) start += vq;
-  }
-  t.e = e;
-  t.seg0 = seg0;
-  t.cnt = end - seg0;
-  // the expert's rows are dealt evenly to its tiles, in whole blocks
-  const int np = (t.cnt + BP - 1) / BP;
-  int pt;
-  band_order(idx - start * q_tiles, np, q_tiles, pt, t.qt);
-  const int blocks = (t.cnt + BLOCK - 1) / BLOCK, each = blocks / np, more = blocks - each * np;
-  t.p0 = BLOCK * (each * pt + min(pt, more));
-  t.p1 = min(t.cnt, t.p0 + BLOCK * (each + (pt < more ? 1 : 0)));
-  return true;
-}
-
-// value / d for 0 <= value, d >= 1, with mul = floor((2^32 - 1) / d): the high product is
-// the quotient or one less, and one compare corrects it.
-__device__ __forceinline__ int div_by(int v, int d, uint32_t mul) {
-  uint32_t q = __umulhi((uint32_t)v, mul);
-  if ((uint32_t)v - q * (uint32_t)d >= (uint32_t)d) q++;
-  return (int)q;
-}
 
 // The tile of a workgroup: expert e, whose rows start at seg0 of the sorted order; rows
 // p0..cnt of them (gradient of W: the cnt rows of this part of the sum, output rows from p0),
@@ -580,16 +501,6 @@ __global__ __launch_bounds__(256) void split_sum_kernel(const float* __restrict_
 }
 
 // ------------------------------------------------------------------------------------ host
-static inline int ceil_div(int a, int b) { return (int)(((long long)a + b - 1) / b); }
-constexpr long long kMaxThreads = 0xFFFFFF00ll;   // of one launch, in whole workgroups; larger calls are refused
-
-// Tiles of BP rows, at most, into which the experts' rows fall.
-static long long row_tiles(int rows, int E, int bp) { return rows / bp + (E < rows ? E : rows); }
-// Whether the bp x bq tiles of rows x Q outputs, one workgroup of that many threads each, are one launch.
-static bool tiles_fit(int rows, int Q, int E, int bp, int bq, int threads) {
-  return row_tiles(rows, E, bp) * ceil_div(Q, bq) * threads <= kMaxThreads;
-}
-
 // Parts into which the sum over an expert's rows is split: enough workgroups for the chip
 // where an expert's gradient has few tiles, at least four 64-row slices per part.
 static int wgrad_splits(int rows, int N, int K, int E) {
@@ -929,44 +840,8 @@ static int grouped_shape(int rows, int N, int K, int E, int dtype, int out_dtype
   return EXMOE_OK;
 }
 
-static int check_matrix(const char* name, const void* p, size_t ld, int cols, int bytes) {
-  if (!p) return set_error(EXMOE_ERR_INVALID_ARGUMENT, "%s must not be NULL", name);
-  if ((uintptr_t)p % (unsigned)bytes) return set_error(EXMOE_ERR_INVALID_ARGUMENT, "%s must be %d-byte aligned", name, bytes);
-  if (ld < (size_t)cols) return set_error(EXMOE_ERR_INVALID_ARGUMENT, "%s: row stride %zu smaller than its %d columns", name, ld, cols);
-  return EXMOE_OK;
-}
-
-// (the stride of a single expert means nothing)
-static int check_experts(const char* name, size_t ld, size_t stride, int N, int K, int E) {
-  if (E > 1 && stride < (size_t)(N - 1) * ld + K)
-    return set_error(EXMOE_ERR_INVALID_ARGUMENT, "%s: expert stride %zu smaller than a matrix", name, stride);
-  return EXMOE_OK;
-}
-
-static int check_int32(const char* name, const void* p, bool may_be_null) {
-  if (!p && !may_be_null) return set_error(EXMOE_ERR_INVALID_ARGUMENT, "%s must not be NULL", name);
-  if ((uintptr_t)p % 4) return set_error(EXMOE_ERR_INVALID_ARGUMENT, "%s must be 4-byte aligned", name);
-  return EXMOE_OK;
-}
-
-static int check_ws(size_t need, const void* ws, size_t ws_bytes) {
-  if (!need) return EXMOE_OK;
-  if (!ws || ws_bytes < need)
-    return set_error(EXMOE_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, ws ? ws_bytes : 0);
-  if (!aligned16(ws)) return set_error(EXMOE_ERR_INVALID_ARGUMENT, "workspace must be 16-byte aligned");
-  return EXMOE_OK;
-}
-
 static int check_size(bool fits, const char* what) {
   return fits ? EXMOE_OK : set_error(EXMOE_ERR_UNSUPPORTED, "%s: more output tiles or copied elements than one launch holds", what);
-}
-
-static int launched(hipError_t e, const char* what) { return e == hipSuccess ? EXMOE_OK : hip_error(e, what); }
-
-// Whether rows of outputs can be stored 16 bytes at a time.
-static int vec_store(const void* p, size_t ld, size_t stride, int out_f32) {
-  const size_t n = out_f32 ? 4 : 8;
-  return aligned16(p) && ld % n == 0 && stride % n == 0;
 }
 
 static void set_workspace(GroupedArgs& a, const GroupedWorkspace& need, void* ws) {
@@ -975,12 +850,6 @@ static void set_workspace(GroupedArgs& a, const GroupedWorkspace& need, void* ws
   a.pack_a = need.pack_a ? reinterpret_cast<uint16_t*>(p + need.sums) : nullptr;
   a.pack_b = need.pack_b ? reinterpret_cast<uint16_t*>(p + need.sums + need.pack_a) : nullptr;
 }
-
-#define EXMOE_TRY(call)        \
-  do {                         \
-    const int st_ = (call);    \
-    if (st_) return st_;       \
-  } while (0)
 
 extern "C" size_t exmoe_grouped_mm_workspace_bytes(int op, int rows, int N, int K, int E, int k) {
   if (op < EXMOE_GROUPED_MM || op > EXMOE_GROUPED_WGRAD || k < 0) {
