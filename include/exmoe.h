@@ -437,6 +437,98 @@ int exmoe_lora_linear(const void* x, size_t ldx, const void* w, size_t ldw, cons
                       size_t ws_bytes, hipStream_t stream);
 
 /* ------------------------------------------------------------------------------------
+ * The experts in 8 bits (device, asynchronous): activations and weights as e4m3 (OCP 8-bit
+ * floating point: 4 exponent bits, 3 of the fraction, largest 448, no infinities) with an fp32
+ * scale per 128 neighbours, for experts that are neither int4 nor 16-bit: half the weight bytes
+ * and twice the matrix rate of bf16. An expert layer of them is exmoe_rms_norm (16 bits for the
+ * router, 8 for the experts), exmoe_route_topk, exmoe_group_tokens, exmoe_grouped_mm_fp8 on gate
+ * and up, exmoe_swiglu_fp8 with the routing weights, exmoe_grouped_mm_fp8 on down, and the sum of
+ * each token's rows.
+ *   scale = max(largest |v| of the 128 / 448, 2^-126), q = e4m3(v / scale) to nearest even (the
+ *   quotient as v * (1 / scale) in fp32). A NaN among the 128 makes the scale NaN, an infinity
+ *   makes it infinite; the group's values are then NaN by IEEE arithmetic.
+ * A row of K values has ceil(K / 128) scales, the last one for what is left. ld* are elements
+ * between rows, *_stride elements between experts, the last axis is contiguous. Matrices of 16-
+ * and 32-bit values, q and scales need the alignment of their elements only, except where
+ * exmoe_grouped_mm_fp8 reads them. An output that shares bytes with another operand is refused (it
+ * may lie between another's rows), but for the in-place forms named below. Sums are made in a fixed
+ * order: equal calls give equal bits. dtype: bf16, fp16 or fp32.
+ *
+ * exmoe_rms_norm, rows t < T of H <= 16384 columns:
+ *   h = x + residual in fp32, rounded to the residual's type into residual_out (it may be the
+ *       residual itself, same stride), or h = x without a residual (both NULL)
+ *   y = h / sqrt(mean(h^2) + eps) * w in fp32, rounded once into y (x's type; NULL: not
+ *       written), and q, scale of the fp32 value (both NULL: not written)
+ * w is x's type or fp32 (w_dtype), so is the residual (res_dtype; what is stored is what is
+ * normed). T < 2^23.
+ *
+ * exmoe_quantize_fp8: q, scale of rows as they are. exmoe_swiglu_fp8: of silu(g) * u in fp32, g the
+ * first and u the next I columns of gate_up; with weights, row r's scales are multiplied by
+ * weights[row_index[r]] (0 for an index outside [0, n_weights)), or by weights[r] without
+ * row_index: a routing weight that the down product then carries to its output.
+ * exmoe_quantize_fp8_weights: w [E, N, K] with one scale per 128 x 128 block, scale [E,
+ * ceil(N / 128), ceil(K / 128)].
+ *
+ * exmoe_grouped_mm_fp8: exmoe_grouped_mm on such operands,
+ *   y[s, n] = sum_k xv[src(s), k] wv[e, n, k],  xv = x * x_scale[., k / 128],
+ *                                              wv = w * w_scale[e, n / 128, k / 128]
+ * with that call's segments, row_index, row_div and rows outside segments; expert_offsets may be
+ * NULL with E = 1 (one matrix for all rows). K is a multiple of 16; rows of x and w are 16-byte
+ * aligned (base, ld and w_stride), ld <= 2^22; y any alignment, out_dtype bf16, fp16 or fp32. What
+ * x and w hold between K and ld is not read. Each block of 128 positions is
+ * summed by the matrix unit and scaled into an fp32 sum. Its 8-bit adders drop what lies below
+ * 2^-13 of the largest of 8 neighbouring products: for 16-bit outputs that is a tenth of their
+ * rounding or less; 32-bit outputs take products and sums that lose nothing but fp32 roundings, at
+ * half the rate. Products of two scales under 2^-126 lose bits. No workspace.
+ * ---------------------------------------------------------------------------------- */
+int exmoe_rms_norm(const void* x, size_t ldx, const void* w, int w_dtype, const void* residual, size_t ldr, int res_dtype,
+                   void* residual_out, size_t ldro, float eps, int T, int H, int dtype, void* y, size_t ldy, uint8_t* q,
+                   size_t ldq, float* scale, size_t lds, hipStream_t stream);
+
+int exmoe_quantize_fp8(const void* x, size_t ldx, int rows, int K, int dtype, uint8_t* q, size_t ldq, float* scale,
+                       size_t lds, hipStream_t stream);
+
+int exmoe_swiglu_fp8(const void* gate_up, size_t ldx, const float* weights, int n_weights, const int32_t* row_index,
+                     int rows, int I, int dtype, uint8_t* q, size_t ldq, float* scale, size_t lds, hipStream_t stream);
+
+int exmoe_quantize_fp8_weights(const void* w, size_t ldw, size_t w_stride, int E, int N, int K, int dtype, uint8_t* q,
+                               size_t ldq, size_t q_stride, float* scale, size_t lds, size_t s_stride, hipStream_t stream);
+
+int exmoe_grouped_mm_fp8(const uint8_t* x, size_t ldx, const float* x_scale, size_t ldxs, int x_rows,
+                         const int32_t* row_index, int row_div, const int32_t* expert_offsets, const uint8_t* w, size_t ldw,
+                         size_t w_stride, const float* w_scale, size_t ldws, size_t ws_stride, int rows, int N, int K, int E,
+                         int out_dtype, void* y, size_t ldy, hipStream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * The losses that train a router, with their gradient (device, asynchronous): what keeps the
+ * experts' load even, beside the unchanged top-k (abstract; Fig. 1). Of the M tokens t < T that
+ * count (mask NULL: all; else mask[t] != 0), p_t = softmax(logits[t, :]) over E experts, c_e the
+ * number of their topk_ids equal to e (ids outside [0, E) count nowhere):
+ *   losses[0] = E sum_e c_e / (M k) * (sum_t p_te) / M       balance
+ *   losses[1] = (sum_t (log sum_e exp(logits_te))^2) / M      z
+ *   counts[e] = c_e, counts[E] = M                            (int32 [E + 1])
+ * exmoe_balance_loss_backward: dlogits = grad_losses[0] dlosses[0]/dlogits + grad_losses[1]
+ * dlosses[1]/dlogits, counts as constants; zeros for tokens that do not count. counts is what the
+ * forward call wrote (or sums of several calls' counts: a global batch in parts). dlogits may be
+ * logits itself (same type and stride).
+ * logits [T, E] of dtype (bf16, fp16, fp32; router logits are bf16 here), ldl elements between
+ * rows, element alignment; topk_ids int32 [T, k] contiguous; mask uint8 [T]; losses and grad_losses
+ * fp32 [2]; dlogits of dtype or fp32 (out_dtype). 1 <= k <= E <= 256, k <= 64, T <= 2^24. A row of
+ * -inf logits alone has no softmax: it counts, adds nothing to the sums and its gradient is zero.
+ * M = 0 gives zeros. Workspace: exmoe_balance_loss_workspace_bytes(T, E) bytes, 16-byte aligned,
+ * no initialization, not kept; calls that overlap in time must not share one. Equal calls give
+ * equal bits.
+ * ---------------------------------------------------------------------------------- */
+size_t exmoe_balance_loss_workspace_bytes(int T, int E);
+
+int exmoe_balance_loss(const void* logits, size_t ldl, const int32_t* topk_ids, const uint8_t* mask, int T, int E, int k,
+                       int dtype, float* losses, int32_t* counts, void* workspace, size_t ws_bytes, hipStream_t stream);
+
+int exmoe_balance_loss_backward(const void* logits, size_t ldl, const int32_t* counts, const uint8_t* mask,
+                                const float* grad_losses, int T, int E, int k, int dtype, int out_dtype, void* dlogits,
+                                size_t lddl, hipStream_t stream);
+
+/* ------------------------------------------------------------------------------------
  * Per-kernel timing for benchmarks (not part of the layer's semantics). While enabled,
  * each kernel of the library is launched with a hipEvent pair that stamps that kernel's
  * own start and end on its launch stream (hipExtLaunchKernelGGL; skipped on a stream that
@@ -445,7 +537,9 @@ int exmoe_lora_linear(const void* x, size_t ldx, const void* w, size_t ldw, cons
  * count of one kernel by name: "route_logits", "route_token", "route_sel", "topk",
  * "group", "decode_gateup", "decode_down", "decode_fused", "combine", "xsum",
  * "prefill_gateup", "prefill_down", "grouped_mm", "grouped_dgrad", "grouped_wgrad",
- * "pack_rows", "token_sum", "split_sum", "lora_shrink", "lora_linear". Process-global. The events bracket the launch as the
+ * "pack_rows", "token_sum", "split_sum", "lora_shrink", "lora_linear", "rms_norm", "quantize_fp8",
+ * "swiglu_fp8", "quantize_fp8_weights", "grouped_mm_fp8", "balance_loss", "balance_join",
+ * "balance_loss_bwd". Process-global. The events bracket the launch as the
  * stream processes it, so a launch that waits for the host is counted with that wait.
  * ---------------------------------------------------------------------------------- */
 int exmoe_profile_enable(int on);

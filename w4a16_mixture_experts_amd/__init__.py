@@ -115,6 +115,16 @@ _SIGS = {
                                     _vp]),
     "exmoe_grouped_mm_wgrad": (_i, [_vp, _sz, _vp, _sz, _i, _vp, _i, _vp, _i, _i, _i, _i, _i, _i, _vp, _sz, _sz, _vp,
                                     _sz, _vp]),
+    "exmoe_rms_norm": (_i, [_vp, _sz, _vp, _i, _vp, _sz, _i, _vp, _sz, ctypes.c_float, _i, _i, _i, _vp, _sz, _vp, _sz, _vp,
+                            _sz, _vp]),
+    "exmoe_quantize_fp8": (_i, [_vp, _sz, _i, _i, _i, _vp, _sz, _vp, _sz, _vp]),
+    "exmoe_swiglu_fp8": (_i, [_vp, _sz, _vp, _i, _vp, _i, _i, _i, _vp, _sz, _vp, _sz, _vp]),
+    "exmoe_quantize_fp8_weights": (_i, [_vp, _sz, _sz, _i, _i, _i, _i, _vp, _sz, _sz, _vp, _sz, _sz, _vp]),
+    "exmoe_grouped_mm_fp8": (_i, [_vp, _sz, _vp, _sz, _i, _vp, _i, _vp, _vp, _sz, _sz, _vp, _sz, _sz, _i, _i, _i, _i, _i, _vp,
+                                  _sz, _vp]),
+    "exmoe_balance_loss_workspace_bytes": (_sz, [_i, _i]),
+    "exmoe_balance_loss": (_i, [_vp, _sz, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _vp, _sz, _vp]),
+    "exmoe_balance_loss_backward": (_i, [_vp, _sz, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _sz, _vp]),
     "exmoe_lora_workspace_bytes": (_sz, [_i] * 5),
     "exmoe_lora_linear": (_i, [_vp, _sz, _vp, _sz, ctypes.POINTER(LoraBankC), _vp, _i, _i, _i, _i, _vp, _sz, _vp, _sz,
                                _vp]),
@@ -472,6 +482,13 @@ def _no_gradient():
                          "torch.no_grad() (an autograd function around grouped_mm calls grouped_mm_dgrad and grouped_mm_wgrad)")
 
 
+def _needs_no_gradient(*tensors):
+    for t in tensors:
+        if t is not None and t.requires_grad:
+            _no_gradient()
+            return
+
+
 def grouped_mm_workspace_bytes(op: int, rows: int, N: int, K: int, E: int, k: int = 0) -> int:
     return _lib.exmoe_grouped_mm_workspace_bytes(op, rows, N, K, E, k)
 
@@ -606,6 +623,214 @@ def lora_linear(x, w, bank: LoraBank, ids, y=None, workspace=None):
     _run_on(dev, _lib.exmoe_lora_linear, x.data_ptr(), ldx, wp, ldw, bank.ref, _int32("ids", ids, dev, T), T, N, K,
             _dtype_code(dtype), y.data_ptr(), _rows_ld("y", y), ws, ws_bytes)
     return y
+
+
+# ----------------------------------------------------------------------------- experts in 8 bits
+def _f8_rows(name: str, t, dev: int, ndim: int = 2) -> int:
+    ld = _rows_ld(name, t, ndim)
+    if t.dtype is not _torch().float8_e4m3fn or t.get_device() != dev:
+        raise ValueError(f"{name} must be float8_e4m3fn on GPU {dev}")
+    return ld
+
+
+def _scales(name: str, t, shape, dev: int) -> int:
+    ld = _rows_ld(name, t, len(shape))
+    if t.shape != shape or t.dtype is not _torch().float32 or t.get_device() != dev:
+        raise ValueError(f"{name} must be {tuple(shape)} float32 on GPU {dev}")
+    return ld
+
+
+def _f8_outputs(q, scale, rows: int, K: int, dev: int, like):
+    """The given outputs, or new ones: q with rows of a multiple of 16 bytes, as the product reads them."""
+    torch = _torch()
+    if q is None:
+        q = like.new_empty((rows, (K + 15) // 16 * 16), dtype=torch.float8_e4m3fn)[:, :K]
+    elif q.shape != (rows, K):
+        raise ValueError(f"q must be {(rows, K)} (got {tuple(q.shape)})")
+    if scale is None:
+        scale = like.new_empty((rows, (K + 127) // 128), dtype=torch.float32)
+    return q, scale, _f8_rows("q", q, dev), _scales("scale", scale, (rows, (K + 127) // 128), dev)
+
+
+@dataclass
+class NormOutputs:
+    """What rms_norm wrote (None: not asked for)."""
+    y: object = None          # [T, H] of x's type
+    q: object = None          # [T, H] float8_e4m3fn
+    scale: object = None      # [T, ceil(H / 128)] float32
+    residual: object = None   # [T, H]: x + residual
+
+
+def rms_norm(x, w, eps: float = 1e-6, residual=None, out: str = "y", y=None, q=None, scale=None, residual_out=None) -> NormOutputs:
+    """y = h / sqrt(mean(h^2) + eps) * w over the rows of h = x + residual (or x).
+
+    x [T, H] (bf16, fp16 or fp32), w [H] and residual [T, H] of x's type or fp32. out: "y" (x's
+    type), "fp8" (e4m3 q with a scale per 128 columns) or "both". h is rounded to the residual's type
+    and written to residual_out (a new tensor, or the residual itself). Records no gradient."""
+    _needs_no_gradient(x, w, residual, y, residual_out)
+    torch = _torch()
+    if out not in ("y", "fp8", "both"):
+        raise ValueError(f'out must be "y", "fp8" or "both" (got {out!r})')
+    ldx = _rows_ld("x", x)
+    T, H = x.shape
+    dev, dtype = x.get_device(), x.dtype
+    if w.shape != (H,) or not w.is_contiguous() or w.get_device() != dev:
+        raise ValueError(f"w must be a contiguous tensor of {H} on GPU {dev}")
+    r = NormOutputs()
+    res = [None, 0, 0, None, 0]
+    if residual is not None:
+        if residual.shape != (T, H) or residual.get_device() != dev:
+            raise ValueError(f"residual must be {(T, H)} on GPU {dev}")
+        ldr = _rows_ld("residual", residual)
+        r.residual = _result("residual_out", residual_out, (T, H), residual.dtype, dev, residual)
+        res = [residual.data_ptr(), ldr, _dtype_code(residual.dtype), r.residual.data_ptr(), _rows_ld("residual_out", r.residual)]
+    elif residual_out is not None:
+        raise ValueError("residual_out without a residual")
+    o = [None, 0, None, 0, None, 0]
+    if out != "fp8":
+        r.y = _result("y", y, (T, H), dtype, dev, x)
+        o[0:2] = [r.y.data_ptr(), _rows_ld("y", r.y)]
+    elif y is not None:
+        raise ValueError('y with out="fp8"')
+    if out != "y":
+        r.q, r.scale, ldq, lds = _f8_outputs(q, scale, T, H, dev, x)
+        o[2:6] = [r.q.data_ptr(), ldq, r.scale.data_ptr(), lds]
+    elif q is not None or scale is not None:
+        raise ValueError('q or scale with out="y"')
+    _run_on(dev, _lib.exmoe_rms_norm, x.data_ptr(), ldx, w.data_ptr(), _dtype_code(w.dtype), *res, eps, T, H,
+            _dtype_code(dtype), *o)
+    return r
+
+
+def quantize_fp8(x, q=None, scale=None):
+    """(q, scale) of x [rows, K] (bf16, fp16 or fp32): e4m3 with a scale per 128 columns of a row."""
+    _needs_no_gradient(x)
+    ldx = _rows_ld("x", x)
+    rows, K = x.shape
+    dev = x.get_device()
+    q, scale, ldq, lds = _f8_outputs(q, scale, rows, K, dev, x)
+    _run_on(dev, _lib.exmoe_quantize_fp8, x.data_ptr(), ldx, rows, K, _dtype_code(x.dtype), q.data_ptr(), ldq,
+            scale.data_ptr(), lds)
+    return q, scale
+
+
+def swiglu_fp8(gate_up, weights=None, row_index=None, q=None, scale=None):
+    """(q, scale) of silu(gate) * up [rows, I], gate_up [rows, 2 I] with the gate's columns first.
+    weights fp32 (any shape, contiguous): row r's scales are multiplied by weights.view(-1)[row_index[r]]
+    (row_index int32 [rows]: sorted_flat of a routed batch), or by its r-th without row_index."""
+    _needs_no_gradient(gate_up, weights)
+    ldx = _rows_ld("gate_up", gate_up)
+    rows, cols = gate_up.shape
+    if cols % 2:
+        raise ValueError(f"gate_up has {cols} columns: gate and up side by side are an even number")
+    dev, I = gate_up.get_device(), cols // 2
+    if weights is not None and (weights.dtype is not _torch().float32 or weights.get_device() != dev or not weights.is_contiguous()):
+        raise ValueError(f"weights must be a contiguous float32 tensor on GPU {dev}")
+    q, scale, ldq, lds = _f8_outputs(q, scale, rows, I, dev, gate_up)
+    _run_on(dev, _lib.exmoe_swiglu_fp8, gate_up.data_ptr(), ldx, _ptr(weights), 0 if weights is None else weights.numel(),
+            _int32("row_index", row_index, dev, rows), rows, I, _dtype_code(gate_up.dtype), q.data_ptr(), ldq,
+            scale.data_ptr(), lds)
+    return q, scale
+
+
+def quantize_fp8_weights(w, q=None, scale=None):
+    """(q, scale) of w [E, N, K] (bf16, fp16 or fp32): e4m3 with a scale per 128 x 128 block, scale
+    fp32 [E, ceil(N / 128), ceil(K / 128)]."""
+    _needs_no_gradient(w)
+    ldw = _rows_ld("w", w, 3)
+    E, N, K = w.shape
+    dev = w.get_device()
+    if q is None:
+        q = w.new_empty((E, N, (K + 15) // 16 * 16), dtype=_torch().float8_e4m3fn)[..., :K]
+    elif q.shape != w.shape:
+        raise ValueError(f"q must be {tuple(w.shape)} (got {tuple(q.shape)})")
+    blocks = (E, (N + 127) // 128, (K + 127) // 128)
+    if scale is None:
+        scale = w.new_empty(blocks, dtype=_torch().float32)
+    ldq, lds = _f8_rows("q", q, dev, 3), _scales("scale", scale, blocks, dev)
+    _run_on(dev, _lib.exmoe_quantize_fp8_weights, w.data_ptr(), ldw, w.stride(0), E, N, K, _dtype_code(w.dtype), q.data_ptr(),
+            ldq, q.stride(0), scale.data_ptr(), lds, scale.stride(0))
+    return q, scale
+
+
+def grouped_mm_fp8(x, x_scale, w, w_scale, offsets=None, row_index=None, row_div: int = 1, out_dtype=None, y=None):
+    """grouped_mm on 8-bit operands: y[s, :] = (w[e] * w_scale[e]) @ (x * x_scale)[src(s), :].
+
+    x [x_rows, K] and w [E, N, K] float8_e4m3fn with 16-byte aligned rows, K a multiple of 16;
+    x_scale fp32 [x_rows, ceil(K / 128)], w_scale fp32 [E, ceil(N / 128), ceil(K / 128)]; offsets,
+    row_index and row_div as in grouped_mm, offsets None for one expert with every row. Returns y
+    [rows, N] in out_dtype (bf16, the default, fp16 or fp32); rows outside every segment are left
+    as they are."""
+    _needs_no_gradient(x_scale, w_scale, y)
+    dev = x.get_device()
+    ldx, ldw = _f8_rows("x", x, dev), _f8_rows("w", w, dev, 3)
+    E, N, K = w.shape
+    x_rows, x_cols = x.shape
+    if x_cols != K:
+        raise ValueError(f"x has {x_cols} columns, w takes {K}")
+    kb = (K + 127) // 128
+    ldxs, ldws = _scales("x_scale", x_scale, (x_rows, kb), dev), _scales("w_scale", w_scale, (E, (N + 127) // 128, kb), dev)
+    rows = x_rows if row_index is None else row_index.numel()
+    out_dtype = _torch().bfloat16 if out_dtype is None else out_dtype
+    y = _result("y", y, (rows, N), out_dtype, dev, x)
+    _run_on(dev, _lib.exmoe_grouped_mm_fp8, x.data_ptr(), ldx, x_scale.data_ptr(), ldxs, x_rows,
+            _int32("row_index", row_index, dev), row_div, _int32("offsets", offsets, dev, E + 1), w.data_ptr(), ldw,
+            w.stride(0), w_scale.data_ptr(), ldws, w_scale.stride(0), rows, N, K, E, _dtype_code(out_dtype), y.data_ptr(),
+            _rows_ld("y", y))
+    return y
+
+
+# ----------------------------------------------------------------------------- router losses
+def _mask(mask, T: int, dev: int):
+    if mask is None:
+        return None
+    if mask.dtype not in (_torch().bool, _torch().uint8) or mask.get_device() != dev or not mask.is_contiguous() or mask.numel() != T:
+        raise ValueError(f"mask must be a contiguous bool tensor of {T} on GPU {dev}")
+    return mask.data_ptr()
+
+
+def balance_loss_workspace_bytes(T: int, E: int) -> int:
+    return _lib.exmoe_balance_loss_workspace_bytes(T, E)
+
+
+def balance_loss(logits, ids, mask=None, losses=None, counts=None, workspace=None):
+    """(losses fp32 [2], counts int32 [E + 1]) of router logits [T, E] (bf16, fp16 or fp32) and their
+    top-k ids int32 [T, k], over the tokens whose mask (bool [T]; None: all) is set: losses[0] = E
+    sum_e f_e P_e (f: share of the routed pairs, P: mean probability), losses[1] = mean squared
+    log-sum-exp, counts: pairs per expert, then the number of tokens. Records no gradient: an autograd
+    function around it calls balance_loss_backward."""
+    _needs_no_gradient(logits, losses)
+    ldl = _rows_ld("logits", logits)
+    T, E = logits.shape
+    dev = logits.get_device()
+    if ids.dim() != 2 or ids.shape[0] != T:
+        raise ValueError(f"ids must be [{T}, k] (got {tuple(ids.shape)})")
+    losses = _result("losses", losses, (2,), _torch().float32, dev, logits)
+    counts = _result("counts", counts, (E + 1,), _torch().int32, dev, logits)
+    if not losses.is_contiguous() or not counts.is_contiguous():
+        raise ValueError("losses and counts must be contiguous")
+    ws, ws_bytes, _keep = _scratch(workspace, lambda: balance_loss_workspace_bytes(T, E), dev)
+    _run_on(dev, _lib.exmoe_balance_loss, logits.data_ptr(), ldl, _int32("ids", ids, dev), _mask(mask, T, dev), T, E,
+            ids.shape[1], _dtype_code(logits.dtype), losses.data_ptr(), counts.data_ptr(), ws, ws_bytes)
+    return losses, counts
+
+
+def balance_loss_backward(logits, counts, k: int, grad_losses, mask=None, out_dtype=None, dlogits=None):
+    """Gradient of grad_losses[0] * losses[0] + grad_losses[1] * losses[1] (fp32 [2], on the GPU) with
+    respect to logits: [T, E] in out_dtype (logits' type, the default, or fp32). counts: what
+    balance_loss returned. dlogits may be logits itself."""
+    _needs_no_gradient(logits, grad_losses, dlogits)
+    ldl = _rows_ld("logits", logits)
+    T, E = logits.shape
+    dev = logits.get_device()
+    if grad_losses.dtype is not _torch().float32 or grad_losses.get_device() != dev or not grad_losses.is_contiguous() or grad_losses.numel() != 2:
+        raise ValueError(f"grad_losses must be a contiguous float32 tensor of 2 on GPU {dev}")
+    out_dtype = logits.dtype if out_dtype is None else out_dtype
+    dlogits = _result("dlogits", dlogits, (T, E), out_dtype, dev, logits)
+    _run_on(dev, _lib.exmoe_balance_loss_backward, logits.data_ptr(), ldl, _int32("counts", counts, dev, E + 1),
+            _mask(mask, T, dev), grad_losses.data_ptr(), T, E, k, _dtype_code(logits.dtype), _dtype_code(out_dtype),
+            dlogits.data_ptr(), _rows_ld("dlogits", dlogits))
+    return dlogits
 
 
 # ----------------------------------------------------------------------------- slot cache

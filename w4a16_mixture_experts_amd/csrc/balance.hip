@@ -1,0 +1,327 @@
+// The losses that train a router, and their gradient, gfx950.
+//
+// Of the M tokens t that count (all, or those whose mask is set), with p_t = softmax(l_t) over E
+// experts, lse_t = log sum_e exp(l_te), and c_e how many of their k routed ids are e:
+//   balance = E sum_e f_e P_e,   f_e = c_e / (M k),   P_e = sum_t p_te / M
+//   z       = sum_t lse_t^2 / M
+//   d/dl_te (ga balance + gz z) = p_te / M (ga E (f_e - sum_j f_j p_tj) + 2 gz lse_t)
+// (f is a count: it has no gradient). A row whose logits are all -inf has no softmax: it counts
+// among the M, adds nothing to P and z, and its gradient is zero.
+// Sums over tokens are made per lane, then per workgroup, then over the workgroups in 64 bits, each
+// in a fixed order. Bound by memory for long batches and by the two launches for short ones.
+#include "checks.h"
+#include "exmoe.h"
+#include "fp8.h"
+#include "overlap.h"
+#include "row_tiles.h"
+
+namespace exmoe {
+
+struct BalanceArgs {
+  const void* l;
+  size_t ldl;
+  const int32_t* ids;
+  const uint8_t* mask;
+  int T, E, k;
+  // forward
+  float* part;               // [blocks][E + 1]: sums of p, then of lse^2
+  int32_t* part_n;           // [blocks][E + 1]: counts, then tokens
+  float* losses;
+  int32_t* counts;           // [E + 1]: c, M
+  // backward
+  const int32_t* counts_in;
+  const float* grad;         // ga, gz
+  void* dl;
+  size_t lddl;
+  int out_f32;
+};
+
+// Softmax of a row held by LANES neighbouring lanes, 8 experts each: v becomes exp(l - max).
+template <int LANES>
+__device__ __forceinline__ float lanes_max(float v) {
+  if constexpr (LANES >= 2) v = fmaxf(v, __uint_as_float(dpp_u32<0xB1>(__float_as_uint(v))));
+  if constexpr (LANES >= 4) v = fmaxf(v, __uint_as_float(dpp_u32<0x4E>(__float_as_uint(v))));
+  if constexpr (LANES >= 8) v = fmaxf(v, __uint_as_float(dpp_u32<0x141>(__float_as_uint(v))));
+  if constexpr (LANES >= 16) v = fmaxf(v, __uint_as_float(dpp_u32<0x140>(__float_as_uint(v))));
+  if constexpr (LANES >= 32) v = fmaxf(v, __shfl_xor(v, 16, 64));
+  return v;
+}
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float v) {
+  if constexpr (LANES >= 2) v += __uint_as_float(dpp_u32<0xB1>(__float_as_uint(v)));
+  if constexpr (LANES >= 4) v += __uint_as_float(dpp_u32<0x4E>(__float_as_uint(v)));
+  if constexpr (LANES >= 8) v += __uint_as_float(dpp_u32<0x141>(__float_as_uint(v)));
+  if constexpr (LANES >= 16) v += __uint_as_float(dpp_u32<0x140>(__float_as_uint(v)));
+  if constexpr (LANES >= 32) v += __shfl_xor(v, 16, 64);
+  return v;
+}
+
+constexpr float kNoLogit = -__builtin_huge_valf();
+
+// p and lse of the row; whether it has a softmax (some logit is not -inf). A NaN or +inf among the
+// logits makes them NaN, as by the formula.
+template <int LANES>
+__device__ __forceinline__ bool row_softmax(f32x8 l, f32x8& p, float& lse) {
+  float top = l[0], s = 0.f;
+#pragma unroll
+  for (int i = 1; i < 8; i++) top = fmaxf(top, l[i]);
+  top = lanes_max<LANES>(top);
+  const bool some = !(top == kNoLogit);
+#pragma unroll
+  for (int i = 0; i < 8; i++) {
+    p[i] = expf(l[i] - (some ? top : 0.f));
+    s += p[i];
+  }
+  s = lanes_sum<LANES>(s);
+  const bool has = some || s != s;     // (fmaxf passes over a NaN, the sum does not)
+  lse = has ? (some ? top : 0.f) + logf(s) : 0.f;
+  const float inv = has ? 1.f / s : 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; i++) p[i] *= inv;
+  return has;
+}
+
+template <int DT>
+__device__ __forceinline__ f32x8 load_logits(const BalanceArgs& a, int row, int c) {
+  f32x8 v = load_upto8<DT>(a.l, (size_t)row * a.ldl + c, a.E - c);
+#pragma unroll
+  for (int i = 0; i < 8; i++)
+    if (c + i >= a.E) v[i] = kNoLogit;
+  return v;
+}
+
+constexpr int kBalThreads = 256;
+
+// LANES lanes per row; a workgroup takes every gridDim.x-th run of rows.
+template <int DT, int LANES>
+__global__ __launch_bounds__(kBalThreads) void balance_kernel(BalanceArgs a) {
+  constexpr int kRows = kBalThreads / LANES, kE = 8 * LANES;
+  __shared__ float s_p[kBalThreads / 64][kE + 1];
+  __shared__ int s_n[kE + 1];
+  const int t = threadIdx.x, lane = t & 63, wave = t / 64, c = 8 * (t % LANES);
+  for (int e = t; e <= kE; e += kBalThreads) s_n[e] = 0;
+  __syncthreads();
+  f32x8 sum = {0, 0, 0, 0, 0, 0, 0, 0};
+  float z = 0.f;
+  int n = 0;
+  for (int r0 = blockIdx.x * kRows; r0 < a.T; r0 += gridDim.x * kRows) {
+    const int row = r0 + t / LANES;
+    const bool live = row < a.T && (!a.mask || a.mask[row]);
+    if (!live) continue;     // (the lanes of a row together)
+    f32x8 p;
+    float lse;
+    if (row_softmax<LANES>(load_logits<DT>(a, row, c), p, lse)) {
+#pragma unroll
+      for (int i = 0; i < 8; i++) sum[i] += p[i];
+      if (c == 0) z += lse * lse;
+    }
+    if (c == 0) n++;
+    for (int j = t % LANES; j < a.k; j += LANES) {
+      const int e = a.ids[(size_t)row * a.k + j];
+      if ((unsigned)e < (unsigned)a.E) atomicAdd(&s_n[e], 1);   // (whole numbers: any order)
+    }
+  }
+  // over the wave's rows, then over the waves
+#pragma unroll
+  for (int m = LANES; m < 64; m <<= 1) {
+#pragma unroll
+    for (int i = 0; i < 8; i++) sum[i] += __shfl_xor(sum[i], m, 64);
+  }
+  z = wave_sum(z);
+  if (lane < LANES) {
+#pragma unroll
+    for (int i = 0; i < 8; i++) s_p[wave][c + i] = sum[i];
+  }
+  if (lane == 0) s_p[wave][kE] = z;
+  if (n) atomicAdd(&s_n[kE], n);
+  __syncthreads();
+  for (int e = t; e <= a.E; e += kBalThreads) {
+    const int at = e < a.E ? e : kE;
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kBalThreads / 64; w++) v += s_p[w][at];
+    a.part[(size_t)blockIdx.x * (a.E + 1) + e] = v;
+    a.part_n[(size_t)blockIdx.x * (a.E + 1) + e] = s_n[at];
+  }
+}
+
+// The sums over the workgroups, and the losses.
+__global__ __launch_bounds__(1024) void balance_join_kernel(BalanceArgs a, int blocks) {
+  __shared__ double s_p[kMaxExperts + 1];
+  __shared__ int s_n[kMaxExperts + 1];
+  const int wave = threadIdx.x / 64, lane = threadIdx.x & 63;
+  for (int e = wave; e <= a.E; e += 16) {
+    double v = 0.;
+    int n = 0;
+    for (int b = lane; b < blocks; b += 64) {
+      v += a.part[(size_t)b * (a.E + 1) + e];
+      n += a.part_n[(size_t)b * (a.E + 1) + e];
+    }
+    v = wave_sum(v);
+    for (int m = 32; m >= 1; m >>= 1) n += __shfl_xor(n, m, 64);
+    if (lane == 0) {
+      s_p[e] = v;
+      s_n[e] = n;
+      a.counts[e] = n;
+    }
+  }
+  __syncthreads();
+  if (wave == 0) {
+    double v = 0.;
+    for (int e = lane; e < a.E; e += 64) v += s_p[e] * (double)s_n[e];
+    v = wave_sum(v);
+    const double M = s_n[a.E];
+    if (lane == 0) {
+      a.losses[0] = M > 0. ? (float)(v * a.E / (M * M * a.k)) : 0.f;
+      a.losses[1] = M > 0. ? (float)(s_p[a.E] / M) : 0.f;
+    }
+  }
+}
+
+template <int DT, int LANES, bool OUT_F32>
+__global__ __launch_bounds__(kBalThreads) void balance_bwd_kernel(BalanceArgs a) {
+  constexpr int OT = OUT_F32 ? (int)EXMOE_DTYPE_FP32 : DT;
+  const int t = threadIdx.x, c = 8 * (t % LANES);
+  const size_t i0 = ((size_t)blockIdx.x * kBalThreads + t) / LANES;
+  if (i0 >= (size_t)a.T) return;
+  const int row = (int)i0;
+  const int M = a.counts_in[a.E];
+  f32x8 d = {0, 0, 0, 0, 0, 0, 0, 0};
+  const bool live = M > 0 && (!a.mask || a.mask[row]);
+  if (live) {
+    f32x8 p;
+    float lse;
+    if (row_softmax<LANES>(load_logits<DT>(a, row, c), p, lse)) {
+      const float ga = a.grad[0] * (float)a.E, gz = 2.f * a.grad[1] * lse, per = 1.f / ((float)M * (float)a.k);
+      f32x8 f;
+      float dot = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+        f[i] = c + i < a.E ? (float)a.counts_in[c + i] * per : 0.f;
+        dot += f[i] * p[i];
+      }
+      dot = lanes_sum<LANES>(dot);
+      const float m = 1.f / (float)M;
+#pragma unroll
+      for (int i = 0; i < 8; i++) d[i] = p[i] * (ga * (f[i] - dot) + gz) * m;
+    }
+  }
+  if (a.E > c) store_upto8<OT>(a.dl, (size_t)row * a.lddl + c, a.E - c, d);
+}
+
+// ------------------------------------------------------------------------------------ host
+template <class F>
+static hipError_t by_lanes(int E, F f) {
+  if (E <= 8) return f(std::integral_constant<int, 1>{});
+  if (E <= 16) return f(std::integral_constant<int, 2>{});
+  if (E <= 32) return f(std::integral_constant<int, 4>{});
+  if (E <= 64) return f(std::integral_constant<int, 8>{});
+  if (E <= 128) return f(std::integral_constant<int, 16>{});
+  return f(std::integral_constant<int, 32>{});
+}
+static int lanes_of(int E) {
+  int l = 1;
+  while (8 * l < E) l *= 2;
+  return l;
+}
+// Workgroups of the forward pass: four rows a lane at least, at most 512 of them.
+static int balance_blocks(int T, int E) {
+  const long long n = ((long long)T * lanes_of(E) + 4 * kBalThreads - 1) / (4 * kBalThreads);
+  return n > 512 ? 512 : (n < 1 ? 1 : (int)n);
+}
+
+}  // namespace exmoe
+
+using namespace exmoe;
+
+// ------------------------------------------------------------------------------------ C ABI
+static int check_router(int T, int E, int k, int dtype) {
+  if (T < 0 || T > (1 << 24)) return set_error(EXMOE_ERR_INVALID_ARGUMENT, "T must be in [0, 2^24] (got %d)", T);
+  if (E < 1 || E > kMaxExperts) return set_error(EXMOE_ERR_INVALID_ARGUMENT, "E must be in [1, 256] (got %d)", E);
+  if (k < 1 || k > E) return set_error(EXMOE_ERR_INVALID_ARGUMENT, "k must be in [1, E] (got k=%d, E=%d)", k, E);
+  if (k > kMaxK) return set_error(EXMOE_ERR_UNSUPPORTED, "k > 64 is not supported (got %d)", k);
+  if (dtype < EXMOE_DTYPE_BF16 || dtype > EXMOE_DTYPE_FP32)
+    return set_error(EXMOE_ERR_INVALID_ARGUMENT, "dtype must be bf16, fp16 or fp32 (got %d)", dtype);
+  return EXMOE_OK;
+}
+
+extern "C" size_t exmoe_balance_loss_workspace_bytes(int T, int E) {
+  if (check_router(T, E, 1, EXMOE_DTYPE_BF16)) return 0;
+  return (size_t)balance_blocks(T, E) * (E + 1) * 8;
+}
+
+extern "C" int exmoe_balance_loss(const void* logits, size_t ldl, const int32_t* topk_ids, const uint8_t* mask, int T, int E,
+                                  int k, int dtype, float* losses, int32_t* counts, void* workspace, size_t ws_bytes,
+                                  hipStream_t stream) {
+  EXMOE_TRY(check_router(T, E, k, dtype));
+  if (!losses || (uintptr_t)losses % 4) return set_error(EXMOE_ERR_INVALID_ARGUMENT, "losses must be non-NULL and 4-byte aligned");
+  EXMOE_TRY(check_int32("counts", counts, false));
+  const int b = dtype_bytes(dtype);
+  if (T > 0) {
+    EXMOE_TRY(check_matrix("logits", logits, ldl, E, b));
+    EXMOE_TRY(check_int32("topk_ids", topk_ids, false));
+  }
+  const size_t need = exmoe_balance_loss_workspace_bytes(T, E);
+  EXMOE_TRY(check_ws(need, workspace, ws_bytes));
+  const MemRows ml = mem_matrix("logits", logits, T, ldl, E, b), mi = mem_flat("topk_ids", topk_ids, (size_t)T * k * 4),
+                mm = mem_flat("mask", mask, T), mo = mem_flat("losses", losses, 8), mc = mem_flat("counts", counts, (E + 1) * 4);
+  EXMOE_TRY(check_apart(mo, {ml, mi, mm, mc}));
+  EXMOE_TRY(check_apart(mc, {ml, mi, mm}));
+  EXMOE_TRY(check_apart(mem_flat("workspace", workspace, need), {ml, mi, mm, mo, mc}));
+  BalanceArgs a{};
+  a.l = logits; a.ldl = ldl; a.ids = topk_ids; a.mask = mask; a.T = T; a.E = E; a.k = k; a.losses = losses; a.counts = counts;
+  const int blocks = balance_blocks(T, E);
+  a.part = static_cast<float*>(workspace);
+  a.part_n = reinterpret_cast<int32_t*>(a.part + (size_t)blocks * (E + 1));
+  return launched(by_dtype(dtype, [&](auto dt) {
+                    return by_lanes(E, [&](auto lanes) {
+                      ProfScope prof("balance_loss", stream);
+                      EXMOE_LAUNCH(prof, (balance_kernel<decltype(dt)::value, decltype(lanes)::value>), dim3(blocks),
+                                   dim3(kBalThreads), 0, stream, a);
+                      const hipError_t e = hipGetLastError();
+                      if (e != hipSuccess) return e;
+                      ProfScope join("balance_join", stream);
+                      EXMOE_LAUNCH(join, balance_join_kernel, dim3(1), dim3(1024), 0, stream, a, blocks);
+                      return hipGetLastError();
+                    });
+                  }),
+                  "exmoe_balance_loss");
+}
+
+extern "C" int exmoe_balance_loss_backward(const void* logits, size_t ldl, const int32_t* counts, const uint8_t* mask,
+                                           const float* grad_losses, int T, int E, int k, int dtype, int out_dtype,
+                                           void* dlogits, size_t lddl, hipStream_t stream) {
+  EXMOE_TRY(check_router(T, E, k, dtype));
+  if (out_dtype != dtype && out_dtype != EXMOE_DTYPE_FP32)
+    return set_error(EXMOE_ERR_INVALID_ARGUMENT, "out_dtype must be dtype or fp32 (got %d)", out_dtype);
+  if (T == 0) return EXMOE_OK;
+  const int b = dtype_bytes(dtype), ob = dtype_bytes(out_dtype);
+  EXMOE_TRY(check_matrix("logits", logits, ldl, E, b));
+  EXMOE_TRY(check_int32("counts", counts, false));
+  if (!grad_losses || (uintptr_t)grad_losses % 4)
+    return set_error(EXMOE_ERR_INVALID_ARGUMENT, "grad_losses must be non-NULL and 4-byte aligned");
+  EXMOE_TRY(check_matrix("dlogits", dlogits, lddl, E, ob));
+  // (a row is read whole before it is written: dlogits may lie on logits of its type)
+  const bool in_place = dlogits == logits && b == ob && (ldl == lddl || T == 1);
+  const MemRows ml = mem_matrix("logits", logits, T, ldl, E, b), mc = mem_flat("counts", counts, (E + 1) * 4),
+                mm = mem_flat("mask", mask, T), mg = mem_flat("grad_losses", grad_losses, 8),
+                md = mem_matrix("dlogits", dlogits, T, lddl, E, ob);
+  if (!in_place) EXMOE_TRY(check_apart(md, {ml}));
+  EXMOE_TRY(check_apart(md, {mc, mm, mg}));
+  BalanceArgs a{};
+  a.l = logits; a.ldl = ldl; a.mask = mask; a.T = T; a.E = E; a.k = k; a.counts_in = counts; a.grad = grad_losses;
+  a.dl = dlogits; a.lddl = lddl; a.out_f32 = ob == 4;
+  return launched(by_dtype(dtype, [&](auto dt) {
+                    return by_lanes(E, [&](auto lanes) {
+                      constexpr int DT = decltype(dt)::value, LANES = decltype(lanes)::value;
+                      const unsigned blocks = (unsigned)(((size_t)T * LANES + kBalThreads - 1) / kBalThreads);
+                      ProfScope prof("balance_loss_bwd", stream);
+                      if (a.out_f32)
+                        EXMOE_LAUNCH(prof, (balance_bwd_kernel<DT, LANES, true>), dim3(blocks), dim3(kBalThreads), 0, stream, a);
+                      else
+                        EXMOE_LAUNCH(prof, (balance_bwd_kernel<DT, LANES, false>), dim3(blocks), dim3(kBalThreads), 0, stream, a);
+                      return hipGetLastError();
+                    });
+                  }),
+                  "exmoe_balance_loss_backward");
+}
