@@ -452,7 +452,9 @@ int exmoe_lora_linear(const void* x, size_t ldx, const void* w, size_t ldw, cons
  * and 32-bit values, q and scales need the alignment of their elements only, except where
  * exmoe_grouped_mm_fp8 reads them. An output that shares bytes with another operand is refused (it
  * may lie between another's rows), but for the in-place forms named below. Sums are made in a fixed
- * order: equal calls give equal bits. dtype: bf16, fp16 or fp32.
+ * order: equal calls give equal bits. dtype: bf16, fp16 or fp32. A call's arguments lie in a struct
+ * (host memory, read before the call returns; a binding that converts argument by argument spends more on
+ * twenty of them than on the launch).
  *
  * exmoe_rms_norm, rows t < T of H <= 16384 columns:
  *   h = x + residual in fp32, rounded to the residual's type into residual_out (it may be the
@@ -460,10 +462,10 @@ int exmoe_lora_linear(const void* x, size_t ldx, const void* w, size_t ldw, cons
  *   y = h / sqrt(mean(h^2) + eps) * w in fp32, rounded once into y (x's type; NULL: not
  *       written), and q, scale of the fp32 value (both NULL: not written)
  * w is x's type or fp32 (w_dtype), so is the residual (res_dtype; what is stored is what is
- * normed). T < 2^23.
+ * normed). T < 2^22.
  *
  * exmoe_quantize_fp8: q, scale of rows as they are. exmoe_swiglu_fp8: of silu(g) * u in fp32, g the
- * first and u the next I columns of gate_up; with weights, row r's scales are multiplied by
+ * first and u the next n columns of x; with weights (either call), row r's scales are multiplied by
  * weights[row_index[r]] (0 for an index outside [0, n_weights)), or by weights[r] without
  * row_index: a routing weight that the down product then carries to its output.
  * exmoe_quantize_fp8_weights: w [E, N, K] with one scale per 128 x 128 block, scale [E,
@@ -481,23 +483,66 @@ int exmoe_lora_linear(const void* x, size_t ldx, const void* w, size_t ldw, cons
  * rounding or less; 32-bit outputs take products and sums that lose nothing but fp32 roundings, at
  * half the rate. Products of two scales under 2^-126 lose bits. No workspace.
  * ---------------------------------------------------------------------------------- */
-int exmoe_rms_norm(const void* x, size_t ldx, const void* w, int w_dtype, const void* residual, size_t ldr, int res_dtype,
-                   void* residual_out, size_t ldro, float eps, int T, int H, int dtype, void* y, size_t ldy, uint8_t* q,
-                   size_t ldq, float* scale, size_t lds, hipStream_t stream);
+typedef struct exmoe_norm {
+  const void* x;
+  size_t ldx;
+  const void* w;
+  const void* residual; /* or NULL */
+  size_t ldr;
+  void* residual_out;
+  size_t ldro;
+  void* y;    /* or NULL */
+  size_t ldy;
+  uint8_t* q; /* or NULL, with scale */
+  size_t ldq;
+  float* scale;
+  size_t lds;
+  float eps;
+  int T, H, dtype, w_dtype, res_dtype;
+} exmoe_norm;
+int exmoe_rms_norm(const exmoe_norm* call, hipStream_t stream);
 
-int exmoe_quantize_fp8(const void* x, size_t ldx, int rows, int K, int dtype, uint8_t* q, size_t ldq, float* scale,
-                       size_t lds, hipStream_t stream);
+typedef struct exmoe_fp8_rows {
+  const void* x; /* [rows, n], or gate and up [rows, 2 n] */
+  size_t ldx;
+  const float* weights; /* or NULL */
+  const int32_t* row_index;
+  uint8_t* q; /* [rows, n] */
+  size_t ldq;
+  float* scale; /* [rows, ceil(n / 128)] */
+  size_t lds;
+  int n_weights, rows, n, dtype;
+} exmoe_fp8_rows;
+int exmoe_quantize_fp8(const exmoe_fp8_rows* call, hipStream_t stream);
+int exmoe_swiglu_fp8(const exmoe_fp8_rows* call, hipStream_t stream);
 
-int exmoe_swiglu_fp8(const void* gate_up, size_t ldx, const float* weights, int n_weights, const int32_t* row_index,
-                     int rows, int I, int dtype, uint8_t* q, size_t ldq, float* scale, size_t lds, hipStream_t stream);
+typedef struct exmoe_fp8_matrices {
+  const void* w;
+  size_t ldw, w_stride;
+  uint8_t* q;
+  size_t ldq, q_stride;
+  float* scale;
+  size_t lds, s_stride;
+  int E, N, K, dtype;
+} exmoe_fp8_matrices;
+int exmoe_quantize_fp8_weights(const exmoe_fp8_matrices* call, hipStream_t stream);
 
-int exmoe_quantize_fp8_weights(const void* w, size_t ldw, size_t w_stride, int E, int N, int K, int dtype, uint8_t* q,
-                               size_t ldq, size_t q_stride, float* scale, size_t lds, size_t s_stride, hipStream_t stream);
-
-int exmoe_grouped_mm_fp8(const uint8_t* x, size_t ldx, const float* x_scale, size_t ldxs, int x_rows,
-                         const int32_t* row_index, int row_div, const int32_t* expert_offsets, const uint8_t* w, size_t ldw,
-                         size_t w_stride, const float* w_scale, size_t ldws, size_t ws_stride, int rows, int N, int K, int E,
-                         int out_dtype, void* y, size_t ldy, hipStream_t stream);
+typedef struct exmoe_grouped_fp8 {
+  const uint8_t* x;
+  size_t ldx;
+  const float* x_scale;
+  size_t ldxs;
+  const int32_t* row_index; /* or NULL */
+  const int32_t* expert_offsets;
+  const uint8_t* w;
+  size_t ldw, w_stride;
+  const float* w_scale;
+  size_t ldws, ws_stride;
+  void* y;
+  size_t ldy;
+  int x_rows, row_div, rows, N, K, E, out_dtype;
+} exmoe_grouped_fp8;
+int exmoe_grouped_mm_fp8(const exmoe_grouped_fp8* call, hipStream_t stream);
 
 /* ------------------------------------------------------------------------------------
  * The losses that train a router, with their gradient (device, asynchronous): what keeps the
@@ -521,12 +566,20 @@ int exmoe_grouped_mm_fp8(const uint8_t* x, size_t ldx, const float* x_scale, siz
  * ---------------------------------------------------------------------------------- */
 size_t exmoe_balance_loss_workspace_bytes(int T, int E);
 
-int exmoe_balance_loss(const void* logits, size_t ldl, const int32_t* topk_ids, const uint8_t* mask, int T, int E, int k,
-                       int dtype, float* losses, int32_t* counts, void* workspace, size_t ws_bytes, hipStream_t stream);
-
-int exmoe_balance_loss_backward(const void* logits, size_t ldl, const int32_t* counts, const uint8_t* mask,
-                                const float* grad_losses, int T, int E, int k, int dtype, int out_dtype, void* dlogits,
-                                size_t lddl, hipStream_t stream);
+typedef struct exmoe_balance {
+  const void* logits;
+  size_t ldl;
+  const int32_t* topk_ids; /* backward: not read */
+  const uint8_t* mask;     /* or NULL */
+  float* losses;           /* backward: not read */
+  int32_t* counts;         /* forward: written, backward: read */
+  const float* grad_losses; /* this and the next two: backward only */
+  void* dlogits;
+  size_t lddl;
+  int T, E, k, dtype, out_dtype;
+} exmoe_balance;
+int exmoe_balance_loss(const exmoe_balance* call, void* workspace, size_t ws_bytes, hipStream_t stream);
+int exmoe_balance_loss_backward(const exmoe_balance* call, hipStream_t stream);
 
 /* ------------------------------------------------------------------------------------
  * Per-kernel timing for benchmarks (not part of the layer's semantics). While enabled,

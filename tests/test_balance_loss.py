@@ -17,11 +17,13 @@ L, IDS, MASK, LOSS, CNT, WSP, GRAD, DL = (i << 40 for i in range(1, 9))
 
 
 def fwd(l=L, ldl=8, ids=IDS, mask=None, T=40, E=8, k=2, dt=0, losses=LOSS, counts=CNT, ws=WSP, wsb=1 << 20):
-    return exm._lib.exmoe_balance_loss(l, ldl, ids, mask, T, E, k, dt, losses, counts, ws, wsb, None)
+    return exm._lib.exmoe_balance_loss(exm._BALANCE.pack(*(v or 0 for v in (l, ldl, ids, mask, losses, counts, 0, 0, 0)), T, E, k, dt, 0),
+                                       ws, wsb, None)
 
 
 def bwd(l=L, ldl=8, counts=CNT, mask=None, grad=GRAD, T=40, E=8, k=2, dt=0, od=0, dl=DL, lddl=8):
-    return exm._lib.exmoe_balance_loss_backward(l, ldl, counts, mask, grad, T, E, k, dt, od, dl, lddl, None)
+    return exm._lib.exmoe_balance_loss_backward(
+        exm._BALANCE.pack(*(v or 0 for v in (l, ldl, 0, mask, 0, counts, grad, dl, lddl)), T, E, k, dt, od), None)
 
 
 def test_refusals():

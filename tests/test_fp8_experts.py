@@ -74,25 +74,40 @@ def on_gpu(v, shift=0, more=0, fill=float("nan")):
 # ------------------------------------------------------------------ refusals (no GPU)
 def norm(x=X, ldx=256, w=W, wd=0, r=None, ldr=256, rd=0, ro=None, ldro=256, eps=1e-6, T=4, H=256, dt=0, y=Y, ldy=256, q=None,
          ldq=256, s=None, lds=2):
-    return exm._lib.exmoe_rms_norm(x, ldx, w, wd, r, ldr, rd, ro, ldro, eps, T, H, dt, y, ldy, q, ldq, s, lds, None)
+    return exm._lib.exmoe_rms_norm(exm._NORM.pack(*(v or 0 for v in (x, ldx, w, r, ldr, ro, ldro, y, ldy, q, ldq, s, lds)), eps, T, H,
+                                                  dt, wd, rd), None)
 
 
-def quant(x=X, ldx=256, rows=4, K=256, dt=0, q=Q, ldq=256, s=S, lds=2):
-    return exm._lib.exmoe_quantize_fp8(x, ldx, rows, K, dt, q, ldq, s, lds, None)
+def rows_of(x, ldx, w, ri, q, ldq, s, lds, n, rows, K, dt):
+    return exm._FP8_ROWS.pack(*(v or 0 for v in (x, ldx, w, ri, q, ldq, s, lds)), n, rows, K, dt)
+
+
+def quant(x=X, ldx=256, w=None, n=0, ri=None, rows=4, K=256, dt=0, q=Q, ldq=256, s=S, lds=2):
+    return exm._lib.exmoe_quantize_fp8(rows_of(x, ldx, w, ri, q, ldq, s, lds, n, rows, K, dt), None)
 
 
 def swiglu(x=X, ldx=512, w=None, n=0, ri=None, rows=4, I=256, dt=0, q=Q, ldq=256, s=S, lds=2):
-    return exm._lib.exmoe_swiglu_fp8(x, ldx, w, n, ri, rows, I, dt, q, ldq, s, lds, None)
+    return exm._lib.exmoe_swiglu_fp8(rows_of(x, ldx, w, ri, q, ldq, s, lds, n, rows, I, dt), None)
 
 
 def quantw(w=W, ldw=256, wst=256 * 100, E=3, N=100, K=256, dt=0, q=Q, ldq=256, qst=256 * 100, s=S, lds=2, sst=2):
-    return exm._lib.exmoe_quantize_fp8_weights(w, ldw, wst, E, N, K, dt, q, ldq, qst, s, lds, sst, None)
+    return exm._lib.exmoe_quantize_fp8_weights(
+        exm._FP8_MATRICES.pack(*(v or 0 for v in (w, ldw, wst, q, ldq, qst, s, lds, sst)), E, N, K, dt), None)
 
 
 def mm(x=X, ldx=256, xs=XS, ldxs=2, x_rows=8, ri=None, div=1, off=OFF, w=W, ldw=256, wst=256 * 100, ws=WS, ldws=2, wsst=2, rows=8,
        N=100, K=256, E=3, od=0, y=Y, ldy=100):
-    return exm._lib.exmoe_grouped_mm_fp8(x, ldx, xs, ldxs, x_rows, ri, div, off, w, ldw, wst, ws, ldws, wsst, rows, N, K, E, od, y,
-                                         ldy, None)
+    return exm._lib.exmoe_grouped_mm_fp8(exm._GROUPED_FP8.pack(
+        *(v or 0 for v in (x, ldx, xs, ldxs, ri, off, w, ldw, wst, ws, ldws, wsst, y, ldy)), x_rows, div, rows, N, K, E, od), None)
+
+
+def test_the_structs_are_those_of_the_header():
+    """Sizes of the C structs: pointers and sizes of 8 bytes, then 4-byte values, padded to 8."""
+    for st, wide, narrow in ((exm._NORM, 13, 6), (exm._FP8_ROWS, 8, 4), (exm._FP8_MATRICES, 9, 4), (exm._GROUPED_FP8, 14, 7), (exm._BALANCE, 9, 5)):
+        assert st.size == (8 * wide + 4 * narrow + 7) // 8 * 8
+    for name in ("rms_norm", "quantize_fp8", "swiglu_fp8", "quantize_fp8_weights", "grouped_mm_fp8", "balance_loss_backward"):
+        assert getattr(exm._lib, "exmoe_" + name)(None, None) == INV
+    assert exm._lib.exmoe_balance_loss(None, None, 0, None) == INV
 
 
 def refuses(call, status, **cases):
@@ -107,7 +122,7 @@ def test_refusals_of_the_norm():
             eps=[-1.0, float("nan"), float("inf")], pair=[dict(q=Q), dict(s=S), dict(r=R), dict(ro=RO), dict(y=None)],
             fp8=[dict(q=Q, s=S, ldq=255), dict(q=Q, s=S + 2), dict(q=Q, s=S, lds=1)],
             res=[dict(r=R, ro=RO, rd=1), dict(r=R + 1, ro=RO), dict(r=R, ro=RO, ldr=200), dict(r=R, ro=RO, ldro=255)])
-    refuses(norm, UNS, H=[16385], T=[1 << 23])
+    refuses(norm, UNS, H=[16385], T=[1 << 22])
     assert norm(T=0, x=None, y=Y) == 0
 
 
@@ -298,8 +313,8 @@ def norm_ref(x, w, eps, residual=None):
     return h, h / torch.sqrt((h * h).mean(1, keepdim=True) + eps) * w.double()
 
 
-# the sum of squares: 16 chunks of 8 and their sums one after another at most, then the lanes and
-# waves: 50 roundings of 2^-24, half of them after the square root; division, root and products 6
+# the sum of squares: 2 chunks of 8 one after another, then the lanes (8 steps) and at most 16 waves: under
+# 50 roundings of 2^-24, half of them after the square root; division, root and products 6
 NORM_DELTA = 31 * 2.0 ** -24
 
 

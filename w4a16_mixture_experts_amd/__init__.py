@@ -9,8 +9,9 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import numpy as np
 
@@ -46,6 +47,7 @@ DTYPE_BF16, DTYPE_FP16, DTYPE_FP32 = 0, 1, 2
 GROUPED_MM, GROUPED_DGRAD, GROUPED_WGRAD = 0, 1, 2
 
 _vp = ctypes.c_void_p
+_cp = ctypes.c_char_p      # a struct of arguments, packed into bytes
 _i = ctypes.c_int
 _sz = ctypes.c_size_t
 
@@ -115,16 +117,14 @@ _SIGS = {
                                     _vp]),
     "exmoe_grouped_mm_wgrad": (_i, [_vp, _sz, _vp, _sz, _i, _vp, _i, _vp, _i, _i, _i, _i, _i, _i, _vp, _sz, _sz, _vp,
                                     _sz, _vp]),
-    "exmoe_rms_norm": (_i, [_vp, _sz, _vp, _i, _vp, _sz, _i, _vp, _sz, ctypes.c_float, _i, _i, _i, _vp, _sz, _vp, _sz, _vp,
-                            _sz, _vp]),
-    "exmoe_quantize_fp8": (_i, [_vp, _sz, _i, _i, _i, _vp, _sz, _vp, _sz, _vp]),
-    "exmoe_swiglu_fp8": (_i, [_vp, _sz, _vp, _i, _vp, _i, _i, _i, _vp, _sz, _vp, _sz, _vp]),
-    "exmoe_quantize_fp8_weights": (_i, [_vp, _sz, _sz, _i, _i, _i, _i, _vp, _sz, _sz, _vp, _sz, _sz, _vp]),
-    "exmoe_grouped_mm_fp8": (_i, [_vp, _sz, _vp, _sz, _i, _vp, _i, _vp, _vp, _sz, _sz, _vp, _sz, _sz, _i, _i, _i, _i, _i, _vp,
-                                  _sz, _vp]),
+    "exmoe_rms_norm": (_i, [_cp, _vp]),
+    "exmoe_quantize_fp8": (_i, [_cp, _vp]),
+    "exmoe_swiglu_fp8": (_i, [_cp, _vp]),
+    "exmoe_quantize_fp8_weights": (_i, [_cp, _vp]),
+    "exmoe_grouped_mm_fp8": (_i, [_cp, _vp]),
     "exmoe_balance_loss_workspace_bytes": (_sz, [_i, _i]),
-    "exmoe_balance_loss": (_i, [_vp, _sz, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _vp, _sz, _vp]),
-    "exmoe_balance_loss_backward": (_i, [_vp, _sz, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _sz, _vp]),
+    "exmoe_balance_loss": (_i, [_cp, _vp, _sz, _vp]),
+    "exmoe_balance_loss_backward": (_i, [_cp, _vp]),
     "exmoe_lora_workspace_bytes": (_sz, [_i] * 5),
     "exmoe_lora_linear": (_i, [_vp, _sz, _vp, _sz, ctypes.POINTER(LoraBankC), _vp, _i, _i, _i, _i, _vp, _sz, _vp, _sz,
                                _vp]),
@@ -482,13 +482,6 @@ def _no_gradient():
                          "torch.no_grad() (an autograd function around grouped_mm calls grouped_mm_dgrad and grouped_mm_wgrad)")
 
 
-def _needs_no_gradient(*tensors):
-    for t in tensors:
-        if t is not None and t.requires_grad:
-            _no_gradient()
-            return
-
-
 def grouped_mm_workspace_bytes(op: int, rows: int, N: int, K: int, E: int, k: int = 0) -> int:
     return _lib.exmoe_grouped_mm_workspace_bytes(op, rows, N, K, E, k)
 
@@ -626,39 +619,74 @@ def lora_linear(x, w, bank: LoraBank, ids, y=None, workspace=None):
 
 
 # ----------------------------------------------------------------------------- experts in 8 bits
-def _f8_rows(name: str, t, dev: int, ndim: int = 2) -> int:
-    ld = _rows_ld(name, t, ndim)
-    if t.dtype is not _torch().float8_e4m3fn or t.get_device() != dev:
-        raise ValueError(f"{name} must be float8_e4m3fn on GPU {dev}")
-    return ld
+# Argument structs of exmoe.h: pointers and sizes, then ints. (One bytes object per call: ctypes
+# spends about 0.1 us on each argument of its own.)
+_NORM = struct.Struct("13Qf5i")
+_FP8_ROWS = struct.Struct("8Q4i")
+_FP8_MATRICES = struct.Struct("9Q4i")
+_GROUPED_FP8 = struct.Struct("14Q7i4x")
+_BALANCE = struct.Struct("9Q5i4x")
 
 
-def _scales(name: str, t, shape, dev: int) -> int:
-    ld = _rows_ld(name, t, len(shape))
-    if t.shape != shape or t.dtype is not _torch().float32 or t.get_device() != dev:
-        raise ValueError(f"{name} must be {tuple(shape)} float32 on GPU {dev}")
-    return ld
+def _wrong(name: str, t, shape, dtype, dev: int):
+    if t.dtype is dtype and t.get_device() == dev and t.shape == shape:
+        raise ValueError(f"{name}: the last axis must be contiguous")
+    raise ValueError(f"{name} must be {tuple(shape)} {dtype} on GPU {dev} (got {tuple(t.shape)} {t.dtype})")
+
+
+def _mat(name: str, t, shape, dtype, dev: int):
+    """(pointer, elements between rows) of a matrix of this shape and type on GPU dev, last axis contiguous."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
+        _wrong(name, t, shape, dtype, dev)
+    ld, one = t.stride()
+    if one != 1 and shape[1] > 1:
+        _wrong(name, t, shape, dtype, dev)
+    return t.data_ptr(), ld if shape[0] > 1 else shape[1]   # (the stride of a single row means nothing)
+
+
+def _mats(name: str, t, shape, dtype, dev: int):
+    """(pointer, elements between rows, between experts) of one matrix per expert."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
+        _wrong(name, t, shape, dtype, dev)
+    stride, ld, one = t.stride()
+    if one != 1 and shape[2] > 1:
+        _wrong(name, t, shape, dtype, dev)
+    return t.data_ptr(), ld if shape[1] > 1 else shape[2], stride
+
+
+def _axes(name: str, t, n: int):
+    """The shape of a tensor of n axes."""
+    shape = t.shape
+    if len(shape) != n:
+        raise ValueError(f"{name} must have {n} axes (got shape {tuple(shape)})")
+    return shape
+
+
+def _on_gpu(name: str, t) -> int:
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a GPU tensor")
+    return dev
 
 
 def _f8_outputs(q, scale, rows: int, K: int, dev: int, like):
-    """The given outputs, or new ones: q with rows of a multiple of 16 bytes, as the product reads them."""
-    torch = _torch()
+    """The given outputs, or new ones (q with rows of a multiple of 16 bytes, as the product reads
+    them), and their pointers and strides."""
+    torch = _TORCH or _torch()
     if q is None:
         q = like.new_empty((rows, (K + 15) // 16 * 16), dtype=torch.float8_e4m3fn)[:, :K]
-    elif q.shape != (rows, K):
-        raise ValueError(f"q must be {(rows, K)} (got {tuple(q.shape)})")
     if scale is None:
         scale = like.new_empty((rows, (K + 127) // 128), dtype=torch.float32)
-    return q, scale, _f8_rows("q", q, dev), _scales("scale", scale, (rows, (K + 127) // 128), dev)
+    return q, scale, (_mat("q", q, (rows, K), torch.float8_e4m3fn, dev)
+                      + _mat("scale", scale, (rows, (K + 127) // 128), torch.float32, dev))
 
 
-@dataclass
-class NormOutputs:
+class NormOutputs(NamedTuple):
     """What rms_norm wrote (None: not asked for)."""
-    y: object = None          # [T, H] of x's type
-    q: object = None          # [T, H] float8_e4m3fn
-    scale: object = None      # [T, ceil(H / 128)] float32
-    residual: object = None   # [T, H]: x + residual
+    y: object          # [T, H] of x's type
+    q: object          # [T, H] float8_e4m3fn
+    scale: object      # [T, ceil(H / 128)] float32
+    residual: object   # [T, H]: x + residual
 
 
 def rms_norm(x, w, eps: float = 1e-6, residual=None, out: str = "y", y=None, q=None, scale=None, residual_out=None) -> NormOutputs:
@@ -667,50 +695,52 @@ def rms_norm(x, w, eps: float = 1e-6, residual=None, out: str = "y", y=None, q=N
     x [T, H] (bf16, fp16 or fp32), w [H] and residual [T, H] of x's type or fp32. out: "y" (x's
     type), "fp8" (e4m3 q with a scale per 128 columns) or "both". h is rounded to the residual's type
     and written to residual_out (a new tensor, or the residual itself). Records no gradient."""
-    _needs_no_gradient(x, w, residual, y, residual_out)
-    torch = _torch()
-    if out not in ("y", "fp8", "both"):
-        raise ValueError(f'out must be "y", "fp8" or "both" (got {out!r})')
-    ldx = _rows_ld("x", x)
-    T, H = x.shape
-    dev, dtype = x.get_device(), x.dtype
-    if w.shape != (H,) or not w.is_contiguous() or w.get_device() != dev:
+    if (x.requires_grad or w.requires_grad or residual is not None and (residual.requires_grad or residual_out is not None
+                                                                        and residual_out.requires_grad)
+            or y is not None and y.requires_grad):
+        _no_gradient()
+    dev, dtype = _on_gpu("x", x), x.dtype
+    T, H = shape = _axes("x", x, 2)
+    px, ldx = _mat("x", x, shape, dtype, dev)
+    if w.shape != (H,) or w.get_device() != dev or not w.is_contiguous():
         raise ValueError(f"w must be a contiguous tensor of {H} on GPU {dev}")
-    r = NormOutputs()
-    res = [None, 0, 0, None, 0]
+    pr = ldr = po = ldo = py = ldy = res_code = 0
+    f8 = (0, 0, 0, 0)
     if residual is not None:
-        if residual.shape != (T, H) or residual.get_device() != dev:
-            raise ValueError(f"residual must be {(T, H)} on GPU {dev}")
-        ldr = _rows_ld("residual", residual)
-        r.residual = _result("residual_out", residual_out, (T, H), residual.dtype, dev, residual)
-        res = [residual.data_ptr(), ldr, _dtype_code(residual.dtype), r.residual.data_ptr(), _rows_ld("residual_out", r.residual)]
+        res_dtype = residual.dtype
+        pr, ldr = _mat("residual", residual, shape, res_dtype, dev)
+        res_code = _dtype_code(res_dtype)
+        if residual_out is None:
+            residual_out = residual.new_empty(shape)
+        po, ldo = _mat("residual_out", residual_out, shape, res_dtype, dev)
     elif residual_out is not None:
         raise ValueError("residual_out without a residual")
-    o = [None, 0, None, 0, None, 0]
-    if out != "fp8":
-        r.y = _result("y", y, (T, H), dtype, dev, x)
-        o[0:2] = [r.y.data_ptr(), _rows_ld("y", r.y)]
+    if out == "y" or out == "both":
+        if y is None:
+            y = x.new_empty(shape)
+        py, ldy = _mat("y", y, shape, dtype, dev)
+    elif out != "fp8":
+        raise ValueError(f'out must be "y", "fp8" or "both" (got {out!r})')
     elif y is not None:
         raise ValueError('y with out="fp8"')
     if out != "y":
-        r.q, r.scale, ldq, lds = _f8_outputs(q, scale, T, H, dev, x)
-        o[2:6] = [r.q.data_ptr(), ldq, r.scale.data_ptr(), lds]
+        q, scale, f8 = _f8_outputs(q, scale, T, H, dev, x)
     elif q is not None or scale is not None:
         raise ValueError('q or scale with out="y"')
-    _run_on(dev, _lib.exmoe_rms_norm, x.data_ptr(), ldx, w.data_ptr(), _dtype_code(w.dtype), *res, eps, T, H,
-            _dtype_code(dtype), *o)
-    return r
+    _run_on(dev, _lib.exmoe_rms_norm, _NORM.pack(px, ldx, w.data_ptr(), pr, ldr, po, ldo, py, ldy, *f8, eps, T, H,
+                                                 _dtype_code(dtype), _dtype_code(w.dtype), res_code))
+    return NormOutputs(y, q, scale, residual_out)
 
 
 def quantize_fp8(x, q=None, scale=None):
     """(q, scale) of x [rows, K] (bf16, fp16 or fp32): e4m3 with a scale per 128 columns of a row."""
-    _needs_no_gradient(x)
-    ldx = _rows_ld("x", x)
-    rows, K = x.shape
-    dev = x.get_device()
-    q, scale, ldq, lds = _f8_outputs(q, scale, rows, K, dev, x)
-    _run_on(dev, _lib.exmoe_quantize_fp8, x.data_ptr(), ldx, rows, K, _dtype_code(x.dtype), q.data_ptr(), ldq,
-            scale.data_ptr(), lds)
+    if x.requires_grad:
+        _no_gradient()
+    dev, dtype = _on_gpu("x", x), x.dtype
+    rows, K = shape = _axes("x", x, 2)
+    px, ldx = _mat("x", x, shape, dtype, dev)
+    q, scale, f8 = _f8_outputs(q, scale, rows, K, dev, x)
+    _run_on(dev, _lib.exmoe_quantize_fp8, _FP8_ROWS.pack(px, ldx, 0, 0, *f8, 0, rows, K, _dtype_code(dtype)))
     return q, scale
 
 
@@ -718,38 +748,42 @@ def swiglu_fp8(gate_up, weights=None, row_index=None, q=None, scale=None):
     """(q, scale) of silu(gate) * up [rows, I], gate_up [rows, 2 I] with the gate's columns first.
     weights fp32 (any shape, contiguous): row r's scales are multiplied by weights.view(-1)[row_index[r]]
     (row_index int32 [rows]: sorted_flat of a routed batch), or by its r-th without row_index."""
-    _needs_no_gradient(gate_up, weights)
-    ldx = _rows_ld("gate_up", gate_up)
-    rows, cols = gate_up.shape
+    if gate_up.requires_grad or weights is not None and weights.requires_grad:
+        _no_gradient()
+    dev, dtype = _on_gpu("gate_up", gate_up), gate_up.dtype
+    rows, cols = shape = _axes("gate_up", gate_up, 2)
+    px, ldx = _mat("gate_up", gate_up, shape, dtype, dev)
     if cols % 2:
         raise ValueError(f"gate_up has {cols} columns: gate and up side by side are an even number")
-    dev, I = gate_up.get_device(), cols // 2
-    if weights is not None and (weights.dtype is not _torch().float32 or weights.get_device() != dev or not weights.is_contiguous()):
-        raise ValueError(f"weights must be a contiguous float32 tensor on GPU {dev}")
-    q, scale, ldq, lds = _f8_outputs(q, scale, rows, I, dev, gate_up)
-    _run_on(dev, _lib.exmoe_swiglu_fp8, gate_up.data_ptr(), ldx, _ptr(weights), 0 if weights is None else weights.numel(),
-            _int32("row_index", row_index, dev, rows), rows, I, _dtype_code(gate_up.dtype), q.data_ptr(), ldq,
-            scale.data_ptr(), lds)
+    pw = n = 0
+    if weights is not None:
+        if weights.dtype is not _torch().float32 or weights.get_device() != dev or not weights.is_contiguous():
+            raise ValueError(f"weights must be a contiguous float32 tensor on GPU {dev}")
+        pw, n = weights.data_ptr(), weights.numel()
+    I = cols // 2
+    q, scale, f8 = _f8_outputs(q, scale, rows, I, dev, gate_up)
+    _run_on(dev, _lib.exmoe_swiglu_fp8, _FP8_ROWS.pack(px, ldx, pw, _int32("row_index", row_index, dev, rows) or 0, *f8, n, rows,
+                                                       I, _dtype_code(dtype)))
     return q, scale
 
 
 def quantize_fp8_weights(w, q=None, scale=None):
     """(q, scale) of w [E, N, K] (bf16, fp16 or fp32): e4m3 with a scale per 128 x 128 block, scale
     fp32 [E, ceil(N / 128), ceil(K / 128)]."""
-    _needs_no_gradient(w)
-    ldw = _rows_ld("w", w, 3)
-    E, N, K = w.shape
-    dev = w.get_device()
-    if q is None:
-        q = w.new_empty((E, N, (K + 15) // 16 * 16), dtype=_torch().float8_e4m3fn)[..., :K]
-    elif q.shape != w.shape:
-        raise ValueError(f"q must be {tuple(w.shape)} (got {tuple(q.shape)})")
+    if w.requires_grad:
+        _no_gradient()
+    torch = _torch()
+    dev, dtype = _on_gpu("w", w), w.dtype
+    E, N, K = shape = _axes("w", w, 3)
+    pw = _mats("w", w, shape, dtype, dev)
     blocks = (E, (N + 127) // 128, (K + 127) // 128)
+    if q is None:
+        q = w.new_empty((E, N, (K + 15) // 16 * 16), dtype=torch.float8_e4m3fn)[..., :K]
     if scale is None:
-        scale = w.new_empty(blocks, dtype=_torch().float32)
-    ldq, lds = _f8_rows("q", q, dev, 3), _scales("scale", scale, blocks, dev)
-    _run_on(dev, _lib.exmoe_quantize_fp8_weights, w.data_ptr(), ldw, w.stride(0), E, N, K, _dtype_code(w.dtype), q.data_ptr(),
-            ldq, q.stride(0), scale.data_ptr(), lds, scale.stride(0))
+        scale = w.new_empty(blocks, dtype=torch.float32)
+    _run_on(dev, _lib.exmoe_quantize_fp8_weights, _FP8_MATRICES.pack(*pw, *_mats("q", q, shape, torch.float8_e4m3fn, dev),
+                                                                     *_mats("scale", scale, blocks, torch.float32, dev), E, N, K,
+                                                                     _dtype_code(dtype)))
     return q, scale
 
 
@@ -761,29 +795,37 @@ def grouped_mm_fp8(x, x_scale, w, w_scale, offsets=None, row_index=None, row_div
     row_index and row_div as in grouped_mm, offsets None for one expert with every row. Returns y
     [rows, N] in out_dtype (bf16, the default, fp16 or fp32); rows outside every segment are left
     as they are."""
-    _needs_no_gradient(x_scale, w_scale, y)
-    dev = x.get_device()
-    ldx, ldw = _f8_rows("x", x, dev), _f8_rows("w", w, dev, 3)
-    E, N, K = w.shape
-    x_rows, x_cols = x.shape
-    if x_cols != K:
-        raise ValueError(f"x has {x_cols} columns, w takes {K}")
-    kb = (K + 127) // 128
-    ldxs, ldws = _scales("x_scale", x_scale, (x_rows, kb), dev), _scales("w_scale", w_scale, (E, (N + 127) // 128, kb), dev)
-    rows = x_rows if row_index is None else row_index.numel()
-    out_dtype = _torch().bfloat16 if out_dtype is None else out_dtype
-    y = _result("y", y, (rows, N), out_dtype, dev, x)
-    _run_on(dev, _lib.exmoe_grouped_mm_fp8, x.data_ptr(), ldx, x_scale.data_ptr(), ldxs, x_rows,
-            _int32("row_index", row_index, dev), row_div, _int32("offsets", offsets, dev, E + 1), w.data_ptr(), ldw,
-            w.stride(0), w_scale.data_ptr(), ldws, w_scale.stride(0), rows, N, K, E, _dtype_code(out_dtype), y.data_ptr(),
-            _rows_ld("y", y))
+    if x_scale.requires_grad or w_scale.requires_grad or y is not None and y.requires_grad:
+        _no_gradient()
+    torch = _TORCH or _torch()
+    dev, f8, f32 = _on_gpu("x", x), torch.float8_e4m3fn, torch.float32
+    E, N, K = shape = _axes("w", w, 3)
+    pw, ldw, sw = _mats("w", w, shape, f8, dev)
+    rows, cols = shape = _axes("x", x, 2)
+    if cols != K:
+        raise ValueError(f"x has {cols} columns, w takes {K}")
+    px, ldx = _mat("x", x, shape, f8, dev)
+    kb, x_rows, pi, pf = (K + 127) // 128, rows, 0, 0
+    pxs, ldxs = _mat("x_scale", x_scale, (rows, kb), f32, dev)
+    pws, ldws, sws = _mats("w_scale", w_scale, (E, (N + 127) // 128, kb), f32, dev)
+    if row_index is not None:
+        rows, pi = row_index.numel(), _int32("row_index", row_index, dev)
+    if offsets is not None:
+        pf = _int32("offsets", offsets, dev, E + 1)
+    if out_dtype is None:
+        out_dtype = torch.bfloat16
+    if y is None:
+        y = x.new_empty((rows, N), dtype=out_dtype)
+    py, ldy = _mat("y", y, (rows, N), out_dtype, dev)
+    _run_on(dev, _lib.exmoe_grouped_mm_fp8, _GROUPED_FP8.pack(px, ldx, pxs, ldxs, pi, pf, pw, ldw, sw, pws, ldws, sws, py, ldy,
+                                                              x_rows, row_div, rows, N, K, E, _dtype_code(out_dtype)))
     return y
 
 
 # ----------------------------------------------------------------------------- router losses
-def _mask(mask, T: int, dev: int):
+def _mask(mask, T: int, dev: int) -> int:
     if mask is None:
-        return None
+        return 0
     if mask.dtype not in (_torch().bool, _torch().uint8) or mask.get_device() != dev or not mask.is_contiguous() or mask.numel() != T:
         raise ValueError(f"mask must be a contiguous bool tensor of {T} on GPU {dev}")
     return mask.data_ptr()
@@ -799,19 +841,22 @@ def balance_loss(logits, ids, mask=None, losses=None, counts=None, workspace=Non
     sum_e f_e P_e (f: share of the routed pairs, P: mean probability), losses[1] = mean squared
     log-sum-exp, counts: pairs per expert, then the number of tokens. Records no gradient: an autograd
     function around it calls balance_loss_backward."""
-    _needs_no_gradient(logits, losses)
-    ldl = _rows_ld("logits", logits)
-    T, E = logits.shape
-    dev = logits.get_device()
+    if logits.requires_grad or losses is not None and losses.requires_grad:
+        _no_gradient()
+    torch = _torch()
+    dev, dtype = _on_gpu("logits", logits), logits.dtype
+    T, E = shape = _axes("logits", logits, 2)
+    pl, ldl = _mat("logits", logits, shape, dtype, dev)
     if ids.dim() != 2 or ids.shape[0] != T:
         raise ValueError(f"ids must be [{T}, k] (got {tuple(ids.shape)})")
-    losses = _result("losses", losses, (2,), _torch().float32, dev, logits)
-    counts = _result("counts", counts, (E + 1,), _torch().int32, dev, logits)
+    losses = _result("losses", losses, (2,), torch.float32, dev, logits)
+    counts = _result("counts", counts, (E + 1,), torch.int32, dev, logits)
     if not losses.is_contiguous() or not counts.is_contiguous():
         raise ValueError("losses and counts must be contiguous")
     ws, ws_bytes, _keep = _scratch(workspace, lambda: balance_loss_workspace_bytes(T, E), dev)
-    _run_on(dev, _lib.exmoe_balance_loss, logits.data_ptr(), ldl, _int32("ids", ids, dev), _mask(mask, T, dev), T, E,
-            ids.shape[1], _dtype_code(logits.dtype), losses.data_ptr(), counts.data_ptr(), ws, ws_bytes)
+    _run_on(dev, _lib.exmoe_balance_loss, _BALANCE.pack(pl, ldl, _int32("ids", ids, dev), _mask(mask, T, dev), losses.data_ptr(),
+                                                        counts.data_ptr(), 0, 0, 0, T, E, ids.shape[1], _dtype_code(dtype), 0),
+            ws, ws_bytes)
     return losses, counts
 
 
@@ -819,17 +864,22 @@ def balance_loss_backward(logits, counts, k: int, grad_losses, mask=None, out_dt
     """Gradient of grad_losses[0] * losses[0] + grad_losses[1] * losses[1] (fp32 [2], on the GPU) with
     respect to logits: [T, E] in out_dtype (logits' type, the default, or fp32). counts: what
     balance_loss returned. dlogits may be logits itself."""
-    _needs_no_gradient(logits, grad_losses, dlogits)
-    ldl = _rows_ld("logits", logits)
-    T, E = logits.shape
-    dev = logits.get_device()
-    if grad_losses.dtype is not _torch().float32 or grad_losses.get_device() != dev or not grad_losses.is_contiguous() or grad_losses.numel() != 2:
+    if logits.requires_grad or grad_losses.requires_grad or dlogits is not None and dlogits.requires_grad:
+        _no_gradient()
+    dev, dtype = _on_gpu("logits", logits), logits.dtype
+    T, E = shape = _axes("logits", logits, 2)
+    pl, ldl = _mat("logits", logits, shape, dtype, dev)
+    if (grad_losses.dtype is not _torch().float32 or grad_losses.get_device() != dev or not grad_losses.is_contiguous()
+            or grad_losses.numel() != 2):
         raise ValueError(f"grad_losses must be a contiguous float32 tensor of 2 on GPU {dev}")
-    out_dtype = logits.dtype if out_dtype is None else out_dtype
-    dlogits = _result("dlogits", dlogits, (T, E), out_dtype, dev, logits)
-    _run_on(dev, _lib.exmoe_balance_loss_backward, logits.data_ptr(), ldl, _int32("counts", counts, dev, E + 1),
-            _mask(mask, T, dev), grad_losses.data_ptr(), T, E, k, _dtype_code(logits.dtype), _dtype_code(out_dtype),
-            dlogits.data_ptr(), _rows_ld("dlogits", dlogits))
+    if out_dtype is None:
+        out_dtype = dtype
+    if dlogits is None:
+        dlogits = logits.new_empty(shape, dtype=out_dtype)
+    pd, ldd = _mat("dlogits", dlogits, shape, out_dtype, dev)
+    _run_on(dev, _lib.exmoe_balance_loss_backward,
+            _BALANCE.pack(pl, ldl, 0, _mask(mask, T, dev), 0, _int32("counts", counts, dev, E + 1), grad_losses.data_ptr(), pd, ldd, T,
+                          E, k, _dtype_code(dtype), _dtype_code(out_dtype)))
     return dlogits
 
 

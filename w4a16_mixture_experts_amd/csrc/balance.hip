@@ -67,9 +67,11 @@ __device__ __forceinline__ bool row_softmax(f32x8 l, f32x8& p, float& lse) {
   for (int i = 1; i < 8; i++) top = fmaxf(top, l[i]);
   top = lanes_max<LANES>(top);
   const bool some = !(top == kNoLogit);
+  // (2^x of the rounded product x = (l - top) log2(e): off by (1 + |l - top|) 2^-24, which is small where
+  // p is not)
 #pragma unroll
   for (int i = 0; i < 8; i++) {
-    p[i] = expf(l[i] - (some ? top : 0.f));
+    p[i] = __builtin_amdgcn_exp2f((l[i] - (some ? top : 0.f)) * 1.4426950408889634f);
     s += p[i];
   }
   s = lanes_sum<LANES>(s);
@@ -81,16 +83,61 @@ __device__ __forceinline__ bool row_softmax(f32x8 l, f32x8& p, float& lse) {
   return has;
 }
 
-template <int DT>
-__device__ __forceinline__ f32x8 load_logits(const BalanceArgs& a, int row, int c) {
-  f32x8 v = load_upto8<DT>(a.l, (size_t)row * a.ldl + c, a.E - c);
+// Columns of a lane (the l-th of its row's): 8 l .. 8 l + 7, or, where rows of 32 bits are read or written, 4 l .. 4 l + 3
+// and as many behind the first 4 LANES, so that neighbouring lanes always touch neighbouring 16 bytes.
+template <int LANES, bool SPLIT>
+struct LaneCols {
+  int c;
+  __device__ __forceinline__ explicit LaneCols(int l) : c(SPLIT ? 4 * l : 8 * l) {}
+  __device__ __forceinline__ int at(int i) const { return c + i + (SPLIT && i >= 4 ? 4 * LANES - 4 : 0); }
+  template <int DT>
+  __device__ __forceinline__ f32x8 load(const void* p, size_t row, int E) const {   // (past E: no logit)
+    f32x8 v;
+    if constexpr (SPLIT) {
 #pragma unroll
-  for (int i = 0; i < 8; i++)
-    if (c + i >= a.E) v[i] = kNoLogit;
-  return v;
-}
+      for (int h = 0; h < 2; h++) {
+        const int c0 = at(4 * h);
+        f32x4 w = {kNoLogit, kNoLogit, kNoLogit, kNoLogit};
+        if (c0 + 4 <= E) {
+          w = Elems<DT>::load4(p, row + c0);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 3; i++)
+            if (c0 + i < E) w[i] = Elems<DT>::get(p, row + c0 + i);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; i++) v[4 * h + i] = w[i];
+      }
+    } else {
+      v = load_upto8<DT>(p, row + c, E - c);
+#pragma unroll
+      for (int i = 0; i < 8; i++)
+        if (c + i >= E) v[i] = kNoLogit;
+    }
+    return v;
+  }
+  template <int DT>
+  __device__ __forceinline__ void store(void* p, size_t row, int E, f32x8 v) const {
+    if constexpr (SPLIT) {
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        const int c0 = at(4 * h);
+        if (c0 + 4 <= E) {
+          Elems<DT>::store4(p, row + c0, f32x4{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]});
+        } else {
+#pragma unroll
+          for (int i = 0; i < 3; i++)
+            if (c0 + i < E) Elems<DT>::put(p, row + c0 + i, v[4 * h + i]);
+        }
+      }
+    } else if (c < E) {
+      store_upto8<DT>(p, row + c, E - c, v);
+    }
+  }
+};
 
 constexpr int kBalThreads = 256;
+constexpr int kBwdRows = 4;   // rows of a lane in the backward pass, loaded together
 
 // LANES lanes per row; a workgroup takes every gridDim.x-th run of rows.
 template <int DT, int LANES>
@@ -98,7 +145,8 @@ __global__ __launch_bounds__(kBalThreads) void balance_kernel(BalanceArgs a) {
   constexpr int kRows = kBalThreads / LANES, kE = 8 * LANES;
   __shared__ float s_p[kBalThreads / 64][kE + 1];
   __shared__ int s_n[kE + 1];
-  const int t = threadIdx.x, lane = t & 63, wave = t / 64, c = 8 * (t % LANES);
+  const int t = threadIdx.x, lane = t & 63, wave = t / 64;
+  const LaneCols<LANES, DT == EXMOE_DTYPE_FP32> cols(t % LANES);
   for (int e = t; e <= kE; e += kBalThreads) s_n[e] = 0;
   __syncthreads();
   f32x8 sum = {0, 0, 0, 0, 0, 0, 0, 0};
@@ -110,12 +158,12 @@ __global__ __launch_bounds__(kBalThreads) void balance_kernel(BalanceArgs a) {
     if (!live) continue;     // (the lanes of a row together)
     f32x8 p;
     float lse;
-    if (row_softmax<LANES>(load_logits<DT>(a, row, c), p, lse)) {
+    if (row_softmax<LANES>(cols.template load<DT>(a.l, (size_t)row * a.ldl, a.E), p, lse)) {
 #pragma unroll
       for (int i = 0; i < 8; i++) sum[i] += p[i];
-      if (c == 0) z += lse * lse;
+      if (t % LANES == 0) z += lse * lse;
     }
-    if (c == 0) n++;
+    if (t % LANES == 0) n++;
     for (int j = t % LANES; j < a.k; j += LANES) {
       const int e = a.ids[(size_t)row * a.k + j];
       if ((unsigned)e < (unsigned)a.E) atomicAdd(&s_n[e], 1);   // (whole numbers: any order)
@@ -130,7 +178,7 @@ __global__ __launch_bounds__(kBalThreads) void balance_kernel(BalanceArgs a) {
   z = wave_sum(z);
   if (lane < LANES) {
 #pragma unroll
-    for (int i = 0; i < 8; i++) s_p[wave][c + i] = sum[i];
+    for (int i = 0; i < 8; i++) s_p[wave][cols.at(i)] = sum[i];
   }
   if (lane == 0) s_p[wave][kE] = z;
   if (n) atomicAdd(&s_n[kE], n);
@@ -145,35 +193,49 @@ __global__ __launch_bounds__(kBalThreads) void balance_kernel(BalanceArgs a) {
   }
 }
 
-// The sums over the workgroups, and the losses.
+// The sums over the workgroups, and the losses: wave w adds those of workgroups w, w + 16, .. (64
+// experts at a time, all loads at once), then the waves' sums in wave order.
 __global__ __launch_bounds__(1024) void balance_join_kernel(BalanceArgs a, int blocks) {
-  __shared__ double s_p[kMaxExperts + 1];
-  __shared__ int s_n[kMaxExperts + 1];
+  constexpr int kCols = (kMaxExperts + 64) / 64 * 64;
+  __shared__ double s_p[16][64];
+  __shared__ int s_n[16][64];
+  __shared__ double s_sum[kCols];
+  __shared__ int s_cnt[kCols];
   const int wave = threadIdx.x / 64, lane = threadIdx.x & 63;
-  for (int e = wave; e <= a.E; e += 16) {
+  for (int e0 = 0; e0 <= a.E; e0 += 64) {
+    const int e = e0 + lane;
     double v = 0.;
     int n = 0;
-    for (int b = lane; b < blocks; b += 64) {
-      v += a.part[(size_t)b * (a.E + 1) + e];
-      n += a.part_n[(size_t)b * (a.E + 1) + e];
+    if (e <= a.E) {
+#pragma unroll 8
+      for (int b = wave; b < blocks; b += 16) {
+        v += a.part[(size_t)b * (a.E + 1) + e];
+        n += a.part_n[(size_t)b * (a.E + 1) + e];
+      }
     }
-    v = wave_sum(v);
-    for (int m = 32; m >= 1; m >>= 1) n += __shfl_xor(n, m, 64);
-    if (lane == 0) {
-      s_p[e] = v;
-      s_n[e] = n;
-      a.counts[e] = n;
+    s_p[wave][lane] = v;
+    s_n[wave][lane] = n;
+    __syncthreads();
+    if (wave == 0) {
+#pragma unroll
+      for (int w = 1; w < 16; w++) {
+        v += s_p[w][lane];
+        n += s_n[w][lane];
+      }
+      s_sum[e] = v;
+      s_cnt[e] = n;
+      if (e <= a.E) a.counts[e] = n;
     }
+    __syncthreads();
   }
-  __syncthreads();
   if (wave == 0) {
     double v = 0.;
-    for (int e = lane; e < a.E; e += 64) v += s_p[e] * (double)s_n[e];
+    for (int e = lane; e < a.E; e += 64) v += s_sum[e] * (double)s_cnt[e];
     v = wave_sum(v);
-    const double M = s_n[a.E];
+    const double M = s_cnt[a.E];
     if (lane == 0) {
       a.losses[0] = M > 0. ? (float)(v * a.E / (M * M * a.k)) : 0.f;
-      a.losses[1] = M > 0. ? (float)(s_p[a.E] / M) : 0.f;
+      a.losses[1] = M > 0. ? (float)(s_sum[a.E] / M) : 0.f;
     }
   }
 }
@@ -181,32 +243,42 @@ __global__ __launch_bounds__(1024) void balance_join_kernel(BalanceArgs a, int b
 template <int DT, int LANES, bool OUT_F32>
 __global__ __launch_bounds__(kBalThreads) void balance_bwd_kernel(BalanceArgs a) {
   constexpr int OT = OUT_F32 ? (int)EXMOE_DTYPE_FP32 : DT;
-  const int t = threadIdx.x, c = 8 * (t % LANES);
-  const size_t i0 = ((size_t)blockIdx.x * kBalThreads + t) / LANES;
-  if (i0 >= (size_t)a.T) return;
-  const int row = (int)i0;
+  constexpr int kRows = kBalThreads / LANES;   // of a workgroup at a time
+  const int t = threadIdx.x;
+  const LaneCols<LANES, OUT_F32 || DT == EXMOE_DTYPE_FP32> cols(t % LANES);
   const int M = a.counts_in[a.E];
-  f32x8 d = {0, 0, 0, 0, 0, 0, 0, 0};
-  const bool live = M > 0 && (!a.mask || a.mask[row]);
-  if (live) {
-    f32x8 p;
-    float lse;
-    if (row_softmax<LANES>(load_logits<DT>(a, row, c), p, lse)) {
-      const float ga = a.grad[0] * (float)a.E, gz = 2.f * a.grad[1] * lse, per = 1.f / ((float)M * (float)a.k);
-      f32x8 f;
-      float dot = 0.f;
+  const float ga = a.grad[0] * (float)a.E, gz = 2.f * a.grad[1], per = M > 0 ? 1.f / ((float)M * (float)a.k) : 0.f,
+              m = M > 0 ? 1.f / (float)M : 0.f;
+  f32x8 f;
 #pragma unroll
-      for (int i = 0; i < 8; i++) {
-        f[i] = c + i < a.E ? (float)a.counts_in[c + i] * per : 0.f;
-        dot += f[i] * p[i];
-      }
-      dot = lanes_sum<LANES>(dot);
-      const float m = 1.f / (float)M;
+  for (int i = 0; i < 8; i++) f[i] = cols.at(i) < a.E ? (float)a.counts_in[cols.at(i)] * per : 0.f;
+  const size_t first = (size_t)blockIdx.x * kRows * kBwdRows + t / LANES;
+  f32x8 l[kBwdRows];
+  bool live[kBwdRows];
 #pragma unroll
-      for (int i = 0; i < 8; i++) d[i] = p[i] * (ga * (f[i] - dot) + gz) * m;
-    }
+  for (int u = 0; u < kBwdRows; u++) {
+    const size_t row = first + u * kRows;
+    live[u] = M > 0 && row < (size_t)a.T && (!a.mask || a.mask[row]);
+    if (live[u]) l[u] = cols.template load<DT>(a.l, row * a.ldl, a.E);
   }
-  if (a.E > c) store_upto8<OT>(a.dl, (size_t)row * a.lddl + c, a.E - c, d);
+#pragma unroll
+  for (int u = 0; u < kBwdRows; u++) {
+    const size_t row = first + u * kRows;
+    f32x8 d = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (live[u]) {           // (the lanes of a row together)
+      f32x8 p;
+      float lse;
+      if (row_softmax<LANES>(l[u], p, lse)) {
+        float dot = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; i++) dot += f[i] * p[i];
+        dot = lanes_sum<LANES>(dot);
+#pragma unroll
+        for (int i = 0; i < 8; i++) d[i] = p[i] * (ga * (f[i] - dot) + gz * lse) * m;
+      }
+    }
+    if (row < (size_t)a.T) cols.template store<OT>(a.dl, row * a.lddl, a.E, d);
+  }
 }
 
 // ------------------------------------------------------------------------------------ host
@@ -224,9 +296,10 @@ static int lanes_of(int E) {
   while (8 * l < E) l *= 2;
   return l;
 }
-// Workgroups of the forward pass: four rows a lane at least, at most 512 of them.
+// Workgroups of the forward pass: a row per LANES lanes, at most 512 of them (two per compute unit; what is
+// left of the rows they take in turn, and the join reads 512 sums).
 static int balance_blocks(int T, int E) {
-  const long long n = ((long long)T * lanes_of(E) + 4 * kBalThreads - 1) / (4 * kBalThreads);
+  const long long n = ((long long)T * lanes_of(E) + kBalThreads - 1) / kBalThreads;
   return n > 512 ? 512 : (n < 1 ? 1 : (int)n);
 }
 
@@ -250,9 +323,15 @@ extern "C" size_t exmoe_balance_loss_workspace_bytes(int T, int E) {
   return (size_t)balance_blocks(T, E) * (E + 1) * 8;
 }
 
-extern "C" int exmoe_balance_loss(const void* logits, size_t ldl, const int32_t* topk_ids, const uint8_t* mask, int T, int E,
-                                  int k, int dtype, float* losses, int32_t* counts, void* workspace, size_t ws_bytes,
-                                  hipStream_t stream) {
+extern "C" int exmoe_balance_loss(const exmoe_balance* call, void* workspace, size_t ws_bytes, hipStream_t stream) {
+  EXMOE_CALL(call);
+  const void* logits = call->logits;
+  const int32_t* topk_ids = call->topk_ids;
+  const uint8_t* mask = call->mask;
+  float* losses = call->losses;
+  int32_t* counts = call->counts;
+  const size_t ldl = call->ldl;
+  const int T = call->T, E = call->E, k = call->k, dtype = call->dtype;
   EXMOE_TRY(check_router(T, E, k, dtype));
   if (!losses || (uintptr_t)losses % 4) return set_error(EXMOE_ERR_INVALID_ARGUMENT, "losses must be non-NULL and 4-byte aligned");
   EXMOE_TRY(check_int32("counts", counts, false));
@@ -288,9 +367,15 @@ extern "C" int exmoe_balance_loss(const void* logits, size_t ldl, const int32_t*
                   "exmoe_balance_loss");
 }
 
-extern "C" int exmoe_balance_loss_backward(const void* logits, size_t ldl, const int32_t* counts, const uint8_t* mask,
-                                           const float* grad_losses, int T, int E, int k, int dtype, int out_dtype,
-                                           void* dlogits, size_t lddl, hipStream_t stream) {
+extern "C" int exmoe_balance_loss_backward(const exmoe_balance* call, hipStream_t stream) {
+  EXMOE_CALL(call);
+  const void* logits = call->logits;
+  const int32_t* counts = call->counts;
+  const uint8_t* mask = call->mask;
+  const float* grad_losses = call->grad_losses;
+  void* dlogits = call->dlogits;
+  const size_t ldl = call->ldl, lddl = call->lddl;
+  const int T = call->T, E = call->E, k = call->k, dtype = call->dtype, out_dtype = call->out_dtype;
   EXMOE_TRY(check_router(T, E, k, dtype));
   if (out_dtype != dtype && out_dtype != EXMOE_DTYPE_FP32)
     return set_error(EXMOE_ERR_INVALID_ARGUMENT, "out_dtype must be dtype or fp32 (got %d)", out_dtype);
@@ -314,7 +399,7 @@ extern "C" int exmoe_balance_loss_backward(const void* logits, size_t ldl, const
   return launched(by_dtype(dtype, [&](auto dt) {
                     return by_lanes(E, [&](auto lanes) {
                       constexpr int DT = decltype(dt)::value, LANES = decltype(lanes)::value;
-                      const unsigned blocks = (unsigned)(((size_t)T * LANES + kBalThreads - 1) / kBalThreads);
+                      const unsigned blocks = (unsigned)(((size_t)T * LANES + kBalThreads * kBwdRows - 1) / (kBalThreads * kBwdRows));
                       ProfScope prof("balance_loss_bwd", stream);
                       if (a.out_f32)
                         EXMOE_LAUNCH(prof, (balance_bwd_kernel<DT, LANES, true>), dim3(blocks), dim3(kBalThreads), 0, stream, a);

@@ -49,3 +49,8 @@ inline int vec_store(const void* p, size_t ld, size_t stride, int out_f32) {
     const int st_ = (call);    \
     if (st_) return st_;       \
   } while (0)
+
+#define EXMOE_CALL(call)                                                                    \
+  do {                                                                                     \
+    if (!(call)) return set_error(EXMOE_ERR_INVALID_ARGUMENT, "call must not be NULL");     \
+  } while (0)

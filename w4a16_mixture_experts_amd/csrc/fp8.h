@@ -34,6 +34,12 @@ struct Elems<EXMOE_DTYPE_FP32> {
     const f32x4_u a = q[0], b = q[1];
     return f32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
   }
+  static __device__ __forceinline__ f32x4 load4(const void* p, size_t off) {
+    return *reinterpret_cast<const f32x4_u*>(static_cast<const float*>(p) + off);
+  }
+  static __device__ __forceinline__ void store4(void* p, size_t off, f32x4 v) {
+    *reinterpret_cast<f32x4_u*>(static_cast<float*>(p) + off) = v;
+  }
   static __device__ __forceinline__ void store8(void* p, size_t off, f32x8 v) {
     f32x4_u* q = reinterpret_cast<f32x4_u*>(static_cast<float*>(p) + off);
     q[0] = f32x4_u{v[0], v[1], v[2], v[3]};
@@ -58,6 +64,14 @@ struct Elems16 {
       v[2 * i + 1] = F::to_f32((uint16_t)(w[i] >> 16));
     }
     return v;
+  }
+  typedef uint32_t u32x2_u __attribute__((ext_vector_type(2), aligned(2)));
+  static __device__ __forceinline__ f32x4 load4(const void* p, size_t off) {
+    const u32x2_u w = *reinterpret_cast<const u32x2_u*>(static_cast<const uint16_t*>(p) + off);
+    return f32x4{F::to_f32((uint16_t)w[0]), F::to_f32((uint16_t)(w[0] >> 16)), F::to_f32((uint16_t)w[1]), F::to_f32((uint16_t)(w[1] >> 16))};
+  }
+  static __device__ __forceinline__ void store4(void* p, size_t off, f32x4 v) {
+    *reinterpret_cast<u32x2_u*>(static_cast<uint16_t*>(p) + off) = u32x2_u{F::pack2(v[0], v[1]), F::pack2(v[2], v[3])};
   }
   static __device__ __forceinline__ void store8(void* p, size_t off, f32x8 v) {
     u32x4_u w;

@@ -43,14 +43,24 @@ struct FragF8 {
 struct FragBF16 {
   bf16x8 v[4];
 };
-__device__ __forceinline__ FragF8 read_frag(FragF8*, const uint16_t* lds, int r0, int lane) {
-  const i32x4 a = __builtin_bit_cast(i32x4, NarrowRows<16, 64>::frag(lds, r0, 0, lane));
-  const i32x4 b = __builtin_bit_cast(i32x4, NarrowRows<16, 64>::frag(lds, r0, 1, lane));
+// Where a lane finds its two chunks of a fragment behind its first row (whose number is a multiple
+// of 16: the swizzle of WideRows is then the lane's own).
+struct FragPlace {
+  uint32_t lo, hi;   // bytes
+  __device__ __forceinline__ explicit FragPlace(int lane, int first_row) {
+    const int row = lane & 15;
+    lo = (first_row + row) * 128 + 16 * ((lane >> 4) ^ (row >> 1));
+    hi = lo ^ 64;
+  }
+};
+__device__ __forceinline__ FragF8 read_frag(FragF8*, const uint16_t* lds, int r0, FragPlace at) {
+  const char* p = reinterpret_cast<const char*>(lds) + 128 * r0;
+  const i32x4 a = *reinterpret_cast<const i32x4*>(p + at.lo), b = *reinterpret_cast<const i32x4*>(p + at.hi);
   return {__builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7)};
 }
-__device__ __forceinline__ FragBF16 read_frag(FragBF16*, const uint16_t* lds, int r0, int lane) {
+__device__ __forceinline__ FragBF16 read_frag(FragBF16*, const uint16_t* lds, int r0, FragPlace at) {
   typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-  const i32x8 f = read_frag((FragF8*)nullptr, lds, r0, lane).v;
+  const i32x8 f = read_frag((FragF8*)nullptr, lds, r0, at).v;
   FragBF16 r;
 #pragma unroll
   for (int i = 0; i < 4; i++) {
@@ -104,13 +114,27 @@ struct TileRows {
   }
 };
 
-// 16 TP WP x 16 TQ WQ outputs per workgroup of WP x WQ waves; 128-deep slices of both operands
-// double-buffered in LDS, one barrier per slice.
+// 16 TP WP x 16 TQ WQ outputs per workgroup of WP x WQ waves; 128-deep slices of both operands and
+// their scales double-buffered in LDS, one barrier per slice. A slice is TP steps of TQ matrix
+// instructions: step i multiplies the wave's columns, held in registers, with row block i, whose
+// fragment was read a step before, and scales the results of the step before into the sums. The
+// slice's one barrier comes before its last step's products: the wave then holds that step's
+// fragments, so every wave is done reading the slice, and the next but one is copied over it while the
+// first fragments of the next are read between those products.
+// Row blocks are dealt to the WP wave rows in turn, and blocks past the tile's rows are skipped.
 template <class ET, class Frag, int TP, int TQ, int WP, int WQ, int OCC>
 __global__ __launch_bounds__(64 * WP * WQ, OCC) void fp8_tile_kernel(Fp8Args a, int q_tiles) {
   constexpr int NW = WP * WQ, BP = 16 * TP * WP, BQ = 16 * TQ * WQ, D = 64;   // (D: pairs of bytes)
   static_assert(BQ % 128 == 0 && 128 % (16 * TQ) == 0, "a wave's columns lie in one block of scales");
+  static_assert(TP % 2 == 0, "steps in pairs");
+  constexpr bool F32 = std::is_same<Frag, FragBF16>::value;
+  constexpr int kMfma = TQ * (F32 ? 4 : 1);   // matrix instructions of a step
+  // (separate arrays: the compiler then sees that reading one does not wait for copies into another)
   __shared__ __attribute__((aligned(16))) uint16_t s_p0[BP * D], s_p1[BP * D], s_q0[BQ * D], s_q1[BQ * D];
+  // scales of the rows, then of the columns' blocks (wave w copies those of rows 64 w.. of the tile, the
+  // next one those of the columns, what is left zeros, so that every wave's copies are alike)
+  constexpr int kScaleCopies = (BP / 64 + NW) / NW;
+  __shared__ float s_s0[64 * NW * kScaleCopies], s_s1[64 * NW * kScaleCopies];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wp = wave / WQ, wq = wave % WQ;
   RowTile r;
@@ -127,58 +151,148 @@ __global__ __launch_bounds__(64 * WP * WQ, OCC) void fp8_tile_kernel(Fp8Args a, 
   const int ncols = min(BQ, a.N - q0);
   op_q.init(make_buf(a.w + (size_t)r.e * a.w_stride + (size_t)q0 * a.ldw, (size_t)(ncols - 1) * a.ldw + a.K), red, wave, lane,
             [&](int i) { return i < ncols ? (uint32_t)((size_t)i * a.ldw) : kNowhere; });
-  uint32_t xs_off[TP];
+  buf_t sc_buf[kScaleCopies];
+  uint32_t sc_off[kScaleCopies];
 #pragma unroll
-  for (int i = 0; i < TP; i++) {
-    const int s = rows.row(a, r, 16 * (i * WP + wp) + (lane & 15), dmul);
-    xs_off[i] = s < 0 ? kNowhere : (uint32_t)((size_t)s * a.ldxs * 4);
+  for (int c = 0; c < kScaleCopies; c++) {
+    const int part = c * NW + wave;
+    sc_buf[c] = rows.xs;
+    sc_off[c] = kNowhere;
+    if (part < BP / 64) {
+      const int s = rows.row(a, r, 64 * part + lane, dmul);
+      if (s >= 0) sc_off[c] = (uint32_t)((size_t)s * a.ldxs * 4);
+    } else if (part == BP / 64) {
+      const int nb = (ncols + 127) / 128;
+      sc_buf[c] = make_buf(a.ws + (size_t)r.e * a.ws_stride + (size_t)(q0 / 128) * a.ldws, 4 * ((size_t)(nb - 1) * a.ldws + (a.K + 127) / 128));
+      if (lane < nb) sc_off[c] = (uint32_t)((size_t)lane * a.ldws * 4);
+    }
   }
-  const int nb = min((q0 + 16 * TQ * wq) / 128, (a.N - 1) / 128);   // (columns past N: any scale)
-  const float* ws = a.ws + (size_t)r.e * a.ws_stride + (size_t)nb * a.ldws;
+  const int steps = (a.K + 127) / 128;
+  auto stage_scales = [&](int s, float* ls) __attribute__((always_inline)) {
+#pragma unroll
+    for (int c = 0; c < kScaleCopies; c++)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(sc_buf[c], (__attribute__((address_space(3))) void*)(ls + 64 * (c * NW + wave)), 4,
+                                               s < steps ? sc_off[c] : kNowhere, s < steps ? 4 * s : 0, 0, 0);
+  };
 
   f32x4 acc[TQ][TP];
 #pragma unroll
   for (int j = 0; j < TQ; j++)
 #pragma unroll
     for (int i = 0; i < TP; i++) acc[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const int steps = (a.K + 127) / 128;
-  auto slice = [&](int s, const uint16_t* cp, const uint16_t* cq, uint16_t* np, uint16_t* nq) __attribute__((always_inline)) {
-    float sc[TP];
-    const float w = ws[s];
+  auto block_p = [&](int i) __attribute__((always_inline)) { return 16 * (i * WP + wp); };   // first row of row block i
+  int nblk = 0;                                                                              // of them hold rows
 #pragma unroll
-    for (int i = 0; i < TP; i++) sc[i] = buf_load_f32(rows.xs, xs_off[i], 4 * s) * w;
-    wait_vm<0>();
-    wait_lds();
-    block_barrier();
-    if (s + 1 < steps) {
-      op_p.stage(np, (s + 1) * D);
-      op_q.stage(nq, (s + 1) * D);
+  for (int i = 0; i < TP; i++) nblk += r.p0 + block_p(i) < r.p1 ? 1 : 0;
+  nblk = __builtin_amdgcn_readfirstlane(nblk);
+
+  const FragPlace at_p(lane, 16 * wp), at_q(lane, 16 * TQ * wq);
+  Frag fq[TQ], fp[2];
+  float sx[2], sw = 0.f;         // scales of the row block in fp[.], and of the columns
+  f32x4 part[2][TQ];             // products of a step, scaled a step later
+  float part_s[2];
+  // products of row block i (in fp[i & 1]); those of the step before, of row block i - 1, go into the sums
+  auto multiply = [&](auto full, auto i_c) __attribute__((always_inline)) {
+    constexpr int i = decltype(i_c)::value, set = i & 1, before = (i + TP - 1) % TP;
+    if (decltype(full)::value || i < nblk) {
+      part_s[set] = sx[set] * sw;
+#pragma unroll
+      for (int j = 0; j < TQ; j++) part[set][j] = block_product(fq[j], fp[set]);
     }
-    Frag fq[TQ];
+    if (decltype(full)::value || before < nblk) {
 #pragma unroll
-    for (int j = 0; j < TQ; j++) fq[j] = read_frag((Frag*)nullptr, cq, (wq * TQ + j) * 16, lane);
+      for (int j = 0; j < TQ; j++)
 #pragma unroll
-    for (int i = 0; i < TP; i++) {
-      const Frag fp = read_frag((Frag*)nullptr, cp, 16 * (i * WP + wp), lane);
+        for (int v = 0; v < 4; v++) acc[j][before][v] += part[set ^ 1][j][v] * part_s[set ^ 1];
+      // (the sums stay here: moved down past a branch, they would keep the products of a whole slice)
 #pragma unroll
-      for (int j = 0; j < TQ; j++) {
-        const f32x4 c = block_product(fq[j], fp);
-#pragma unroll
-        for (int v = 0; v < 4; v++) acc[j][i][v] += c[v] * sc[i];
-      }
+      for (int j = 0; j < TQ; j++) asm volatile("" : "+v"(acc[j][before]));
     }
   };
-  op_p.stage(s_p0, 0);
+  auto read_p = [&](auto i_c, const uint16_t* lp, const float* ls) __attribute__((always_inline)) {
+    constexpr int i = decltype(i_c)::value;
+    fp[i & 1] = read_frag((Frag*)nullptr, lp, 16 * i * WP, at_p);
+    sx[i & 1] = ls[block_p(i) + (lane & 15)];
+  };
+  // a step by itself, its reads first, the copies and multiply-adds spread between its products
+  auto interleave = [&](auto full, auto reads_c, auto copies_c) __attribute__((always_inline)) {
+    if constexpr (decltype(full)::value) {
+      constexpr int reads = decltype(reads_c)::value, copies = decltype(copies_c)::value;
+#pragma unroll
+      for (int j = 0; j < kMfma; j++) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        const int nr = reads <= 3 ? (j == 0 ? reads : 0) : (j + 1) * reads / kMfma - j * reads / kMfma;
+        const int nc = (j + 1) * copies / kMfma - j * copies / kMfma;
+        for (int e = 0; e < nr; e++) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        for (int e = 0; e < nc; e++) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, 4 * TQ / kMfma, 0);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // the last step of the slice before, while the first fragments of slice s are read and slice s + 1
+  // (or zeros past the last one) is copied; then all but the last step of slice s
+  auto slice = [&](auto full, int s, uint16_t* cp, uint16_t* cq, float* cs, uint16_t* np, uint16_t* nq, float* ns)
+      __attribute__((always_inline)) {
+    wait_lds();      // this wave holds its last fragments of slice s - 1
+    wait_vm<0>();    // its copies of slice s have landed
+    block_barrier();
+    multiply(full, std::integral_constant<int, TP - 1>{});
+    sw = cs[BP + wq * 16 * TQ / 128];
+    read_p(std::integral_constant<int, 0>{}, cp, cs);
+#pragma unroll
+    for (int j = 0; j < TQ; j++) fq[j] = read_frag((Frag*)nullptr, cq, 16 * j, at_q);
+    interleave(full, std::integral_constant<int, 2 * TQ + 4>{}, std::integral_constant<int, 0>{});
+    auto step = [&](auto i) __attribute__((always_inline)) {
+      if constexpr (decltype(i)::value + 1 < TP) {
+        read_p(std::integral_constant<int, decltype(i)::value + 1>{}, cp, cs);
+        multiply(full, i);
+        constexpr int copies = decltype(i)::value == 0 ? decltype(op_q)::kSlots : decltype(i)::value == 1 ? decltype(op_p)::kSlots : decltype(i)::value == 2 ? kScaleCopies : 0;
+        if constexpr (decltype(i)::value == 0) op_q.stage(nq, (s + 1) * D);
+        if constexpr (decltype(i)::value == 1) op_p.stage(np, (s + 1) * D);
+        if constexpr (decltype(i)::value == 2) stage_scales(s + 1, ns);
+        interleave(full, std::integral_constant<int, 3>{}, std::integral_constant<int, copies>{});
+      }
+    };
+    step(std::integral_constant<int, 0>{});
+    step(std::integral_constant<int, 1>{});
+    step(std::integral_constant<int, 2>{});
+    step(std::integral_constant<int, 3>{});
+    step(std::integral_constant<int, 4>{});
+    step(std::integral_constant<int, 5>{});
+    step(std::integral_constant<int, 6>{});
+  };
+  auto loop = [&](auto full) __attribute__((always_inline)) {
+    for (int s = 0; s < steps; s += 2) {
+      slice(full, s, s_p0, s_q0, s_s0, s_p1, s_q1, s_s1);
+      if (s + 1 < steps) slice(full, s + 1, s_p1, s_q1, s_s1, s_p0, s_q0, s_s0);
+    }
+    multiply(full, std::integral_constant<int, TP - 1>{});
+#pragma unroll
+    for (int j = 0; j < TQ; j++)
+#pragma unroll
+      for (int v = 0; v < 4; v++) acc[j][TP - 1][v] += part[(TP - 1) & 1][j][v] * part_s[(TP - 1) & 1];
+  };
   op_q.stage(s_q0, 0);
-  for (int s = 0; s < steps; s += 2) {
-    slice(s, s_p0, s_q0, s_p1, s_q1);
-    if (s + 1 < steps) slice(s + 1, s_p1, s_q1, s_p0, s_q0);
+  op_p.stage(s_p0, 0);
+  stage_scales(0, s_s0);
+#pragma unroll
+  for (int b = 0; b < 2; b++) {
+    fp[b] = Frag{};
+    sx[b] = part_s[b] = 0.f;
+#pragma unroll
+    for (int j = 0; j < TQ; j++) part[b][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
+#pragma unroll
+  for (int j = 0; j < TQ; j++) fq[j] = Frag{};
+  if (nblk == TP) loop(std::true_type{});
+  else loop(std::false_type{});
+  wait_vm<0>();    // no copy is left behind the workgroup's end
+
   // lane l holds row l % 16 and columns 4 (l / 16) + 0..3 of each 16 x 16 block
-  constexpr bool F32 = std::is_same<Frag, FragBF16>::value;
 #pragma unroll
   for (int i = 0; i < TP; i++) {
-    const int p = r.p0 + 16 * (i * WP + wp) + (lane & 15);
+    const int p = r.p0 + block_p(i) + (lane & 15);
     if (p >= r.p1) continue;
     const size_t row = (size_t)(r.seg0 + p) * a.ldo;
 #pragma unroll
@@ -189,15 +303,137 @@ __global__ __launch_bounds__(64 * WP * WQ, OCC) void fp8_tile_kernel(Fp8Args a, 
   }
 }
 
+// Few rows per expert, or few tiles: 16 TP rows x 16 TQ columns per workgroup, whose waves split the
+// blocks of 128 positions (wave w: blocks w, w + NW, ..). Each wave copies its own slices of both operands
+// into its own part of LDS, two in flight, without a barrier; the sums are added in wave order.
+template <class ET, class Frag, int TP, int TQ, int NW>
+__global__ __launch_bounds__(64 * NW) void fp8_narrow_kernel(Fp8Args a, int q_tiles) {
+  constexpr int D = 64, kPart = 16 * (TP + TQ) * D;
+  using OpX = NarrowRows<16 * TP, D>;
+  using OpW = NarrowRows<16 * TQ, D>;
+  constexpr bool F32 = std::is_same<Frag, FragBF16>::value;
+  __shared__ __attribute__((aligned(16))) uint16_t s_a[2][NW][kPart];
+  static_assert(sizeof(f32x4) * TP * TQ * 64 * NW <= sizeof(s_a), "the sums fit into the slices' part");
+  static_assert(128 % (16 * TQ) == 0, "the columns lie in one block of scales");
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  RowTile r;
+  if (!resolve_rows<16 * TP, 16, true>(a.offsets, a.rows, a.E, q_tiles, blockIdx.x, r)) return;
+  const int n0 = 16 * TQ * r.qt, ncols = min(16 * TQ, a.N - n0), red = a.K / 2, steps = (a.K + 127) / 128;
+  const uint32_t dmul = 0xFFFFFFFFu / (uint32_t)a.row_div;
+  const TileRows rows(a, r);
+  OpX op_x;
+  OpW op_w;
+  op_w.init(make_buf(a.w + (size_t)r.e * a.w_stride + (size_t)n0 * a.ldw, (size_t)(ncols - 1) * a.ldw + a.K), red, lane,
+            [&](int i) { return i < ncols ? (uint32_t)((size_t)i * a.ldw) : kNowhere; });
+  op_x.init(rows.x, red, lane, [&](int i) {
+    const int s = rows.row(a, r, i, dmul);
+    return s < 0 ? kNowhere : (uint32_t)((size_t)s * a.ldx);
+  });
+  uint32_t xs_off[TP];
+#pragma unroll
+  for (int i = 0; i < TP; i++) {
+    const int s = rows.row(a, r, 16 * i + (lane & 15), dmul);
+    xs_off[i] = s < 0 ? kNowhere : (uint32_t)((size_t)s * a.ldxs * 4);
+  }
+  const buf_t ws = make_buf(a.ws + (size_t)r.e * a.ws_stride + (size_t)(n0 / 128) * a.ldws, 4 * (size_t)steps);
+
+  f32x4 acc[TQ][TP];
+#pragma unroll
+  for (int j = 0; j < TQ; j++)
+#pragma unroll
+    for (int i = 0; i < TP; i++) acc[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const FragPlace at(lane, 0);
+  constexpr int kLoads = OpX::kSlots + OpW::kSlots + TP + 1;
+  float sx[2][TP], sw[2];
+  auto issue = [&](auto set, int n, uint16_t* lds) __attribute__((always_inline)) {
+    const int b = n * NW + wave;
+    op_w.stage(lds, b * D);
+    op_x.stage(lds + OpW::kElems, b * D);
+    const uint32_t off = b < steps ? 4 * (uint32_t)b : 0;
+    sw[set] = buf_load_f32(ws, b < steps ? 0 : kNowhere, off);
+#pragma unroll
+    for (int i = 0; i < TP; i++) sx[set][i] = buf_load_f32(rows.xs, b < steps ? xs_off[i] : kNowhere, off);
+  };
+  auto compute = [&](auto set, const uint16_t* lds) __attribute__((always_inline)) {
+    wait_vm<kLoads>();
+    asm volatile("" ::: "memory");
+    Frag fw[TQ], fx[TP];
+#pragma unroll
+    for (int j = 0; j < TQ; j++) fw[j] = read_frag((Frag*)nullptr, lds, 16 * j, at);
+#pragma unroll
+    for (int i = 0; i < TP; i++) fx[i] = read_frag((Frag*)nullptr, lds + OpW::kElems, 16 * i, at);
+#pragma unroll
+    for (int i = 0; i < TP; i++) {
+      const float scale = sx[set][i] * sw[set];
+#pragma unroll
+      for (int j = 0; j < TQ; j++) {
+        const f32x4 c = block_product(fw[j], fx[i]);
+#pragma unroll
+        for (int v = 0; v < 4; v++) acc[j][i][v] += c[v] * scale;
+      }
+    }
+    wait_lds();   // read, before the next copies into this part
+    asm volatile("" ::: "memory");
+  };
+  using Zero = std::integral_constant<int, 0>;
+  using One = std::integral_constant<int, 1>;
+  const int n = (steps + NW - 1) / NW;
+  issue(Zero{}, 0, s_a[0][wave]);
+  issue(One{}, 1, s_a[1][wave]);
+  for (int t = 0; t < n; t += 2) {
+    compute(Zero{}, s_a[0][wave]);
+    issue(Zero{}, t + 2, s_a[0][wave]);
+    compute(One{}, s_a[1][wave]);
+    issue(One{}, t + 3, s_a[1][wave]);
+  }
+  wait_vm<0>();   // no copy is left behind
+  __syncthreads();
+  f32x4 v[TQ];
+  skinny_reduce<TP, TQ, NW>(reinterpret_cast<f32x4(*)[TQ * TP][64]>(&s_a[0][0][0]), acc, wave, lane, v);
+  const int p = r.p0 + 16 * wave + (lane & 15);
+  if (wave >= TP || p >= r.p1) return;
+#pragma unroll
+  for (int j = 0; j < TQ; j++) {
+    const int q = n0 + 16 * j + 4 * (lane >> 4);
+    if (q < a.N) store4<ET>(a.out, (size_t)(r.seg0 + p) * a.ldo + q, F32, a.vec, a.N - q, v[j]);
+  }
+}
+
 // ------------------------------------------------------------------------------------ host
-template <class ET, class Frag>
-static hipError_t launch_fp8(const Fp8Args& a, hipStream_t s) {
-  constexpr int BP = 128, BQ = 128;
+template <class ET, class Frag, int TP, int TQ, int WP, int WQ, int OCC>
+static hipError_t launch_tile(const Fp8Args& a, hipStream_t s) {
+  constexpr int BP = 16 * TP * WP, BQ = 16 * TQ * WQ;
   const int qt = ceil_div(a.N, BQ);
   ProfScope prof("grouped_mm_fp8", s);
-  EXMOE_LAUNCH(prof, (fp8_tile_kernel<ET, Frag, 4, 4, 2, 2, 2>), dim3((unsigned)(row_tiles(a.rows, a.E, BP) * qt)), dim3(256), 0, s,
-               a, qt);
+  EXMOE_LAUNCH(prof, (fp8_tile_kernel<ET, Frag, TP, TQ, WP, WQ, OCC>), dim3((unsigned)(row_tiles(a.rows, a.E, BP) * qt)),
+               dim3(64 * WP * WQ), 0, s, a, qt);
   return hipGetLastError();
+}
+
+template <class ET, class Frag, int TP, int TQ, int NW>
+static hipError_t launch_narrow(const Fp8Args& a, hipStream_t s) {
+  const int qt = ceil_div(a.N, 16 * TQ);
+  ProfScope prof("grouped_mm_fp8", s);
+  EXMOE_LAUNCH(prof, (fp8_narrow_kernel<ET, Frag, TP, TQ, NW>), dim3((unsigned)(row_tiles(a.rows, a.E, 16 * TP) * qt)), dim3(64 * NW),
+               0, s, a, qt);
+  return hipGetLastError();
+}
+
+// Rows per expert up to which 16 x 32 blocks on two waves, bound by reading W, run instead of 128 x 128 tiles.
+constexpr int kNarrowRows = 12;
+// Fewer 128 x 128 tiles than half the CUs: 16 x 64 blocks whose waves split the reduction.
+static bool few_tiles(int rows, int Q, int E) {
+  return (rows / 128 + (long long)(E < rows ? E : rows)) * ceil_div(Q, 128) < 128;
+}
+
+template <class ET, class Frag>
+static hipError_t launch_fp8(const Fp8Args& a, hipStream_t s) {
+  if (a.rows <= kNarrowRows * (long long)a.E) return launch_narrow<ET, Frag, 1, 2, 2>(a, s);
+  if (few_tiles(a.rows, a.N, a.E)) return launch_narrow<ET, Frag, 1, 4, 4>(a, s);
+  if constexpr (std::is_same<Frag, FragF8>::value) {
+    if (a.rows / a.E >= 160 && (long long)(a.rows / 256) * ceil_div(a.N, 256) >= 256) return launch_tile<ET, Frag, 8, 4, 2, 4, 2>(a, s);
+  }
+  return launch_tile<ET, Frag, 4, 4, 2, 2, 2>(a, s);
 }
 
 }  // namespace exmoe
@@ -212,10 +448,10 @@ static int check_fp8(const char* name, const void* p, size_t ld, int K) {
   return EXMOE_OK;
 }
 
-extern "C" int exmoe_grouped_mm_fp8(const uint8_t* x, size_t ldx, const float* x_scale, size_t ldxs, int x_rows,
-                                    const int32_t* row_index, int row_div, const int32_t* expert_offsets, const uint8_t* w,
-                                    size_t ldw, size_t w_stride, const float* w_scale, size_t ldws, size_t ws_stride, int rows,
-                                    int N, int K, int E, int out_dtype, void* y, size_t ldy, hipStream_t stream) {
+extern "C" int exmoe_grouped_mm_fp8(const exmoe_grouped_fp8* call, hipStream_t stream) {
+  EXMOE_CALL(call);
+  const auto& [x, ldx, x_scale, ldxs, row_index, expert_offsets, w, ldw, w_stride, w_scale, ldws, ws_stride, y, ldy, x_rows, row_div,
+               rows, N, K, E, out_dtype] = *call;
   if (rows < 0 || rows > (1 << 30)) return set_error(EXMOE_ERR_INVALID_ARGUMENT, "rows must be in [0, 2^30] (got %d)", rows);
   if (N < 1 || K < 1) return set_error(EXMOE_ERR_INVALID_ARGUMENT, "N and K must be positive (got %d, %d)", N, K);
   if (K % 16) return set_error(EXMOE_ERR_INVALID_ARGUMENT, "K must be a multiple of 16 (got %d)", K);

@@ -118,12 +118,15 @@ static hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
     return hipGetLastError();
   };
   using std::integral_constant;
+  // As many waves as give each lane one chunk: a short chain of loads per row, also where rows are many (bf16
+  // with residual, both outputs; one wave per row / four: 1 x 2048 5.0 / 2.7 us, 1024 x 2048 7.0 / 4.9, 4096 x
+  // 2048 14.8 / 13.6; four waves / eight: 4096 x 4096 24.8 / 24.0 us, 6.3 TB/s).
   if (a.H <= 512) return go(integral_constant<int, 1>{}, integral_constant<int, 1>{});
-  if (a.H <= 1024) return go(integral_constant<int, 1>{}, integral_constant<int, 2>{});
-  if (a.H <= 2048) return go(integral_constant<int, 1>{}, integral_constant<int, 4>{});
-  if (a.H <= 4096) return go(integral_constant<int, 4>{}, integral_constant<int, 2>{});
-  if (a.H <= 8192) return go(integral_constant<int, 4>{}, integral_constant<int, 4>{});
-  return go(integral_constant<int, 8>{}, integral_constant<int, 4>{});
+  if (a.H <= 1024) return go(integral_constant<int, 2>{}, integral_constant<int, 1>{});
+  if (a.H <= 2048) return go(integral_constant<int, 4>{}, integral_constant<int, 1>{});
+  if (a.H <= 4096) return go(integral_constant<int, 8>{}, integral_constant<int, 1>{});
+  if (a.H <= 8192) return go(integral_constant<int, 16>{}, integral_constant<int, 1>{});
+  return go(integral_constant<int, 16>{}, integral_constant<int, 2>{});
 }
 
 }  // namespace exmoe
@@ -131,11 +134,11 @@ static hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
 using namespace exmoe;
 
 // ------------------------------------------------------------------------------------ C ABI
-extern "C" int exmoe_rms_norm(const void* x, size_t ldx, const void* w, int w_dtype, const void* residual, size_t ldr,
-                              int res_dtype, void* residual_out, size_t ldro, float eps, int T, int H, int dtype, void* y,
-                              size_t ldy, uint8_t* q, size_t ldq, float* scale, size_t lds, hipStream_t stream) {
+extern "C" int exmoe_rms_norm(const exmoe_norm* call, hipStream_t stream) {
+  EXMOE_CALL(call);
+  const auto& [x, ldx, w, residual, ldr, residual_out, ldro, y, ldy, q, ldq, scale, lds, eps, T, H, dtype, w_dtype, res_dtype] = *call;
   if (T < 0) return set_error(EXMOE_ERR_INVALID_ARGUMENT, "T must be >= 0 (got %d)", T);
-  if (T >= 1 << 23) return set_error(EXMOE_ERR_UNSUPPORTED, "T must be < 2^23 (got %d)", T);
+  if (T >= 1 << 22) return set_error(EXMOE_ERR_UNSUPPORTED, "T must be < 2^22 (got %d)", T);
   if (H < 1) return set_error(EXMOE_ERR_INVALID_ARGUMENT, "H must be positive (got %d)", H);
   if (H > kMaxDim) return set_error(EXMOE_ERR_UNSUPPORTED, "H must be <= %d (got %d)", kMaxDim, H);
   if (dtype < EXMOE_DTYPE_BF16 || dtype > EXMOE_DTYPE_FP32)

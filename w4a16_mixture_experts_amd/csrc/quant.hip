@@ -117,9 +117,10 @@ static int check_input(int n, int dtype) {
   return EXMOE_OK;
 }
 
-static int quant_rows(const char* what, const void* x, size_t ldx, const float* weights, int n_weights,
-                      const int32_t* row_index, int rows, int n, int dtype, bool gated, uint8_t* q, size_t ldq, float* scale,
-                      size_t lds, hipStream_t stream) {
+static int quant_rows(const char* what, const exmoe_fp8_rows* call, bool gated, hipStream_t stream) {
+  EXMOE_CALL(call);
+  const exmoe_fp8_rows& c = *call;
+  const int rows = c.rows, n = c.n, dtype = c.dtype;
   EXMOE_TRY(check_input(n, dtype));
   if (rows < 0 || rows > (1 << 30)) return set_error(EXMOE_ERR_INVALID_ARGUMENT, "rows must be in [0, 2^30] (got %d)", rows);
   const int groups = ceil_div(n, 128);
@@ -127,62 +128,59 @@ static int quant_rows(const char* what, const void* x, size_t ldx, const float* 
     return set_error(EXMOE_ERR_UNSUPPORTED, "%s: more groups than one launch holds", what);
   if (rows == 0) return EXMOE_OK;
   const int cols = gated ? 2 * n : n, b = dtype_bytes(dtype);
-  EXMOE_TRY(check_matrix("x", x, ldx, cols, b));
-  EXMOE_TRY(check_matrix("q", q, ldq, n, 1));
-  EXMOE_TRY(check_matrix("scale", scale, lds, groups, 4));
-  EXMOE_TRY(check_int32("weights", weights, true));
-  EXMOE_TRY(check_int32("row_index", row_index, true));
-  if (!weights && row_index) return set_error(EXMOE_ERR_INVALID_ARGUMENT, "row_index without weights");
-  if (weights && n_weights < (row_index ? 1 : rows))
-    return set_error(EXMOE_ERR_INVALID_ARGUMENT, "%d weights, at least %d needed", n_weights, row_index ? 1 : rows);
-  const MemRows mx = mem_matrix("x", x, rows, ldx, cols, b), mq = mem_matrix("q", q, rows, ldq, n, 1),
-                ms = mem_matrix("scale", scale, rows, lds, groups, 4),
-                mw = mem_flat("weights", weights, (size_t)(row_index ? n_weights : rows) * 4),
-                mi = mem_flat("row_index", row_index, (size_t)rows * 4);
+  EXMOE_TRY(check_matrix("x", c.x, c.ldx, cols, b));
+  EXMOE_TRY(check_matrix("q", c.q, c.ldq, n, 1));
+  EXMOE_TRY(check_matrix("scale", c.scale, c.lds, groups, 4));
+  EXMOE_TRY(check_int32("weights", c.weights, true));
+  EXMOE_TRY(check_int32("row_index", c.row_index, true));
+  if (!c.weights && c.row_index) return set_error(EXMOE_ERR_INVALID_ARGUMENT, "row_index without weights");
+  if (c.weights && c.n_weights < (c.row_index ? 1 : rows))
+    return set_error(EXMOE_ERR_INVALID_ARGUMENT, "%d weights, at least %d needed", c.n_weights, c.row_index ? 1 : rows);
+  const MemRows mx = mem_matrix("x", c.x, rows, c.ldx, cols, b), mq = mem_matrix("q", c.q, rows, c.ldq, n, 1),
+                ms = mem_matrix("scale", c.scale, rows, c.lds, groups, 4),
+                mw = mem_flat("weights", c.weights, (size_t)(c.row_index ? c.n_weights : rows) * 4),
+                mi = mem_flat("row_index", c.row_index, (size_t)rows * 4);
   EXMOE_TRY(check_apart(mq, {mx, mw, mi, ms}));
   EXMOE_TRY(check_apart(ms, {mx, mw, mi}));
   QuantRows a{};
-  a.x = x; a.ldx = ldx; a.rows = rows; a.n = n; a.groups = groups; a.div_mul = 0xFFFFFFFFu / (uint32_t)groups;
-  a.weights = weights; a.row_index = row_index; a.n_weights = row_index ? n_weights : rows; a.q = q; a.ldq = ldq;
-  a.scale = scale; a.lds = lds;
+  a.x = c.x; a.ldx = c.ldx; a.rows = rows; a.n = n; a.groups = groups; a.div_mul = 0xFFFFFFFFu / (uint32_t)groups;
+  a.weights = c.weights; a.row_index = c.row_index; a.n_weights = c.row_index ? c.n_weights : rows; a.q = c.q; a.ldq = c.ldq;
+  a.scale = c.scale; a.lds = c.lds;
   return launched(launch_rows(a, dtype, gated, stream), what);
 }
 
-extern "C" int exmoe_quantize_fp8(const void* x, size_t ldx, int rows, int K, int dtype, uint8_t* q, size_t ldq, float* scale,
-                                  size_t lds, hipStream_t stream) {
-  return quant_rows("exmoe_quantize_fp8", x, ldx, nullptr, 0, nullptr, rows, K, dtype, false, q, ldq, scale, lds, stream);
+extern "C" int exmoe_quantize_fp8(const exmoe_fp8_rows* call, hipStream_t stream) {
+  return quant_rows("exmoe_quantize_fp8", call, false, stream);
 }
 
-extern "C" int exmoe_swiglu_fp8(const void* gate_up, size_t ldx, const float* weights, int n_weights, const int32_t* row_index,
-                                int rows, int I, int dtype, uint8_t* q, size_t ldq, float* scale, size_t lds,
-                                hipStream_t stream) {
-  return quant_rows("exmoe_swiglu_fp8", gate_up, ldx, weights, n_weights, row_index, rows, I, dtype, true, q, ldq, scale, lds,
-                    stream);
+extern "C" int exmoe_swiglu_fp8(const exmoe_fp8_rows* call, hipStream_t stream) {
+  return quant_rows("exmoe_swiglu_fp8", call, true, stream);
 }
 
-extern "C" int exmoe_quantize_fp8_weights(const void* w, size_t ldw, size_t w_stride, int E, int N, int K, int dtype, uint8_t* q,
-                                          size_t ldq, size_t q_stride, float* scale, size_t lds, size_t s_stride,
-                                          hipStream_t stream) {
-  EXMOE_TRY(check_input(K, dtype));
+extern "C" int exmoe_quantize_fp8_weights(const exmoe_fp8_matrices* call, hipStream_t stream) {
+  EXMOE_CALL(call);
+  const exmoe_fp8_matrices& c = *call;
+  const int E = c.E, N = c.N, K = c.K;
+  EXMOE_TRY(check_input(K, c.dtype));
   if (E < 1 || N < 1) return set_error(EXMOE_ERR_INVALID_ARGUMENT, "E and N must be positive (got %d, %d)", E, N);
   const int nb = ceil_div(N, 128), kb = ceil_div(K, 128);
   if (E > 65535 || nb > 65535 || (long long)E * nb * kb > kMaxThreads / 256)
     return set_error(EXMOE_ERR_UNSUPPORTED, "exmoe_quantize_fp8_weights: more blocks than one launch holds");
-  const int b = dtype_bytes(dtype);
-  EXMOE_TRY(check_matrix("w", w, ldw, K, b));
-  EXMOE_TRY(check_experts("w", ldw, w_stride, N, K, E));
-  EXMOE_TRY(check_matrix("q", q, ldq, K, 1));
-  EXMOE_TRY(check_experts("q", ldq, q_stride, N, K, E));
-  EXMOE_TRY(check_matrix("scale", scale, lds, kb, 4));
-  EXMOE_TRY(check_experts("scale", lds, s_stride, nb, kb, E));
-  const MemRows mw = mem_matrices("w", w, E, w_stride, N, ldw, K, b), mq = mem_matrices("q", q, E, q_stride, N, ldq, K, 1),
-                ms = mem_matrices("scale", scale, E, s_stride, nb, lds, kb, 4);
+  const int b = dtype_bytes(c.dtype);
+  EXMOE_TRY(check_matrix("w", c.w, c.ldw, K, b));
+  EXMOE_TRY(check_experts("w", c.ldw, c.w_stride, N, K, E));
+  EXMOE_TRY(check_matrix("q", c.q, c.ldq, K, 1));
+  EXMOE_TRY(check_experts("q", c.ldq, c.q_stride, N, K, E));
+  EXMOE_TRY(check_matrix("scale", c.scale, c.lds, kb, 4));
+  EXMOE_TRY(check_experts("scale", c.lds, c.s_stride, nb, kb, E));
+  const MemRows mw = mem_matrices("w", c.w, E, c.w_stride, N, c.ldw, K, b), mq = mem_matrices("q", c.q, E, c.q_stride, N, c.ldq, K, 1),
+                ms = mem_matrices("scale", c.scale, E, c.s_stride, nb, c.lds, kb, 4);
   EXMOE_TRY(check_apart(mq, {mw, ms}));
   EXMOE_TRY(check_apart(ms, {mw}));
   QuantMatrices a{};
-  a.w = w; a.ldw = ldw; a.w_stride = E > 1 ? w_stride : 0; a.N = N; a.K = K; a.q = q; a.ldq = ldq; a.q_stride = E > 1 ? q_stride : 0;
-  a.scale = scale; a.lds = lds; a.s_stride = E > 1 ? s_stride : 0;
-  return launched(by_dtype(dtype, [&](auto dt) {
+  a.w = c.w; a.ldw = c.ldw; a.w_stride = E > 1 ? c.w_stride : 0; a.N = N; a.K = K; a.q = c.q; a.ldq = c.ldq;
+  a.q_stride = E > 1 ? c.q_stride : 0; a.scale = c.scale; a.lds = c.lds; a.s_stride = E > 1 ? c.s_stride : 0;
+  return launched(by_dtype(c.dtype, [&](auto dt) {
                     ProfScope prof("quantize_fp8_weights", stream);
                     EXMOE_LAUNCH(prof, (quant_matrix_kernel<decltype(dt)::value>), dim3(kb, nb, E), dim3(256), 0, stream, a);
                     return hipGetLastError();
