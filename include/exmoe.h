@@ -476,7 +476,7 @@ int exmoe_lora_linear(const void* x, size_t ldx, const void* w, size_t ldw, cons
  *                                              wv = w * w_scale[e, n / 128, k / 128]
  * with that call's segments, row_index, row_div and rows outside segments; expert_offsets may be
  * NULL with E = 1 (one matrix for all rows). K is a multiple of 16; rows of x and w are 16-byte
- * aligned (base, ld and w_stride), ld <= 2^22; y any alignment, out_dtype bf16, fp16 or fp32. What
+ * aligned (base, ld and w_stride), ld <= 2^22 (of scales: 2^20); y any alignment, out_dtype bf16, fp16 or fp32. What
  * x and w hold between K and ld is not read. Each block of 128 positions is
  * summed by the matrix unit and scaled into an fp32 sum. Its 8-bit adders drop what lies below
  * 2^-13 of the largest of 8 neighbouring products: for 16-bit outputs that is a tenth of their

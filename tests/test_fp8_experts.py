@@ -141,7 +141,7 @@ def test_refusals_of_the_product():
     refuses(mm, INV, rows=[-1], N=[0], K=[0, 8, 100], E=[0, 257], od=[3], div=[0], x=[None, X + 8], w=[None, W + 8], xs=[None, XS + 2],
             ws=[None, WS + 1], ldx=[255, 264], ldw=[128, 260], wst=[100, 256 * 100 + 8], ldxs=[1], ldws=[1], wsst=[1], off=[None, OFF + 2],
             y=[None, Y + 1], ldy=[99], x_rows=[7], ri=[dict(ri=RI, x_rows=0), dict(ri=RI + 1)])
-    refuses(mm, UNS, N=[(1 << 24) + 1], ldx=[(1 << 22) + 16], ldxs=[(1 << 20) + 1],
+    refuses(mm, UNS, N=[(1 << 24) + 1], ldx=[(1 << 22) + 16], ldxs=[(1 << 20) + 1], ldws=[dict(ldws=(1 << 20) + 1, wsst=1 << 22)],
             tiles=[dict(rows=1 << 30, x_rows=1 << 30, N=1 << 24, ldy=1 << 24, wst=1 << 34, wsst=1 << 20)])
     assert mm(rows=0, x=None) == 0
 
@@ -384,7 +384,7 @@ def test_norm_of_special_rows():
 
 
 # ------------------------------------------------------------------ product
-def product_ref(x, xs, w, ws, offsets, src):
+def product_ref(x, xs, w, ws, offsets, src, cuts=False):
     """y and the products' magnitudes, in 64 bits; x, w the e4m3 values, src: the row of x of each row, -1: zeros."""
     rows, (E, N, K) = len(src), w.shape
     xv = x.double() * spread(xs.double(), x.shape[0], K)
@@ -395,8 +395,9 @@ def product_ref(x, xs, w, ws, offsets, src):
         a, b = int(offsets[e]), int(offsets[e + 1])
         if a < b:
             y[a:b] = xr[a:b] @ wv[e].t()
-            mag[a:b] = xr[a:b].abs() @ wv[e].abs().t()
-            for k in range(0, K, 8):     # the largest product of each 8 neighbours
+            if cuts:
+                mag[a:b] = xr[a:b].abs() @ wv[e].abs().t()
+            for k in range(0, K if cuts else 0, 8):     # the largest product of each 8 neighbours
                 part = xr[a:b, None, k:k + 8].abs() * wv[e][None, :, k:k + 8].abs()
                 cut[a:b] += part.amax(-1)
     return y, mag, cut
@@ -427,7 +428,7 @@ def check_product(x, xs, w, ws, counts, dtype, row_index=None, row_div=1, exact=
     rows = int(off[-1]) if row_index is None else len(row_index)
     src = torch.arange(rows) if row_index is None else torch.where(row_index >= 0, row_index // row_div, -1).long()
     src = torch.where(src < x.shape[0], src, -1)
-    y, mag, cut = product_ref(x.float(), xs, w.float(), ws, off, src)
+    y, mag, cut = product_ref(x.float(), xs, w.float(), ws, off, src, cuts=not exact)
     yd = torch.full((rows, w.shape[1] + ragged), 7.0, dtype=dtype, device="cuda")[:, ragged // 2:w.shape[1] + ragged // 2]
     ri = None if row_index is None else row_index.cuda()
     xd, wd = (on_gpu(t, 0, 16 * bool(ragged)) for t in (x, w))
@@ -452,7 +453,8 @@ def whole_operands(gen, rows, E, N, K):
 
 PRODUCTS = [([1], 1, 16), ([1], 16, 16), ([1], 128, 128), ([3, 0, 1], 40, 272), ([0, 0, 0, 2], 517, 128), ([16], 256, 2048),
             ([17, 1, 40, 0, 9], 200, 400), ([130], 130, 144), ([200, 3, 64], 384, 640), ([300], 64, 1008), ([515, 257], 256, 256),
-            ([1] * 60 + [0] * 4, 48, 256), ([2500], 136, 128)]
+            ([1] * 60 + [0] * 4, 48, 256), ([2500], 136, 128), ([40] * 30, 640, 144), ([90, 0, 130, 77] * 4, 4100, 128),
+            ([1200, 3, 900], 6700, 160), ([2049], 6400, 272)]
 
 
 @gpu
@@ -528,6 +530,28 @@ def test_a_nan_stays_in_its_row_and_column(rows):
         assert torch.equal(got[fine], y.to(dtype)[fine])
         assert bool(torch.isnan(got[1]).all()) and bool(torch.isnan(got[:, 40]).all()) and bool(torch.isnan(got[:, 128:]).all())
         assert not bool(torch.isfinite(got[2]).any())
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_rows_of_x_beyond_32_bit_offsets(dtype):
+    """x of 2.2 GiB behind row_index: rows at its start, around 2 GiB and at its end; zeros elsewhere."""
+    gen = torch.Generator().manual_seed(13)
+    N, K, rows = 200, 2048, 1150000
+    at = torch.tensor([0, 3, (1 << 20) - 1, 1 << 20, (1 << 20) + 1, rows - 2, rows - 1])
+    x, xs, w, ws = whole_operands(gen, len(at), 2, N, K)
+    xd = torch.zeros((rows, K), dtype=torch.uint8, device="cuda").view(F8)
+    sd = torch.zeros((rows, K // 128), device="cuda")
+    xd.view(torch.uint8)[at.cuda()] = x.view(torch.uint8).cuda()
+    sd[at.cuda()] = xs.cuda()
+    pick = torch.randint(0, len(at), (150,), generator=gen)
+    index = at[pick].to(torch.int32)
+    index[7], index[8], index[9] = -1, rows, 77
+    src = torch.where(torch.arange(150) == 9, len(at), torch.where((index < 0) | (index >= rows), -1, pick))
+    off = offsets_of([60, 90])
+    y, _, _ = product_ref(torch.cat([x.float(), torch.zeros((1, K))]), torch.cat([xs, torch.zeros((1, K // 128))]), w.float(), ws, off, src)
+    got = exm.grouped_mm_fp8(xd, sd, w.cuda(), ws.cuda(), off.cuda(), row_index=index.cuda(), out_dtype=dtype)
+    assert torch.equal(got.cpu().double(), y.to(dtype).double())
 
 
 @gpu

@@ -31,6 +31,7 @@ struct Fp8Args {
   void* out;
   size_t ldo;
   int vec;
+  int far;                          // rows of x behind row_index lie further apart than 32-bit offsets reach
 };
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
@@ -114,6 +115,31 @@ struct TileRows {
   }
 };
 
+// Rows of x anywhere in memory (behind row_index, 2 GiB of x and more): 64-bit addresses per lane in
+// place of offsets into a buffer; the layout in LDS is that of WideRows.
+template <int B, int NW>
+struct FarRows {
+  static constexpr int kSlots = B / (8 * NW);
+  int red, wave, chunk;
+  const uint8_t* row[kSlots];   // null: zeros
+  template <class F>
+  __device__ __forceinline__ void init(int red_, int wave_, int lane, F row_at) {
+    red = red_;
+    wave = wave_;
+    chunk = 8 * ((lane & 7) ^ WideRows<B, NW, 64>::swz(wave * 8 + lane / 8));
+#pragma unroll
+    for (int i = 0; i < kSlots; i++) row[i] = row_at((i * NW + wave) * 8 + lane / 8);
+  }
+  __device__ __forceinline__ void stage(uint16_t* lds, int k0) const {
+#pragma unroll
+    for (int i = 0; i < kSlots; i++) {
+      const void* src = g_zero16;
+      if (k0 + chunk < red && row[i]) src = row[i] + 2 * (size_t)(k0 + chunk);
+      lds_copy16(src, lds + (i * NW + wave) * 8 * 64);
+    }
+  }
+};
+
 // 16 TP WP x 16 TQ WQ outputs per workgroup of WP x WQ waves; 128-deep slices of both operands and
 // their scales double-buffered in LDS, one barrier per slice. A slice is TP steps of TQ matrix
 // instructions: step i multiplies the wave's columns, held in registers, with row block i, whose
@@ -122,7 +148,7 @@ struct TileRows {
 // fragments, so every wave is done reading the slice, and the next but one is copied over it while the
 // first fragments of the next are read between those products.
 // Row blocks are dealt to the WP wave rows in turn, and blocks past the tile's rows are skipped.
-template <class ET, class Frag, int TP, int TQ, int WP, int WQ, int OCC>
+template <class ET, class Frag, int TP, int TQ, int WP, int WQ, int OCC, bool FAR>
 __global__ __launch_bounds__(64 * WP * WQ, OCC) void fp8_tile_kernel(Fp8Args a, int q_tiles) {
   constexpr int NW = WP * WQ, BP = 16 * TP * WP, BQ = 16 * TQ * WQ, D = 64;   // (D: pairs of bytes)
   static_assert(BQ % 128 == 0 && 128 % (16 * TQ) == 0, "a wave's columns lie in one block of scales");
@@ -142,37 +168,54 @@ __global__ __launch_bounds__(64 * WP * WQ, OCC) void fp8_tile_kernel(Fp8Args a, 
   const int q0 = BQ * r.qt, red = a.K / 2;
   const uint32_t dmul = 0xFFFFFFFFu / (uint32_t)a.row_div;
   const TileRows rows(a, r);
-  WideRows<BP, NW, D> op_p;
+  std::conditional_t<FAR, FarRows<BP, NW>, WideRows<BP, NW, D>> op_p;
   WideRows<BQ, NW, D> op_q;
-  op_p.init(rows.x, red, wave, lane, [&](int i) {
-    const int s = rows.row(a, r, i, dmul);
-    return s < 0 ? kNowhere : (uint32_t)((size_t)s * a.ldx);
-  });
+  if constexpr (FAR) {
+    op_p.init(red, wave, lane, [&](int i) {
+      const int s = rows.row(a, r, i, dmul);
+      return s < 0 ? nullptr : a.x + (size_t)s * a.ldx;
+    });
+  } else {
+    op_p.init(rows.x, red, wave, lane, [&](int i) {
+      const int s = rows.row(a, r, i, dmul);
+      return s < 0 ? kNowhere : (uint32_t)((size_t)s * a.ldx);
+    });
+  }
   const int ncols = min(BQ, a.N - q0);
   op_q.init(make_buf(a.w + (size_t)r.e * a.w_stride + (size_t)q0 * a.ldw, (size_t)(ncols - 1) * a.ldw + a.K), red, wave, lane,
             [&](int i) { return i < ncols ? (uint32_t)((size_t)i * a.ldw) : kNowhere; });
   buf_t sc_buf[kScaleCopies];
   uint32_t sc_off[kScaleCopies];
+  const float* sc_far[kScaleCopies];   // (FAR: addresses in place of offsets; null: zeros)
 #pragma unroll
   for (int c = 0; c < kScaleCopies; c++) {
     const int part = c * NW + wave;
     sc_buf[c] = rows.xs;
     sc_off[c] = kNowhere;
+    sc_far[c] = nullptr;
     if (part < BP / 64) {
       const int s = rows.row(a, r, 64 * part + lane, dmul);
-      if (s >= 0) sc_off[c] = (uint32_t)((size_t)s * a.ldxs * 4);
+      if (s >= 0) sc_off[c] = (uint32_t)((size_t)s * a.ldxs * 4), sc_far[c] = a.xs + (size_t)s * a.ldxs;
     } else if (part == BP / 64) {
       const int nb = (ncols + 127) / 128;
-      sc_buf[c] = make_buf(a.ws + (size_t)r.e * a.ws_stride + (size_t)(q0 / 128) * a.ldws, 4 * ((size_t)(nb - 1) * a.ldws + (a.K + 127) / 128));
-      if (lane < nb) sc_off[c] = (uint32_t)((size_t)lane * a.ldws * 4);
+      const float* ws = a.ws + (size_t)r.e * a.ws_stride + (size_t)(q0 / 128) * a.ldws;
+      sc_buf[c] = make_buf(ws, 4 * ((size_t)(nb - 1) * a.ldws + (a.K + 127) / 128));
+      if (lane < nb) sc_off[c] = (uint32_t)((size_t)lane * a.ldws * 4), sc_far[c] = ws + (size_t)lane * a.ldws;
     }
   }
   const int steps = (a.K + 127) / 128;
   auto stage_scales = [&](int s, float* ls) __attribute__((always_inline)) {
 #pragma unroll
-    for (int c = 0; c < kScaleCopies; c++)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(sc_buf[c], (__attribute__((address_space(3))) void*)(ls + 64 * (c * NW + wave)), 4,
-                                               s < steps ? sc_off[c] : kNowhere, s < steps ? 4 * s : 0, 0, 0);
+    for (int c = 0; c < kScaleCopies; c++) {
+      auto* dst = (__attribute__((address_space(3))) void*)(ls + 64 * (c * NW + wave));
+      if constexpr (FAR) {
+        const void* src = g_zero16;
+        if (s < steps && sc_far[c]) src = sc_far[c] + s;
+        __builtin_amdgcn_global_load_lds(src, dst, 4, 0, 0);
+      } else {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(sc_buf[c], dst, 4, s < steps ? sc_off[c] : kNowhere, s < steps ? 4 * s : 0, 0, 0);
+      }
+    }
   };
 
   f32x4 acc[TQ][TP];
@@ -214,7 +257,7 @@ __global__ __launch_bounds__(64 * WP * WQ, OCC) void fp8_tile_kernel(Fp8Args a, 
     fp[i & 1] = read_frag((Frag*)nullptr, lp, 16 * i * WP, at_p);
     sx[i & 1] = ls[block_p(i) + (lane & 15)];
   };
-  // a step by itself, its reads first, the copies and multiply-adds spread between its products
+  // a step by itself: its reads, copies and multiply-adds spread between its products
   auto interleave = [&](auto full, auto reads_c, auto copies_c) __attribute__((always_inline)) {
     if constexpr (decltype(full)::value) {
       constexpr int reads = decltype(reads_c)::value, copies = decltype(copies_c)::value;
@@ -247,10 +290,12 @@ __global__ __launch_bounds__(64 * WP * WQ, OCC) void fp8_tile_kernel(Fp8Args a, 
       if constexpr (decltype(i)::value + 1 < TP) {
         read_p(std::integral_constant<int, decltype(i)::value + 1>{}, cp, cs);
         multiply(full, i);
-        constexpr int copies = decltype(i)::value == 0 ? decltype(op_q)::kSlots : decltype(i)::value == 1 ? decltype(op_p)::kSlots : decltype(i)::value == 2 ? kScaleCopies : 0;
-        if constexpr (decltype(i)::value == 0) op_q.stage(nq, (s + 1) * D);
-        if constexpr (decltype(i)::value == 1) op_p.stage(np, (s + 1) * D);
-        if constexpr (decltype(i)::value == 2) stage_scales(s + 1, ns);
+        constexpr int at = decltype(i)::value, with_p = TP > 2 ? 1 : 0, with_s = TP > 3 ? 2 : with_p;
+        constexpr int copies = (at == 0 ? decltype(op_q)::kSlots : 0) + (at == with_p ? decltype(op_p)::kSlots : 0) +
+                               (at == with_s ? kScaleCopies : 0);
+        if constexpr (at == 0) op_q.stage(nq, (s + 1) * D);
+        if constexpr (at == with_p) op_p.stage(np, (s + 1) * D);
+        if constexpr (at == with_s) stage_scales(s + 1, ns);
         interleave(full, std::integral_constant<int, 3>{}, std::integral_constant<int, copies>{});
       }
     };
@@ -289,16 +334,44 @@ __global__ __launch_bounds__(64 * WP * WQ, OCC) void fp8_tile_kernel(Fp8Args a, 
   else loop(std::false_type{});
   wait_vm<0>();    // no copy is left behind the workgroup's end
 
-  // lane l holds row l % 16 and columns 4 (l / 16) + 0..3 of each 16 x 16 block
+  // Lane l holds row l % 16 and columns 4 (l / 16) + 0..3 of each 16 x 16 block: each wave turns a row block
+  // at a time through its own part of LDS, so that rows leave in pieces of 16 bytes a lane, 16 TQ outputs
+  // together (chunks swizzled by the row). The stores bypass the caches.
+  block_barrier();   // everyone is done with the slices
+  constexpr int kCols = 16 * TQ, SZ = F32 ? 4 : 2, kPitch = kCols * SZ;
+  constexpr int kLanes = kPitch / 16, kRows = 64 / kLanes;   // lanes (16-byte chunks) per row, rows per store
+  static_assert(16 * kPitch * NW <= (BP < BQ ? BP : BQ) * D * 4 && kLanes >= 8 && kLanes <= 16, "a block of rows per wave fits");
+  char* mine = reinterpret_cast<char*>(wave < NW / 2 ? s_p0 : s_p1) + wave % (NW / 2) * 16 * kPitch;
+  auto at = [&](int row, int byte) __attribute__((always_inline)) { return mine + row * kPitch + (byte ^ (16 * (row & (kLanes - 1)))); };
+  const int qw = q0 + wq * kCols;
 #pragma unroll
   for (int i = 0; i < TP; i++) {
-    const int p = r.p0 + block_p(i) + (lane & 15);
-    if (p >= r.p1) continue;
-    const size_t row = (size_t)(r.seg0 + p) * a.ldo;
+    if (i >= nblk) break;
 #pragma unroll
     for (int j = 0; j < TQ; j++) {
-      const int q = q0 + (wq * TQ + j) * 16 + 4 * (lane >> 4);
-      if (q < a.N) store4<ET>(a.out, row + q, F32, a.vec, a.N - q, acc[j][i]);
+      const f32x4& c = acc[j][i];
+      char* p = at(lane & 15, (16 * j + 4 * (lane >> 4)) * SZ);
+      if constexpr (F32) *reinterpret_cast<f32x4*>(p) = c;
+      else *reinterpret_cast<uint2*>(p) = make_uint2(ET::pack2(c[0], c[1]), ET::pack2(c[2], c[3]));
+    }
+    const int pb = r.p0 + block_p(i);
+#pragma unroll
+    for (int r0 = 0; r0 < 16; r0 += kRows) {
+      const int row = r0 + lane / kLanes, col = (lane % kLanes) * (16 / SZ), q = qw + col;
+      const i32x4 v = *reinterpret_cast<const i32x4*>(at(row, col * SZ));
+      if (pb + row < r.p1 && q < a.N) {
+        char* dst = static_cast<char*>(a.out) + ((size_t)(r.seg0 + pb + row) * a.ldo + q) * SZ;
+        if (a.vec && q + 16 / SZ <= a.N) {
+          __builtin_nontemporal_store(v, reinterpret_cast<i32x4*>(dst));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16 / SZ; e++)
+            if (q + e < a.N) {
+              if constexpr (F32) reinterpret_cast<uint32_t*>(dst)[e] = (uint32_t)v[e];
+              else reinterpret_cast<uint16_t*>(dst)[e] = (uint16_t)((uint32_t)v[e / 2] >> (16 * (e & 1)));
+            }
+        }
+      }
     }
   }
 }
@@ -400,12 +473,12 @@ __global__ __launch_bounds__(64 * NW) void fp8_narrow_kernel(Fp8Args a, int q_ti
 }
 
 // ------------------------------------------------------------------------------------ host
-template <class ET, class Frag, int TP, int TQ, int WP, int WQ, int OCC>
+template <class ET, class Frag, int TP, int TQ, int WP, int WQ, int OCC, bool FAR = false>
 static hipError_t launch_tile(const Fp8Args& a, hipStream_t s) {
   constexpr int BP = 16 * TP * WP, BQ = 16 * TQ * WQ;
   const int qt = ceil_div(a.N, BQ);
   ProfScope prof("grouped_mm_fp8", s);
-  EXMOE_LAUNCH(prof, (fp8_tile_kernel<ET, Frag, TP, TQ, WP, WQ, OCC>), dim3((unsigned)(row_tiles(a.rows, a.E, BP) * qt)),
+  EXMOE_LAUNCH(prof, (fp8_tile_kernel<ET, Frag, TP, TQ, WP, WQ, OCC, FAR>), dim3((unsigned)(row_tiles(a.rows, a.E, BP) * qt)),
                dim3(64 * WP * WQ), 0, s, a, qt);
   return hipGetLastError();
 }
@@ -419,19 +492,42 @@ static hipError_t launch_narrow(const Fp8Args& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Rows per expert up to which 16 x 32 blocks on two waves, bound by reading W, run instead of 128 x 128 tiles.
-constexpr int kNarrowRows = 12;
-// Fewer 128 x 128 tiles than half the CUs: 16 x 64 blocks whose waves split the reduction.
-static bool few_tiles(int rows, int Q, int E) {
-  return (rows / 128 + (long long)(E < rows ? E : rows)) * ceil_div(Q, 128) < 128;
-}
+// Tiles of bp rows into which the experts' rows fall, on average over their remainders.
+static double mean_tiles(int rows, int E, int bp) { return E > 1 ? (double)rows / bp + 0.5 * (E < rows ? E : rows) : ceil_div(rows, bp); }
 
+// Form of the call. Measured, us (bf16 out; forms: 16 x 32 blocks / 16 x 64 blocks / 64 x 128 tiles / 128 x 128 /
+// 192 x 256 / 256 x 256), N x K and E experts of R rows on average:
+//   2048 x 2048, E = 64, R = 2       44 /  45 /  55 /  55 /   - /   -
+//                        R = 8       55 /  55 /   - /  59 /   - /   -
+//                        R = 16      63 /  60 /  57 /  57 /  62 /  64
+//                        R = 32      88 /  79 /  58 /  60 /  64 /  66
+//                        R = 64     134 / 116 /  69 /  64 /  67 /  68
+//                        R = 256 (skewed)  - / 350 / 155 / 142 / 125 / 133
+//   1024 x 2048, E = 4,  R = 125     11 /  10 /  14 /  18 /  23 /  24
+//   4096 x 4096, E = 1,  R = 128      - /  13 /  25 /  30 /  38 /  41
+//                        R = 512     47 /  38 /  27 /  31 /  43 /  48
+//   2048 x 2048, E = 1,  R = 2048    51 /  43 /  17 /  19 /  25 /  28
+//   4096 x 4096, E = 8,  R = 1024     - / 530 / 225 / 210 / 174 / 187
+//   4096 x 4096, E = 1,  R = 4096     - /   - /  73 /  79 /  89 /  61
+//   14336 x 4096, E = 8, R = 1024     - /   - /   - / 681 / 597 / 544
+// Few rows per expert are bound by reading W; then the number of tiles decides how many compute units work, and
+// then how often the tiles fill them: 192 x 256 tiles take 0.8 of the time of 256 x 256 ones, and the last round
+// of tiles is half full on average (with one expert their number is known).
 template <class ET, class Frag>
 static hipError_t launch_fp8(const Fp8Args& a, hipStream_t s) {
-  if (a.rows <= kNarrowRows * (long long)a.E) return launch_narrow<ET, Frag, 1, 2, 2>(a, s);
-  if (few_tiles(a.rows, a.N, a.E)) return launch_narrow<ET, Frag, 1, 4, 4>(a, s);
+  const int E = a.E < a.rows ? a.E : a.rows;
+  const long long tiles = (a.rows / 128 + (long long)E) * ceil_div(a.N, 128);
+  if (a.far) return launch_tile<ET, Frag, 4, 4, 2, 2, 2, true>(a, s);
+  if (a.rows <= 12 * (long long)a.E) return launch_narrow<ET, Frag, 1, 2, 2>(a, s);
+  if (tiles < 128) return launch_narrow<ET, Frag, 1, 4, 2>(a, s);
+  if (tiles < 512 || a.rows <= 48 * (long long)a.E) return launch_tile<ET, Frag, 2, 4, 2, 2, 2>(a, s);
   if constexpr (std::is_same<Frag, FragF8>::value) {
-    if (a.rows / a.E >= 160 && (long long)(a.rows / 256) * ceil_div(a.N, 256) >= 256) return launch_tile<ET, Frag, 8, 4, 2, 4, 2>(a, s);
+    const int qt = ceil_div(a.N, 256);
+    if (a.rows / a.E >= 160 && (long long)(a.rows / 256) * qt >= 200) {
+      auto rounds = [&](int bp) { return a.E > 1 ? mean_tiles(a.rows, a.E, bp) * qt / 256 + 0.5 : (double)ceil_div((int)(mean_tiles(a.rows, 1, bp) * qt), 256); };
+      if (0.8 * rounds(192) < rounds(256)) return launch_tile<ET, Frag, 6, 4, 2, 4, 2>(a, s);
+      return launch_tile<ET, Frag, 8, 4, 2, 4, 2>(a, s);
+    }
   }
   return launch_tile<ET, Frag, 4, 4, 2, 2, 2>(a, s);
 }
@@ -472,13 +568,12 @@ extern "C" int exmoe_grouped_mm_fp8(const exmoe_grouped_fp8* call, hipStream_t s
   EXMOE_TRY(check_matrix("x_scale", x_scale, ldxs, kb, 4));
   EXMOE_TRY(check_matrix("w_scale", w_scale, ldws, kb, 4));
   EXMOE_TRY(check_experts("w_scale", ldws, ws_stride, nb, kb, E));
-  if (ldxs > (1u << 20)) return set_error(EXMOE_ERR_UNSUPPORTED, "x_scale: row stride %zu, at most 2^20 is supported", ldxs);
+  if (ldxs > (1u << 20) || ldws > (1u << 20))
+    return set_error(EXMOE_ERR_UNSUPPORTED, "x_scale, w_scale: row strides %zu and %zu, at most 2^20 is supported", ldxs, ldws);
   EXMOE_TRY(check_matrix("y", y, ldy, N, ob));
   EXMOE_TRY(check_int32("row_index", row_index, true));
   EXMOE_TRY(check_int32("expert_offsets", expert_offsets, true));
-  if (row_index && ((size_t)x_rows * ldx >= kMaxSpan || (size_t)x_rows * ldxs * 4 >= kMaxSpan))
-    return set_error(EXMOE_ERR_UNSUPPORTED, "x of %d rows behind row_index spans 2 GiB or more", x_rows);
-  if (!tiles_fit(rows, N, E, 128, 128, 256))
+  if (!tiles_fit(rows, N, E, 64, 128, 256))
     return set_error(EXMOE_ERR_UNSUPPORTED, "exmoe_grouped_mm_fp8: more output tiles than one launch holds");
   const int xr = row_index ? x_rows : rows;
   const MemRows mx = mem_matrix("x", x, xr, ldx, K, 1), mw = mem_matrices("w", w, E, w_stride, N, ldw, K, 1),
@@ -489,6 +584,7 @@ extern "C" int exmoe_grouped_mm_fp8(const exmoe_grouped_fp8* call, hipStream_t s
   a.x = x; a.w = w; a.ldx = ldx; a.ldw = ldw; a.w_stride = E > 1 ? w_stride : 0; a.xs = x_scale; a.ws = w_scale; a.ldxs = ldxs;
   a.ldws = ldws; a.ws_stride = E > 1 ? ws_stride : 0; a.offsets = expert_offsets; a.row_index = row_index; a.row_div = row_div;
   a.x_rows = xr; a.rows = rows; a.N = N; a.K = K; a.E = E; a.out = y; a.ldo = ldy; a.vec = vec_store(y, ldy, 0, ob == 4);
+  a.far = row_index && ((size_t)x_rows * ldx >= kMaxSpan || (size_t)x_rows * ldxs * 4 >= kMaxSpan);
   const hipError_t e = out_dtype == EXMOE_DTYPE_FP32 ? launch_fp8<ElemBF16, FragBF16>(a, stream)
                        : out_dtype == EXMOE_DTYPE_FP16 ? launch_fp8<ElemFP16, FragF8>(a, stream)
                                                        : launch_fp8<ElemBF16, FragF8>(a, stream);
