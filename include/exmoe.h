@@ -544,6 +544,40 @@ typedef struct exmoe_grouped_fp8 {
 } exmoe_grouped_fp8;
 int exmoe_grouped_mm_fp8(const exmoe_grouped_fp8* call, hipStream_t stream);
 
+/* The layer of these calls in one, as exmoe_moe_layer is that of the int4 experts: residual += x (bf16, in
+ * place; NULL: no residual), norm of it by w_norm, exmoe_route_topk of the 16-bit norm (whose rules hold
+ * for w_router, logit_bias, k and renormalize), exmoe_group_tokens, gate and up of the 8-bit norm, exmoe_swiglu_fp8
+ * with the routing weights, down, and y[t] = the sum of token t's k rows in slot order (bf16 rows, fp32
+ * sums). Every result is that of the separate calls, bit for bit.
+ * x, y, residual bf16 [T, H]; w_norm bf16 [H]; w_router bf16 [E, H]; gate_up e4m3 [E, 2 I, H], gate's rows
+ * first, its scales [E, 2 I / 128, H / 128]; down e4m3 [E, H, I], its scales [E, H / 128, I / 128]; logits bf16
+ * [T, E]; the routing and grouping outputs of the calls named. All contiguous and 16-byte aligned; no output
+ * may share bytes with another operand. H and I multiples of 128, up to 16384; T < 2^22, T k <= 2^24.
+ * Workspace: exmoe_moe_layer_fp8_workspace_bytes bytes, 16-byte aligned, no initialization, not kept; calls
+ * that overlap in time must not share one. T == 0 writes expert_offsets only. */
+typedef struct exmoe_layer_fp8 {
+  const exmoe_bf16* x;
+  const exmoe_bf16* w_norm;
+  exmoe_bf16* residual; /* or NULL */
+  const exmoe_bf16* w_router;
+  const float* logit_bias; /* or NULL */
+  const uint8_t* gate_up;
+  const float* gate_up_scale;
+  const uint8_t* down;
+  const float* down_scale;
+  exmoe_bf16* logits;
+  int32_t* topk_ids;
+  float* topk_weights;
+  int32_t* expert_offsets;
+  int32_t* sorted_flat;
+  int32_t* flat_to_sorted;
+  exmoe_bf16* y;
+  float eps;
+  int T, H, I, E, k, renormalize;
+} exmoe_layer_fp8;
+size_t exmoe_moe_layer_fp8_workspace_bytes(int T, int H, int I, int E, int k);
+int exmoe_moe_layer_fp8(const exmoe_layer_fp8* call, void* workspace, size_t ws_bytes, hipStream_t stream);
+
 /* ------------------------------------------------------------------------------------
  * The losses that train a router, with their gradient (device, asynchronous): what keeps the
  * experts' load even, beside the unchanged top-k (abstract; Fig. 1). Of the M tokens t < T that
@@ -592,7 +626,7 @@ int exmoe_balance_loss_backward(const exmoe_balance* call, hipStream_t stream);
  * "prefill_gateup", "prefill_down", "grouped_mm", "grouped_dgrad", "grouped_wgrad",
  * "pack_rows", "token_sum", "split_sum", "lora_shrink", "lora_linear", "rms_norm", "quantize_fp8",
  * "swiglu_fp8", "quantize_fp8_weights", "grouped_mm_fp8", "balance_loss", "balance_join",
- * "balance_loss_bwd". Process-global. The events bracket the launch as the
+ * "balance_loss_bwd", "row_sum". Process-global. The events bracket the launch as the
  * stream processes it, so a launch that waits for the host is counted with that wait.
  * ---------------------------------------------------------------------------------- */
 int exmoe_profile_enable(int on);

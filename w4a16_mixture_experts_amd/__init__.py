@@ -122,6 +122,8 @@ _SIGS = {
     "exmoe_swiglu_fp8": (_i, [_cp, _vp]),
     "exmoe_quantize_fp8_weights": (_i, [_cp, _vp]),
     "exmoe_grouped_mm_fp8": (_i, [_cp, _vp]),
+    "exmoe_moe_layer_fp8_workspace_bytes": (_sz, [_i] * 5),
+    "exmoe_moe_layer_fp8": (_i, [_cp, _vp, _sz, _vp]),
     "exmoe_balance_loss_workspace_bytes": (_sz, [_i, _i]),
     "exmoe_balance_loss": (_i, [_cp, _vp, _sz, _vp]),
     "exmoe_balance_loss_backward": (_i, [_cp, _vp]),
@@ -626,6 +628,7 @@ _FP8_ROWS = struct.Struct("8Q4i")
 _FP8_MATRICES = struct.Struct("9Q4i")
 _GROUPED_FP8 = struct.Struct("14Q7i4x")
 _BALANCE = struct.Struct("9Q5i4x")
+_LAYER_FP8 = struct.Struct("16Qf6i4x")
 
 
 def _wrong(name: str, t, shape, dtype, dev: int):
@@ -820,6 +823,66 @@ def grouped_mm_fp8(x, x_scale, w, w_scale, offsets=None, row_index=None, row_div
     _run_on(dev, _lib.exmoe_grouped_mm_fp8, _GROUPED_FP8.pack(px, ldx, pxs, ldxs, pi, pf, pw, ldw, sw, pws, ldws, sws, py, ldy,
                                                               x_rows, row_div, rows, N, K, E, _dtype_code(out_dtype)))
     return y
+
+
+class Fp8Experts:
+    """Experts in 8 bits: gate_up [E, 2 I, H] (gate's rows first) and down [E, H, I] in bf16, fp16 or fp32,
+    quantised here (quantize_fp8_weights)."""
+
+    def __init__(self, gate_up, down):
+        E, rows, H = _axes("gate_up", gate_up, 3)
+        if rows % 2 or tuple(down.shape) != (E, H, rows // 2):
+            raise ValueError(f"gate_up {tuple(gate_up.shape)} and down {tuple(down.shape)} must be [E, 2 I, H] and [E, H, I]")
+        self.E, self.H, self.I = E, H, rows // 2
+        if H % 128 or self.I % 128:
+            raise ValueError(f"H and I must be multiples of 128 (got {H}, {self.I})")
+        self.gate_up, self.gate_up_scale = quantize_fp8_weights(gate_up)
+        self.down, self.down_scale = quantize_fp8_weights(down)
+
+
+class Fp8LayerBuffers:
+    """Preallocated outputs and workspace of a moe_layer_fp8 call (no allocation per call)."""
+
+    def __init__(self, T, H, I, E, k, device="cuda"):
+        torch = _torch()
+        self.T, self.H, self.I, self.E, self.k = T, H, I, E, k
+        self.logits = torch.empty((T, E), dtype=torch.bfloat16, device=device)
+        self.ids = torch.empty((T, k), dtype=torch.int32, device=device)
+        self.weights = torch.empty((T, k), dtype=torch.float32, device=device)
+        self.offsets = torch.empty(E + 1, dtype=torch.int32, device=device)
+        self.sorted_flat = torch.empty(max(T * k, 1), dtype=torch.int32, device=device)
+        self.flat_to_sorted = torch.empty(max(T * k, 1), dtype=torch.int32, device=device)
+        self.y = torch.empty((T, H), dtype=torch.bfloat16, device=device)
+        self.workspace = torch.empty(max(_lib.exmoe_moe_layer_fp8_workspace_bytes(T, H, I, E, k), 16), dtype=torch.uint8, device=device)
+
+
+def moe_layer_fp8(x, w_norm, w_router, experts: Fp8Experts, k: int, residual=None, bias=None, eps: float = 1e-6,
+                  renormalize: bool = True, buffers: Optional[Fp8LayerBuffers] = None) -> Fp8LayerBuffers:
+    """residual += x (in place, or without one), its norm, routing, grouping and the experts in 8 bits in
+    one call; returns the Fp8LayerBuffers holding every output. x and residual bf16 [T, H], w_norm bf16 [H],
+    w_router bf16 [E, H], bias fp32 [E], all contiguous. Records no gradient."""
+    for t in (x, w_norm, w_router, residual, bias):
+        if t is not None and t.requires_grad:
+            _no_gradient()
+    torch = _torch()
+    dev, bf16 = _on_gpu("x", x), torch.bfloat16
+    T, H = _axes("x", x, 2)
+    E, I = experts.E, experts.I
+    for name, t, shape, dtype in (("x", x, (T, experts.H), bf16), ("w_norm", w_norm, (H,), bf16), ("w_router", w_router, (E, H), bf16),
+                                  ("residual", residual, (T, H), bf16), ("bias", bias, (E,), torch.float32),
+                                  ("experts", experts.gate_up, (E, 2 * I, H), torch.float8_e4m3fn)):
+        if t is not None and (t.shape != shape or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous {tuple(shape)} {dtype} tensor on GPU {dev} (got {tuple(t.shape)} {t.dtype})")
+    b = buffers or Fp8LayerBuffers(T, H, I, E, k, x.device)
+    if (b.T, b.H, b.I, b.E, b.k) != (T, H, I, E, k) or b.y.get_device() != dev:
+        raise ValueError(f"buffers are of another call: {(b.T, b.H, b.I, b.E, b.k)}, not {(T, H, I, E, k)} on GPU {dev}")
+    _run_on(dev, _lib.exmoe_moe_layer_fp8,
+            _LAYER_FP8.pack(x.data_ptr(), w_norm.data_ptr(), _ptr(residual) or 0, w_router.data_ptr(), _ptr(bias) or 0,
+                            experts.gate_up.data_ptr(), experts.gate_up_scale.data_ptr(), experts.down.data_ptr(),
+                            experts.down_scale.data_ptr(), b.logits.data_ptr(), b.ids.data_ptr(), b.weights.data_ptr(),
+                            b.offsets.data_ptr(), b.sorted_flat.data_ptr(), b.flat_to_sorted.data_ptr(), b.y.data_ptr(), eps, T, H, I,
+                            E, k, int(renormalize)), b.workspace.data_ptr(), b.workspace.numel())
+    return b
 
 
 # ----------------------------------------------------------------------------- router losses
