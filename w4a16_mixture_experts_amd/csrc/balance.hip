@@ -136,19 +136,18 @@ struct LaneCols {
   }
 };
 
-constexpr int kBalThreads = 256;
+constexpr int kFwdThreads = 1024, kBalThreads = 256;
 constexpr int kBwdRows = 4;   // rows of a lane in the backward pass, loaded together
 
 // LANES lanes per row; a workgroup takes every gridDim.x-th run of rows.
 template <int DT, int LANES>
-__global__ __launch_bounds__(kBalThreads) void balance_kernel(BalanceArgs a) {
-  constexpr int kRows = kBalThreads / LANES, kE = 8 * LANES;
-  __shared__ float s_p[kBalThreads / 64][kE + 1];
-  __shared__ int s_n[kE + 1];
+__global__ __launch_bounds__(kFwdThreads) void balance_kernel(BalanceArgs a) {
+  constexpr int kRows = kFwdThreads / LANES, kE = 8 * LANES;
+  __shared__ float s_p[kFwdThreads / 64][kE + 1];
+  __shared__ int s_n[kFwdThreads / 64][kE + 1];   // (a wave's own: eight experts' counters are soon contended for)
   const int t = threadIdx.x, lane = t & 63, wave = t / 64;
   const LaneCols<LANES, DT == EXMOE_DTYPE_FP32> cols(t % LANES);
-  for (int e = t; e <= kE; e += kBalThreads) s_n[e] = 0;
-  __syncthreads();
+  for (int e = lane; e <= kE; e += 64) s_n[wave][e] = 0;
   f32x8 sum = {0, 0, 0, 0, 0, 0, 0, 0};
   float z = 0.f;
   int n = 0;
@@ -166,7 +165,7 @@ __global__ __launch_bounds__(kBalThreads) void balance_kernel(BalanceArgs a) {
     if (t % LANES == 0) n++;
     for (int j = t % LANES; j < a.k; j += LANES) {
       const int e = a.ids[(size_t)row * a.k + j];
-      if ((unsigned)e < (unsigned)a.E) atomicAdd(&s_n[e], 1);   // (whole numbers: any order)
+      if ((unsigned)e < (unsigned)a.E) atomicAdd(&s_n[wave][e], 1);   // (whole numbers: any order)
     }
   }
   // over the wave's rows, then over the waves
@@ -181,20 +180,24 @@ __global__ __launch_bounds__(kBalThreads) void balance_kernel(BalanceArgs a) {
     for (int i = 0; i < 8; i++) s_p[wave][cols.at(i)] = sum[i];
   }
   if (lane == 0) s_p[wave][kE] = z;
-  if (n) atomicAdd(&s_n[kE], n);
+  if (n) atomicAdd(&s_n[wave][kE], n);
   __syncthreads();
-  for (int e = t; e <= a.E; e += kBalThreads) {
+  for (int e = t; e <= a.E; e += kFwdThreads) {
     const int at = e < a.E ? e : kE;
     float v = 0.f;
+    int c = 0;
 #pragma unroll
-    for (int w = 0; w < kBalThreads / 64; w++) v += s_p[w][at];
+    for (int w = 0; w < kFwdThreads / 64; w++) {
+      v += s_p[w][at];
+      c += s_n[w][at];
+    }
     a.part[(size_t)blockIdx.x * (a.E + 1) + e] = v;
-    a.part_n[(size_t)blockIdx.x * (a.E + 1) + e] = s_n[at];
+    a.part_n[(size_t)blockIdx.x * (a.E + 1) + e] = c;
   }
 }
 
-// The sums over the workgroups, and the losses: wave w adds those of workgroups w, w + 16, .. (64
-// experts at a time, all loads at once), then the waves' sums in wave order.
+// The sums over the workgroups, and the losses. 64 experts are a wave's columns, and the waves are dealt to the
+// columns: those of one share its workgroups' sums and add up in wave order.
 __global__ __launch_bounds__(1024) void balance_join_kernel(BalanceArgs a, int blocks) {
   constexpr int kCols = (kMaxExperts + 64) / 64 * 64;
   __shared__ double s_p[16][64];
@@ -202,32 +205,29 @@ __global__ __launch_bounds__(1024) void balance_join_kernel(BalanceArgs a, int b
   __shared__ double s_sum[kCols];
   __shared__ int s_cnt[kCols];
   const int wave = threadIdx.x / 64, lane = threadIdx.x & 63;
-  for (int e0 = 0; e0 <= a.E; e0 += 64) {
-    const int e = e0 + lane;
-    double v = 0.;
-    int n = 0;
-    if (e <= a.E) {
-#pragma unroll 8
-      for (int b = wave; b < blocks; b += 16) {
-        v += a.part[(size_t)b * (a.E + 1) + e];
-        n += a.part_n[(size_t)b * (a.E + 1) + e];
-      }
+  const int chunks = a.E / 64 + 1, per = 16 / chunks, chunk = wave / per, e = 64 * chunk + lane;
+  double v = 0.;
+  int n = 0;
+  if (chunk < chunks && e <= a.E) {
+#pragma unroll 4
+    for (int b = wave - chunk * per; b < blocks; b += per) {
+      v += a.part[(size_t)b * (a.E + 1) + e];
+      n += a.part_n[(size_t)b * (a.E + 1) + e];
     }
-    s_p[wave][lane] = v;
-    s_n[wave][lane] = n;
-    __syncthreads();
-    if (wave == 0) {
-#pragma unroll
-      for (int w = 1; w < 16; w++) {
-        v += s_p[w][lane];
-        n += s_n[w][lane];
-      }
-      s_sum[e] = v;
-      s_cnt[e] = n;
-      if (e <= a.E) a.counts[e] = n;
-    }
-    __syncthreads();
   }
+  s_p[wave][lane] = v;
+  s_n[wave][lane] = n;
+  __syncthreads();
+  if (chunk < chunks && wave == chunk * per) {
+    for (int w = 1; w < per; w++) {
+      v += s_p[wave + w][lane];
+      n += s_n[wave + w][lane];
+    }
+    s_sum[e] = v;
+    s_cnt[e] = n;
+    if (e <= a.E) a.counts[e] = n;
+  }
+  __syncthreads();
   if (wave == 0) {
     double v = 0.;
     for (int e = lane; e < a.E; e += 64) v += s_sum[e] * (double)s_cnt[e];
@@ -296,11 +296,12 @@ static int lanes_of(int E) {
   while (8 * l < E) l *= 2;
   return l;
 }
-// Workgroups of the forward pass: a row per LANES lanes, at most 512 of them (two per compute unit; what is
-// left of the rows they take in turn, and the join reads 512 sums).
+// Workgroups of the forward pass: a row per LANES lanes, at most one per compute unit (what is left of the
+// rows they take in turn). Large workgroups leave few sums to join (8192 tokens of 64 experts, both launches:
+// 7.5 us; with workgroups of 256 threads 8.9; 65536 tokens of 256 experts 25 / 40).
 static int balance_blocks(int T, int E) {
-  const long long n = ((long long)T * lanes_of(E) + kBalThreads - 1) / kBalThreads;
-  return n > 512 ? 512 : (n < 1 ? 1 : (int)n);
+  const long long n = ((long long)T * lanes_of(E) + kFwdThreads - 1) / kFwdThreads;
+  return n > 256 ? 256 : (n < 1 ? 1 : (int)n);
 }
 
 }  // namespace exmoe
@@ -356,7 +357,7 @@ extern "C" int exmoe_balance_loss(const exmoe_balance* call, void* workspace, si
                     return by_lanes(E, [&](auto lanes) {
                       ProfScope prof("balance_loss", stream);
                       EXMOE_LAUNCH(prof, (balance_kernel<decltype(dt)::value, decltype(lanes)::value>), dim3(blocks),
-                                   dim3(kBalThreads), 0, stream, a);
+                                   dim3(kFwdThreads), 0, stream, a);
                       const hipError_t e = hipGetLastError();
                       if (e != hipSuccess) return e;
                       ProfScope join("balance_join", stream);
