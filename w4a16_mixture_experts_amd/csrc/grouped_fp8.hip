@@ -148,6 +148,18 @@ struct FarRows {
 // fragments, so every wave is done reading the slice, and the next but one is copied over it while the
 // first fragments of the next are read between those products.
 // Row blocks are dealt to the WP wave rows in turn, and blocks past the tile's rows are skipped.
+//
+// What bounds it. 256 x 256 tiles, 8192 x 8192 x 8192: 487 us, 2.26 PFLOP/s (the installed BLAS, without block
+// scales, 403); the matrix unit is busy 44% of the cycles of the compute units. Per slice
+// and compute unit the LDS moves 256 KB (192 KB read as fragments, 64 KB written by the copies), 2048 cycles
+// at 128 bytes each, as many as the products take, so both together set the pace. With parts left out, an
+// earlier state of 519 us took 487 without the scaling, 477 with copies that always hit the L2, 372-400 without
+// copies, 312 without copies and scaling, 323 without copies and barrier; the products alone are 250 at 2.1 GHz.
+// Measured and dropped, against 488: 32 x 32 x 64 instructions (589), one wave per SIMD with 256 x 192 outputs
+// (703: the sums do not fit beside what vector instructions can address, and move to and fro), the next columns'
+// fragments read ahead (spills), 128 x 128 tiles of eight waves (746) or four (649), raised priority around the
+// products (506), copies spread over more steps (no change). Rows stored straight from the sums' layout, 8 bytes
+// a lane, instead of in whole lines through LDS: 14336 x 4096 with 8 experts 572 us instead of 544.
 template <class ET, class Frag, int TP, int TQ, int WP, int WQ, int OCC, bool FAR>
 __global__ __launch_bounds__(64 * WP * WQ, OCC) void fp8_tile_kernel(Fp8Args a, int q_tiles) {
   constexpr int NW = WP * WQ, BP = 16 * TP * WP, BQ = 16 * TQ * WQ, D = 64;   // (D: pairs of bytes)
@@ -257,13 +269,15 @@ __global__ __launch_bounds__(64 * WP * WQ, OCC) void fp8_tile_kernel(Fp8Args a, 
     fp[i & 1] = read_frag((Frag*)nullptr, lp, 16 * i * WP, at_p);
     sx[i & 1] = ls[block_p(i) + (lane & 15)];
   };
-  // a step by itself: its reads, copies and multiply-adds spread between its products
+  // a step by itself: its reads, copies and multiply-adds spread between its products (without
+  // these groups 8192 x 8192 x 8192 took 495-507 us instead of 488)
   auto interleave = [&](auto full, auto reads_c, auto copies_c) __attribute__((always_inline)) {
     if constexpr (decltype(full)::value) {
       constexpr int reads = decltype(reads_c)::value, copies = decltype(copies_c)::value;
 #pragma unroll
       for (int j = 0; j < kMfma; j++) {
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        // (the next row block is read behind the first product, longer runs of reads are spread)
         const int nr = reads <= 3 ? (j == 0 ? reads : 0) : (j + 1) * reads / kMfma - j * reads / kMfma;
         const int nc = (j + 1) * copies / kMfma - j * copies / kMfma;
         for (int e = 0; e < nr; e++) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
@@ -378,7 +392,9 @@ __global__ __launch_bounds__(64 * WP * WQ, OCC) void fp8_tile_kernel(Fp8Args a, 
 
 // Few rows per expert, or few tiles: 16 TP rows x 16 TQ columns per workgroup, whose waves split the
 // blocks of 128 positions (wave w: blocks w, w + NW, ..). Each wave copies its own slices of both operands
-// into its own part of LDS, two in flight, without a barrier; the sums are added in wave order.
+// into its own part of LDS, two in flight, without a barrier; the sums are added in wave order. Bound by
+// reading W: 16 tokens through 64 experts of 2048 x 2048, 237 MB, in 44 us on 16 x 32 blocks of two waves
+// (5.4 TB/s; a copy reaches 5.1).
 template <class ET, class Frag, int TP, int TQ, int NW>
 __global__ __launch_bounds__(64 * NW) void fp8_narrow_kernel(Fp8Args a, int q_tiles) {
   constexpr int D = 64, kPart = 16 * (TP + TQ) * D;

