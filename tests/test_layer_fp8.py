@@ -26,6 +26,8 @@ def test_refusals():
         assert call(**bad) == INV, bad
     for bad in (dict(H=16384 + 128), dict(I=32768), dict(T=1 << 22), dict(E=128, k=65), dict(T=1 << 21, k=8, E=8, I=16384)):
         assert call(**bad) == UNS, bad
+    # (2^33 threads for the sums of the rows: more than one launch)
+    assert call(T=(1 << 22) - 1, H=16384, k=1) == UNS and call(T=(1 << 22) - 1, H=256, k=1, wsb=16) == exm.ERR_WORKSPACE
     for name in AT:
         if name in ("residual", "logit_bias", "ws"):
             continue

@@ -66,10 +66,10 @@ static int check_layer(int T, int H, int I, int E, int k) {
   if (k < 1 || k > E) return set_error(EXMOE_ERR_INVALID_ARGUMENT, "k must be in [1, E] (got k=%d, E=%d)", k, E);
   if (k > kMaxK) return set_error(EXMOE_ERR_UNSUPPORTED, "k > 64 is not supported (got %d)", k);
   if (H > kMaxDim || I > kMaxDim) return set_error(EXMOE_ERR_UNSUPPORTED, "H and I must be <= %d", kMaxDim);
-  // (what the product's tiles, the sums and the quantised rows hold in one launch)
+  // (what the product's tiles, the quantised rows and the sums hold in one launch)
   if (T >= 1 << 22 || (long long)T * k > (1 << 24) || !tiles_fit(T * k, 2 * I > H ? 2 * I : H, E, 64, 128, 256) ||
-      (long long)T * k * (I / 128) > (kMaxThreads / 256) * 16)
-    return set_error(EXMOE_ERR_UNSUPPORTED, "T*k too large");
+      (long long)T * k * (I / 128) > (kMaxThreads / 256) * 16 || (long long)T * (H / 8) > kMaxThreads)
+    return set_error(EXMOE_ERR_UNSUPPORTED, "T*k, or T with this H, too large");
   return EXMOE_OK;
 }
 
