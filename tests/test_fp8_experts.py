@@ -182,6 +182,29 @@ def test_a_tensor_that_asks_for_a_gradient_is_refused():
             t.requires_grad_(False)
 
 
+def test_8_bit_operands_that_ask_for_a_gradient_are_refused():
+    x8, v = torch.ones((4, 256)).to(F8), torch.ones((4, 2))
+    w8, ws = x8.view(1, 4, 256), v[:1].view(1, 1, 2)
+    for t in (x8, w8):
+        t.requires_grad_()
+        with pytest.raises(ValueError, match="gradient"):
+            exm.grouped_mm_fp8(x8.detach() if t is w8 else x8, v, w8.detach() if t is x8 else w8, ws)
+        t.requires_grad_(False)
+    with pytest.raises(ValueError, match="gradient"):
+        exm.quantize_fp8_weights(torch.ones((1, 4, 256)), scale=torch.ones((1, 1, 2), requires_grad=True))
+
+
+@gpu
+def test_scales_that_ask_for_a_gradient_are_refused():
+    x, w = torch.ones((4, 256), dtype=BF16, device="cuda"), torch.ones(256, dtype=BF16, device="cuda")
+    for cols, call in ((2, lambda s: exm.quantize_fp8(x, scale=s)), (1, lambda s: exm.swiglu_fp8(x, scale=s)),
+                       (2, lambda s: exm.rms_norm(x, w, out="fp8", scale=s))):
+        s = torch.ones((4, cols), device="cuda", requires_grad=True)
+        with pytest.raises(ValueError, match="gradient"):
+            call(s)
+        assert bool((s == 1).all())
+
+
 @gpu
 def test_refusals_of_the_binding():
     x, w = torch.ones((4, 256), dtype=BF16, device="cuda"), torch.ones(256, dtype=BF16, device="cuda")

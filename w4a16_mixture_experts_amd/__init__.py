@@ -680,6 +680,8 @@ def _f8_outputs(q, scale, rows: int, K: int, dev: int, like):
         q = like.new_empty((rows, (K + 15) // 16 * 16), dtype=torch.float8_e4m3fn)[:, :K]
     if scale is None:
         scale = like.new_empty((rows, (K + 127) // 128), dtype=torch.float32)
+    elif scale.requires_grad:
+        _no_gradient()
     return q, scale, (_mat("q", q, (rows, K), torch.float8_e4m3fn, dev)
                       + _mat("scale", scale, (rows, (K + 127) // 128), torch.float32, dev))
 
@@ -773,7 +775,7 @@ def swiglu_fp8(gate_up, weights=None, row_index=None, q=None, scale=None):
 def quantize_fp8_weights(w, q=None, scale=None):
     """(q, scale) of w [E, N, K] (bf16, fp16 or fp32): e4m3 with a scale per 128 x 128 block, scale
     fp32 [E, ceil(N / 128), ceil(K / 128)]."""
-    if w.requires_grad:
+    if w.requires_grad or scale is not None and scale.requires_grad:
         _no_gradient()
     torch = _torch()
     dev, dtype = _on_gpu("w", w), w.dtype
@@ -798,7 +800,8 @@ def grouped_mm_fp8(x, x_scale, w, w_scale, offsets=None, row_index=None, row_div
     row_index and row_div as in grouped_mm, offsets None for one expert with every row. Returns y
     [rows, N] in out_dtype (bf16, the default, fp16 or fp32); rows outside every segment are left
     as they are."""
-    if x_scale.requires_grad or w_scale.requires_grad or y is not None and y.requires_grad:
+    if (x.requires_grad or w.requires_grad or x_scale.requires_grad or w_scale.requires_grad
+            or y is not None and y.requires_grad):
         _no_gradient()
     torch = _TORCH or _torch()
     dev, f8, f32 = _on_gpu("x", x), torch.float8_e4m3fn, torch.float32
