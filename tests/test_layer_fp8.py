@@ -46,6 +46,11 @@ def test_a_tensor_that_asks_for_a_gradient_is_refused():
         exm.moe_layer_fp8(x, x, x, None, 2)
 
 
+def test_experts_on_two_devices_are_refused():
+    with pytest.raises(ValueError, match="same device"):
+        exm.Fp8Experts(torch.ones((2, 256, 128)), torch.ones((2, 128, 128), device="meta"))
+
+
 def operands(T, H, I, E, seed=0):
     gen = torch.Generator().manual_seed(seed + T)
     randn = lambda *s, sigma=1.0: torch.randn(s, generator=gen) * sigma  # noqa: E731

@@ -836,6 +836,8 @@ class Fp8Experts:
         E, rows, H = _axes("gate_up", gate_up, 3)
         if rows % 2 or tuple(down.shape) != (E, H, rows // 2):
             raise ValueError(f"gate_up {tuple(gate_up.shape)} and down {tuple(down.shape)} must be [E, 2 I, H] and [E, H, I]")
+        if gate_up.device != down.device:
+            raise ValueError(f"gate_up and down must be on the same device (got {gate_up.device} and {down.device})")
         self.E, self.H, self.I = E, H, rows // 2
         if H % 128 or self.I % 128:
             raise ValueError(f"H and I must be multiples of 128 (got {H}, {self.I})")
