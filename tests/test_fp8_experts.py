@@ -142,7 +142,10 @@ def test_refusals_of_the_product():
             ws=[None, WS + 1], ldx=[255, 264], ldw=[128, 260], wst=[100, 256 * 100 + 8], ldxs=[1], ldws=[1], wsst=[1], off=[None, OFF + 2],
             y=[None, Y + 1], ldy=[99], x_rows=[7], ri=[dict(ri=RI, x_rows=0), dict(ri=RI + 1)])
     refuses(mm, UNS, N=[(1 << 24) + 1], ldx=[(1 << 22) + 16], ldxs=[(1 << 20) + 1], ldws=[dict(ldws=(1 << 20) + 1, wsst=1 << 22)],
-            tiles=[dict(rows=1 << 30, x_rows=1 << 30, N=1 << 24, ldy=1 << 24, wst=1 << 34, wsst=1 << 20)])
+            tiles=[dict(rows=1 << 30, x_rows=1 << 30, N=1 << 24, ldy=1 << 24, wst=1 << 34, wsst=1 << 20),
+                          # (fits as tiles, not as the smaller blocks that few rows per expert run on)
+                          dict(rows=2560, x_rows=2560, N=6 << 20, K=16, ldx=16, ldw=16, ldxs=1, ldws=1, E=256, ldy=6 << 20,
+                               wst=96 << 20, wsst=48 << 10)])
     assert mm(rows=0, x=None) == 0
 
 

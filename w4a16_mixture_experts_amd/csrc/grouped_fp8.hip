@@ -508,6 +508,8 @@ static hipError_t launch_narrow(const Fp8Args& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+static bool few_rows(int rows, int E) { return rows <= 12 * (long long)E; }   // (16 x 32 blocks of two waves; figures below)
+
 // Tiles of bp rows into which the experts' rows fall, on average over their remainders.
 static double mean_tiles(int rows, int E, int bp) { return E > 1 ? (double)rows / bp + 0.5 * (E < rows ? E : rows) : ceil_div(rows, bp); }
 
@@ -534,7 +536,7 @@ static hipError_t launch_fp8(const Fp8Args& a, hipStream_t s) {
   const int E = a.E < a.rows ? a.E : a.rows;
   const long long tiles = (a.rows / 128 + (long long)E) * ceil_div(a.N, 128);
   if (a.far) return launch_tile<ET, Frag, 4, 4, 2, 2, 2, true>(a, s);
-  if (a.rows <= 12 * (long long)a.E) return launch_narrow<ET, Frag, 1, 2, 2>(a, s);
+  if (few_rows(a.rows, a.E)) return launch_narrow<ET, Frag, 1, 2, 2>(a, s);
   if (tiles < 128) return launch_narrow<ET, Frag, 1, 4, 2>(a, s);
   if (tiles < 512 || a.rows <= 48 * (long long)a.E) return launch_tile<ET, Frag, 2, 4, 2, 2, 2>(a, s);
   if constexpr (std::is_same<Frag, FragF8>::value) {
@@ -589,7 +591,7 @@ extern "C" int exmoe_grouped_mm_fp8(const exmoe_grouped_fp8* call, hipStream_t s
   EXMOE_TRY(check_matrix("y", y, ldy, N, ob));
   EXMOE_TRY(check_int32("row_index", row_index, true));
   EXMOE_TRY(check_int32("expert_offsets", expert_offsets, true));
-  if (!tiles_fit(rows, N, E, 64, 128, 256))
+  if (!tiles_fit(rows, N, E, 64, 128, 256) || (few_rows(rows, E) && !tiles_fit(rows, N, E, 16, 32, 128)))
     return set_error(EXMOE_ERR_UNSUPPORTED, "exmoe_grouped_mm_fp8: more output tiles than one launch holds");
   const int xr = row_index ? x_rows : rows;
   const MemRows mx = mem_matrix("x", x, xr, ldx, K, 1), mw = mem_matrices("w", w, E, w_stride, N, ldw, K, 1),
