@@ -142,7 +142,7 @@ def check(l, ids, mask, k, out_dtype=None, label="", ld=0):
 
 @gpu
 @pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
-@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 8, 2), (3, 5, 5), (16, 64, 8), (129, 13, 2), (300, 16, 4), (257, 33, 3), (2000, 64, 8),
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 8, 2), (3, 5, 5), (16, 64, 8), (129, 13, 2), (300, 16, 4), (257, 33, 3), (2000, 64, 8), (512, 64, 8), (513, 64, 8),
                                    (1025, 128, 8), (513, 200, 1), (700, 256, 64)])
 def test_losses_and_gradient(T, E, k, dtype):
     gen = torch.Generator().manual_seed(T + E)

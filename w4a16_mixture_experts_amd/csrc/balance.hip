@@ -137,10 +137,23 @@ struct LaneCols {
   }
 };
 
+// The losses of the sums p(e) of the probabilities, z of lse^2, and the counts n(e), n(E) = M, by one wave.
+template <class P, class N>
+__device__ __forceinline__ void write_losses(const BalanceArgs& a, int lane, double z, P p, N n) {
+  double v = 0.;
+  for (int e = lane; e < a.E; e += 64) v += p(e) * (double)n(e);
+  v = wave_sum(v);
+  const double M = n(a.E);
+  if (lane == 0) {
+    a.losses[0] = M > 0. ? (float)(v * a.E / (M * M * a.k)) : 0.f;
+    a.losses[1] = M > 0. ? (float)(z / M) : 0.f;
+  }
+}
+
 constexpr int kFwdThreads = 1024, kBalThreads = 256;
 constexpr int kBwdRows = 4;   // rows of a lane in the backward pass, loaded together
 
-// LANES lanes per row; a workgroup takes every gridDim.x-th run of rows.
+// LANES lanes per row; a workgroup takes every gridDim.x-th run of rows, and a lone one writes the losses too.
 template <int DT, int LANES>
 __global__ __launch_bounds__(kFwdThreads) void balance_kernel(BalanceArgs a) {
   constexpr int kRows = kFwdThreads / LANES, kE = 8 * LANES;
@@ -192,9 +205,19 @@ __global__ __launch_bounds__(kFwdThreads) void balance_kernel(BalanceArgs a) {
       v += s_p[w][at];
       c += s_n[w][at];
     }
-    a.part[(size_t)blockIdx.x * (a.E + 1) + e] = v;
-    a.part_n[(size_t)blockIdx.x * (a.E + 1) + e] = c;
+    if (gridDim.x > 1) {
+      a.part[(size_t)blockIdx.x * (a.E + 1) + e] = v;
+      a.part_n[(size_t)blockIdx.x * (a.E + 1) + e] = c;
+    } else {
+      s_p[0][at] = v;        // (this thread alone has read the column)
+      s_n[0][at] = c;
+      a.counts[e] = c;
+    }
   }
+  if (gridDim.x > 1) return;
+  __syncthreads();
+  auto at = [&](int e) { return e < a.E ? e : kE; };
+  if (wave == 0) write_losses(a, lane, s_p[0][kE], [&](int e) { return (double)s_p[0][at(e)]; }, [&](int e) { return s_n[0][at(e)]; });
 }
 
 // The sums over the workgroups, and the losses. 64 experts are a wave's columns, and the waves are dealt to the
@@ -229,16 +252,7 @@ __global__ __launch_bounds__(1024) void balance_join_kernel(BalanceArgs a, int b
     if (e <= a.E) a.counts[e] = n;
   }
   __syncthreads();
-  if (wave == 0) {
-    double v = 0.;
-    for (int e = lane; e < a.E; e += 64) v += s_sum[e] * (double)s_cnt[e];
-    v = wave_sum(v);
-    const double M = s_cnt[a.E];
-    if (lane == 0) {
-      a.losses[0] = M > 0. ? (float)(v * a.E / (M * M * a.k)) : 0.f;
-      a.losses[1] = M > 0. ? (float)(s_sum[a.E] / M) : 0.f;
-    }
-  }
+  if (wave == 0) write_losses(a, lane, s_sum[a.E], [&](int e) { return s_sum[e]; }, [&](int e) { return s_cnt[e]; });
 }
 
 template <int DT, int LANES, bool OUT_F32>
@@ -297,12 +311,15 @@ static int lanes_of(int E) {
   while (8 * l < E) l *= 2;
   return l;
 }
-// Workgroups of the forward pass: a row per LANES lanes, at most one per compute unit (what is left of the
-// rows they take in turn). Large workgroups leave few sums to join (8192 tokens of 64 experts, both launches:
-// 7.5 us; with workgroups of 256 threads 8.9; 65536 tokens of 256 experts 25 / 40).
+// Workgroups of the forward pass: a row per LANES lanes, at most one per compute unit (what is left of the rows
+// they take in turn). Large workgroups leave few sums to join (8192 tokens of 64 experts, both launches 7.5 us,
+// with workgroups of 256 threads 9.4; 65536 tokens of 256 experts 25 / 40). Up to four runs of rows are one
+// workgroup's, which needs no second launch (one / several and the join: 128 tokens of 256 experts 5.6 / 6.9 us,
+// 512 of 64 5.2 / 6.7; 1024 of 64, eight runs, 8.2 / 6.9).
+constexpr int kLoneRuns = 4;
 static int balance_blocks(int T, int E) {
   const long long n = ((long long)T * lanes_of(E) + kFwdThreads - 1) / kFwdThreads;
-  return n > 256 ? 256 : (n < 1 ? 1 : (int)n);
+  return n > 256 ? 256 : (n <= kLoneRuns ? 1 : (int)n);
 }
 
 }  // namespace exmoe
@@ -360,7 +377,7 @@ extern "C" int exmoe_balance_loss(const exmoe_balance* call, void* workspace, si
                       EXMOE_LAUNCH(prof, (balance_kernel<decltype(dt)::value, decltype(lanes)::value>), dim3(blocks),
                                    dim3(kFwdThreads), 0, stream, a);
                       const hipError_t e = hipGetLastError();
-                      if (e != hipSuccess) return e;
+                      if (e != hipSuccess || blocks == 1) return e;
                       ProfScope join("balance_join", stream);
                       EXMOE_LAUNCH(join, balance_join_kernel, dim3(1), dim3(1024), 0, stream, a, blocks);
                       return hipGetLastError();
