@@ -480,7 +480,7 @@ def whole_operands(gen, rows, E, N, K):
 PRODUCTS = [([1], 1, 16), ([1], 16, 16), ([1], 128, 128), ([3, 0, 1], 40, 272), ([0, 0, 0, 2], 517, 128), ([16], 256, 2048),
             ([17, 1, 40, 0, 9], 200, 400), ([130], 130, 144), ([200, 3, 64], 384, 640), ([300], 64, 1008), ([515, 257], 256, 256),
             ([1] * 60 + [0] * 4, 48, 256), ([2500], 136, 128), ([40] * 30, 640, 144), ([90, 0, 130, 77] * 4, 4100, 128),
-            ([1200, 3, 900], 6700, 160), ([2049], 6400, 272)]
+            ([1200, 3, 900], 6700, 160), ([2049], 6400, 272), ([5, 0, 3], 200, 2064), ([9, 2, 12, 1], 3100, 4112), ([100, 2, 30], 264, 2320)]
 
 
 @gpu

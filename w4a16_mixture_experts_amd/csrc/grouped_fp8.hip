@@ -508,7 +508,7 @@ static hipError_t launch_narrow(const Fp8Args& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-static bool few_rows(int rows, int E) { return rows <= 12 * (long long)E; }   // (16 x 32 blocks of two waves; figures below)
+static bool few_rows(int rows, int E) { return rows <= 12 * (long long)E; }   // (16 x 32 blocks; figures below)
 
 // Tiles of bp rows into which the experts' rows fall, on average over their remainders.
 static double mean_tiles(int rows, int E, int bp) { return E > 1 ? (double)rows / bp + 0.5 * (E < rows ? E : rows) : ceil_div(rows, bp); }
@@ -528,6 +528,18 @@ static double mean_tiles(int rows, int E, int bp) { return E > 1 ? (double)rows 
 //   4096 x 4096, E = 8,  R = 1024     - / 530 / 225 / 210 / 174 / 187
 //   4096 x 4096, E = 1,  R = 4096     - /   - /  73 /  79 /  89 /  61
 //   14336 x 4096, E = 8, R = 1024     - /   - /   - / 681 / 597 / 544
+// and of the blocks, two waves / four (replayed, weights in turn):
+//   16 x 32: 4096 x 4096, E = 1, R = 1 (128 blocks)     8.9 /  7.6
+//            2048 x 2048, E = 8, 2 rows (128)           6.3 /  5.5
+//            2048 x 1024, E = 8, 8 rows (512)           6.3 /  6.6
+//            2048 x 2048, E = 64, R = 2 (4608)         44.6 / 48.2
+//            2048 x 4096, E = 64, R = 2 (4608)         90.4 / 83.1
+//            4096 x 14336, E = 8, R = 1 (1024)         64.3 / 65.6
+//   16 x 64: 4096 x 4096, E = 1, R = 64 (320)          11.1 /  9.8
+//            2048 x 8192, E = 1, R = 128 (288)         17.1 / 13.4
+//            1024 x 1024, E = 1, R = 256 (272)          5.3 /  5.4
+//            1024 x 4096, E = 4, R = 125 (560)         16.6 / 19.2
+//            4096 x 8192, E = 1, R = 128 (576)         20.3 / 20.7
 // Few rows per expert are bound by reading W; then the number of tiles decides how many compute units work, and
 // then how often the tiles fill them: 192 x 256 tiles take 0.8 of the time of 256 x 256 ones, and the last round
 // of tiles is half full on average (with one expert their number is known).
@@ -536,8 +548,16 @@ static hipError_t launch_fp8(const Fp8Args& a, hipStream_t s) {
   const int E = a.E < a.rows ? a.E : a.rows;
   const long long tiles = (a.rows / 128 + (long long)E) * ceil_div(a.N, 128);
   if (a.far) return launch_tile<ET, Frag, 4, 4, 2, 2, 2, true>(a, s);
-  if (few_rows(a.rows, a.E)) return launch_narrow<ET, Frag, 1, 2, 2>(a, s);
-  if (tiles < 128) return launch_narrow<ET, Frag, 1, 4, 2>(a, s);
+  // (four waves instead of two in a block where a compute unit has few blocks, or a block of few rows many slices)
+  auto few_blocks = [&](int bq) { return a.K >= 2048 && row_tiles(a.rows, a.E, 16) * ceil_div(a.N, bq) <= 384; };
+  if (few_rows(a.rows, a.E)) {
+    if (a.K >= 4096 || few_blocks(32)) return launch_narrow<ET, Frag, 1, 2, 4>(a, s);
+    return launch_narrow<ET, Frag, 1, 2, 2>(a, s);
+  }
+  if (tiles < 128) {
+    if (few_blocks(64)) return launch_narrow<ET, Frag, 1, 4, 4>(a, s);
+    return launch_narrow<ET, Frag, 1, 4, 2>(a, s);
+  }
   if (tiles < 512 || a.rows <= 48 * (long long)a.E) return launch_tile<ET, Frag, 2, 4, 2, 2, 2>(a, s);
   if constexpr (std::is_same<Frag, FragF8>::value) {
     const int qt = ceil_div(a.N, 256);
@@ -591,7 +611,7 @@ extern "C" int exmoe_grouped_mm_fp8(const exmoe_grouped_fp8* call, hipStream_t s
   EXMOE_TRY(check_matrix("y", y, ldy, N, ob));
   EXMOE_TRY(check_int32("row_index", row_index, true));
   EXMOE_TRY(check_int32("expert_offsets", expert_offsets, true));
-  if (!tiles_fit(rows, N, E, 64, 128, 256) || (few_rows(rows, E) && !tiles_fit(rows, N, E, 16, 32, 128)))
+  if (!tiles_fit(rows, N, E, 64, 128, 256) || (few_rows(rows, E) && !tiles_fit(rows, N, E, 16, 32, 256)))
     return set_error(EXMOE_ERR_UNSUPPORTED, "exmoe_grouped_mm_fp8: more output tiles than one launch holds");
   const int xr = row_index ? x_rows : rows;
   const MemRows mx = mem_matrix("x", x, xr, ldx, K, 1), mw = mem_matrices("w", w, E, w_stride, N, ldw, K, 1),
