@@ -1,6 +1,7 @@
 // An expert layer in 8 bits behind its norm, of this library's own calls: the residual's addition and
 // norm (16 bits for the router, 8 for the experts), routing, grouping, gate and up, silu(gate) * up with the
-// routing weights in its scales, down, and the sum of each token's rows, gfx950.
+// routing weights in its scales, down, and the sum of each token's rows, gfx950. Of 257 us of 2048 tokens (2048
+// wide, 1024 inside, 64 experts, top-8) the two products take about 195 (traced), of 100 us of 16 tokens 70.
 #include "checks.h"
 #include "exmoe.h"
 #include "fp8.h"
@@ -10,7 +11,8 @@
 namespace exmoe {
 
 // y[t, :] = sum_j rows[flat_to_sorted[t k + j], :] in slot order, fp32 sums of the bf16 rows, rounded once.
-// One thread per 8 columns, the loads of 8 rows in flight. (Rows outside [0, n) add nothing.)
+// One thread per 8 columns, the loads of 8 rows in flight: bound by memory (2048 tokens of 8 rows of 2048, 75 MB,
+// 22 us, 3.4 TB/s: each load waits for an index first; 16 tokens 5 us, the latency of the two). (Rows outside [0, n) add nothing.)
 __global__ __launch_bounds__(256) void row_sum_kernel(const uint16_t* __restrict__ rows, const int32_t* __restrict__ f2s, int n,
                                                       int T, int H, int k, uint16_t* __restrict__ y) {
   const int per = H / 8;
