@@ -1,6 +1,6 @@
 // An expert layer in 8 bits behind its norm, of this library's own calls: the residual's addition and
 // norm (16 bits for the router, 8 for the experts), routing, grouping, gate and up, silu(gate) * up with the
-// routing weights in its scales, down, and the sum of each token's rows, gfx950. Of 257 us of 2048 tokens (2048
+// routing weights in its scales, down, and the sum of each token's rows, gfx950. Of 252 us of 2048 tokens (2048
 // wide, 1024 inside, 64 experts, top-8) the two products take about 195 (traced), of 100 us of 16 tokens 70.
 #include "checks.h"
 #include "exmoe.h"
@@ -11,14 +11,15 @@
 namespace exmoe {
 
 // y[t, :] = sum_j rows[flat_to_sorted[t k + j], :] in slot order, fp32 sums of the bf16 rows, rounded once.
-// One thread per 8 columns, the loads of 8 rows in flight: bound by memory (2048 tokens of 8 rows of 2048, 75 MB,
-// 22 us, 3.4 TB/s: each load waits for an index first; 16 tokens 5 us, the latency of the two). (Rows outside [0, n) add nothing.)
+// One thread per 8 columns, a workgroup within one token, so that the indices of its rows are scalar loads; the
+// loads of 8 rows in flight. Bound by memory (2048 tokens of 8 rows of 2048, 75 MB, 18.6 us, 4.1 TB/s: each
+// workgroup's rows wait for its indices; threads numbered over all tokens' columns 22.0), for 16 tokens by the
+// latency of the two loads (5 us). (Rows outside [0, n) add nothing.)
 __global__ __launch_bounds__(256) void row_sum_kernel(const uint16_t* __restrict__ rows, const int32_t* __restrict__ f2s, int n,
-                                                      int T, int H, int k, uint16_t* __restrict__ y) {
-  const int per = H / 8;
-  const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= (size_t)T * per) return;
-  const int t = (int)(i / per), c = 8 * (int)(i - (size_t)t * per);
+                                                      int H, int k, uint16_t* __restrict__ y) {
+  const int parts = (H / 8 + (int)blockDim.x - 1) / (int)blockDim.x, t = (int)blockIdx.x / parts;
+  const int c = 8 * (((int)blockIdx.x - t * parts) * (int)blockDim.x + (int)threadIdx.x);
+  if (c >= H) return;
   f32x8 sum = {0, 0, 0, 0, 0, 0, 0, 0};
   for (int j0 = 0; j0 < k; j0 += 8) {
     f32x8 v[8];
@@ -70,7 +71,7 @@ static int check_layer(int T, int H, int I, int E, int k) {
   if (H > kMaxDim || I > kMaxDim) return set_error(EXMOE_ERR_UNSUPPORTED, "H and I must be <= %d", kMaxDim);
   // (what the product's tiles, the quantised rows and the sums hold in one launch)
   if (T >= 1 << 22 || (long long)T * k > (1 << 24) || !tiles_fit(T * k, 2 * I > H ? 2 * I : H, E, 64, 128, 256) ||
-      (long long)T * k * (I / 128) > (kMaxThreads / 256) * 16 || (long long)T * (H / 8) > kMaxThreads)
+      (long long)T * k * (I / 128) > (kMaxThreads / 256) * 16 || (long long)T * (H / 8 + 255) > kMaxThreads)
     return set_error(EXMOE_ERR_UNSUPPORTED, "T*k, or T with this H, too large");
   return EXMOE_OK;
 }
@@ -145,7 +146,8 @@ extern "C" int exmoe_moe_layer_fp8(const exmoe_layer_fp8* call, void* workspace,
   mm.ldy = H; mm.N = H; mm.K = I;
   EXMOE_TRY(exmoe_grouped_mm_fp8(&mm, stream));
   ProfScope prof("row_sum", stream);
-  EXMOE_LAUNCH(prof, row_sum_kernel, dim3((unsigned)(((size_t)T * (H / 8) + 255) / 256)), dim3(256), 0, stream,
-               reinterpret_cast<const uint16_t*>(ws + part.rows), c.flat_to_sorted, (int)n, T, H, k, c.y);
+  const int threads = H >= 2048 ? 256 : ceil_div(H, 512) * 64;   // (whole waves of 512 columns)
+  EXMOE_LAUNCH(prof, row_sum_kernel, dim3((unsigned)(T * ceil_div(H / 8, threads))), dim3(threads), 0, stream,
+               reinterpret_cast<const uint16_t*>(ws + part.rows), c.flat_to_sorted, (int)n, H, k, c.y);
   return launched(hipGetLastError(), "exmoe_moe_layer_fp8");
 }
