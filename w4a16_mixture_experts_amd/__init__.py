@@ -678,6 +678,8 @@ def _f8_outputs(q, scale, rows: int, K: int, dev: int, like):
     torch = _TORCH or _torch()
     if q is None:
         q = like.new_empty((rows, (K + 15) // 16 * 16), dtype=torch.float8_e4m3fn)[:, :K]
+    elif q.requires_grad:
+        _no_gradient()
     if scale is None:
         scale = like.new_empty((rows, (K + 127) // 128), dtype=torch.float32)
     elif scale.requires_grad:
@@ -775,7 +777,7 @@ def swiglu_fp8(gate_up, weights=None, row_index=None, q=None, scale=None):
 def quantize_fp8_weights(w, q=None, scale=None):
     """(q, scale) of w [E, N, K] (bf16, fp16 or fp32): e4m3 with a scale per 128 x 128 block, scale
     fp32 [E, ceil(N / 128), ceil(K / 128)]."""
-    if w.requires_grad or scale is not None and scale.requires_grad:
+    if w.requires_grad or q is not None and q.requires_grad or scale is not None and scale.requires_grad:
         _no_gradient()
     torch = _torch()
     dev, dtype = _on_gpu("w", w), w.dtype
