@@ -874,10 +874,16 @@ def moe_layer_fp8(x, w_norm, w_router, experts: Fp8Experts, k: int, residual=Non
     torch = _torch()
     dev, bf16 = _on_gpu("x", x), torch.bfloat16
     T, H = _axes("x", x, 2)
-    E, I = experts.E, experts.I
+    E, I, f8, f32 = experts.E, experts.I, torch.float8_e4m3fn, torch.float32
+    held = experts.gate_up, experts.gate_up_scale, experts.down, experts.down_scale   # (a program may have put others there)
+    if any(t.requires_grad for t in held):
+        _no_gradient()
     for name, t, shape, dtype in (("x", x, (T, experts.H), bf16), ("w_norm", w_norm, (H,), bf16), ("w_router", w_router, (E, H), bf16),
-                                  ("residual", residual, (T, H), bf16), ("bias", bias, (E,), torch.float32),
-                                  ("experts", experts.gate_up, (E, 2 * I, H), torch.float8_e4m3fn)):
+                                  ("residual", residual, (T, H), bf16), ("bias", bias, (E,), f32),
+                                  ("experts.gate_up", held[0], (E, 2 * I, H), f8),
+                                  ("experts.gate_up_scale", held[1], (E, 2 * I // 128, H // 128), f32),
+                                  ("experts.down", held[2], (E, H, I), f8),
+                                  ("experts.down_scale", held[3], (E, H // 128, I // 128), f32)):
         if t is not None and (t.shape != shape or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous()):
             raise ValueError(f"{name} must be a contiguous {tuple(shape)} {dtype} tensor on GPU {dev} (got {tuple(t.shape)} {t.dtype})")
     b = buffers or Fp8LayerBuffers(T, H, I, E, k, x.device)
@@ -885,8 +891,7 @@ def moe_layer_fp8(x, w_norm, w_router, experts: Fp8Experts, k: int, residual=Non
         raise ValueError(f"buffers are of another call: {(b.T, b.H, b.I, b.E, b.k)}, not {(T, H, I, E, k)} on GPU {dev}")
     _run_on(dev, _lib.exmoe_moe_layer_fp8,
             _LAYER_FP8.pack(x.data_ptr(), w_norm.data_ptr(), _ptr(residual) or 0, w_router.data_ptr(), _ptr(bias) or 0,
-                            experts.gate_up.data_ptr(), experts.gate_up_scale.data_ptr(), experts.down.data_ptr(),
-                            experts.down_scale.data_ptr(), b.logits.data_ptr(), b.ids.data_ptr(), b.weights.data_ptr(),
+                            *(t.data_ptr() for t in held), b.logits.data_ptr(), b.ids.data_ptr(), b.weights.data_ptr(),
                             b.offsets.data_ptr(), b.sorted_flat.data_ptr(), b.flat_to_sorted.data_ptr(), b.y.data_ptr(), eps, T, H, I,
                             E, k, int(renormalize)), b.workspace.data_ptr(), b.workspace.numel())
     return b
