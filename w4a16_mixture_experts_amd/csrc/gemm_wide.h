@@ -79,11 +79,6 @@ struct WideRows {
 #pragma unroll
     for (int i = 0; i < kSlots; i++) buf_copy16(buf, lds + (i * NW + wave) * kRows * D, in ? voff[i] : kNowhere, soff);
   }
-  __device__ __forceinline__ void stage_slot(uint16_t* lds, int k0, int i) const {
-    const bool in = k0 + chunk < red;
-    const uint32_t soff = k0 < red ? 2 * (uint32_t)k0 : 0;
-    buf_copy16(buf, lds + (i * NW + wave) * kRows * D, in ? voff[i] : kNowhere, soff);
-  }
   // rows r0..r0+31, summed positions 16 ks + 8 (lane / 32) + 0..7 of the slice
   static __device__ __forceinline__ bf16x8 frag(const uint16_t* lds, int r0, int ks, int lane) {
     const int row = r0 + (lane & 31);

@@ -126,7 +126,7 @@ extern "C" int exmoe_moe_layer_fp8(const exmoe_layer_fp8* call, void* workspace,
   uint16_t* x16 = reinterpret_cast<uint16_t*>(ws + part.x16);
   exmoe_norm nm{};
   nm.x = c.x; nm.w = c.w_norm; nm.residual = nm.residual_out = c.residual; nm.y = x16; nm.q = x8; nm.scale = xs;
-  nm.residual_out = c.residual; nm.ldx = nm.ldr = nm.ldro = nm.ldy = nm.ldq = H; nm.lds = kh; nm.eps = c.eps; nm.T = T; nm.H = H;
+  nm.ldx = nm.ldr = nm.ldro = nm.ldy = nm.ldq = H; nm.lds = kh; nm.eps = c.eps; nm.T = T; nm.H = H;
   EXMOE_TRY(exmoe_rms_norm(&nm, stream));
   EXMOE_TRY(exmoe_route_topk(x16, c.w_router, c.logit_bias, T, H, E, k, c.renormalize, c.logits, c.topk_ids, c.topk_weights, stream));
   EXMOE_TRY(exmoe_group_tokens(c.topk_ids, T, k, E, c.expert_offsets, c.sorted_flat, c.flat_to_sorted, ws + part.group,
