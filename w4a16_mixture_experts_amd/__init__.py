@@ -739,15 +739,25 @@ def rms_norm(x, w, eps: float = 1e-6, residual=None, out: str = "y", y=None, q=N
     return NormOutputs(y, q, scale, residual_out)
 
 
-def quantize_fp8(x, q=None, scale=None):
-    """(q, scale) of x [rows, K] (bf16, fp16 or fp32): e4m3 with a scale per 128 columns of a row."""
-    if x.requires_grad:
+def _row_weights(weights, dev: int):
+    """(pointer, number) of the rows' weights."""
+    if weights.dtype is not _torch().float32 or weights.get_device() != dev or not weights.is_contiguous():
+        raise ValueError(f"weights must be a contiguous float32 tensor on GPU {dev}")
+    return weights.data_ptr(), weights.numel()
+
+
+def quantize_fp8(x, q=None, scale=None, weights=None, row_index=None):
+    """(q, scale) of x [rows, K] (bf16, fp16 or fp32): e4m3 with a scale per 128 columns of a row; weights
+    and row_index as in swiglu_fp8."""
+    if x.requires_grad or weights is not None and weights.requires_grad:
         _no_gradient()
     dev, dtype = _on_gpu("x", x), x.dtype
     rows, K = shape = _axes("x", x, 2)
     px, ldx = _mat("x", x, shape, dtype, dev)
+    pw, n = (0, 0) if weights is None else _row_weights(weights, dev)
+    pi = 0 if row_index is None else _int32("row_index", row_index, dev, rows)
     q, scale, f8 = _f8_outputs(q, scale, rows, K, dev, x)
-    _run_on(dev, _lib.exmoe_quantize_fp8, _FP8_ROWS.pack(px, ldx, 0, 0, *f8, 0, rows, K, _dtype_code(dtype)))
+    _run_on(dev, _lib.exmoe_quantize_fp8, _FP8_ROWS.pack(px, ldx, pw, pi, *f8, n, rows, K, _dtype_code(dtype)))
     return q, scale
 
 
@@ -762,11 +772,7 @@ def swiglu_fp8(gate_up, weights=None, row_index=None, q=None, scale=None):
     px, ldx = _mat("gate_up", gate_up, shape, dtype, dev)
     if cols % 2:
         raise ValueError(f"gate_up has {cols} columns: gate and up side by side are an even number")
-    pw = n = 0
-    if weights is not None:
-        if weights.dtype is not _torch().float32 or weights.get_device() != dev or not weights.is_contiguous():
-            raise ValueError(f"weights must be a contiguous float32 tensor on GPU {dev}")
-        pw, n = weights.data_ptr(), weights.numel()
+    pw, n = (0, 0) if weights is None else _row_weights(weights, dev)
     I = cols // 2
     q, scale, f8 = _f8_outputs(q, scale, rows, I, dev, gate_up)
     _run_on(dev, _lib.exmoe_swiglu_fp8, _FP8_ROWS.pack(px, ldx, pw, _int32("row_index", row_index, dev, rows) or 0, *f8, n, rows,
