@@ -439,11 +439,11 @@ int exmoe_lora_linear(const void* x, size_t ldx, const void* w, size_t ldw, cons
 /* ------------------------------------------------------------------------------------
  * The experts in 8 bits (device, asynchronous): activations and weights as e4m3 (OCP 8-bit
  * floating point: 4 exponent bits, 3 of the fraction, largest 448, no infinities) with an fp32
- * scale per 128 neighbours, for experts that are neither int4 nor 16-bit: half the weight bytes
- * and twice the matrix rate of bf16. An expert layer of them is exmoe_rms_norm (16 bits for the
- * router, 8 for the experts), exmoe_route_topk, exmoe_group_tokens, exmoe_grouped_mm_fp8 on gate
- * and up, exmoe_swiglu_fp8 with the routing weights, exmoe_grouped_mm_fp8 on down, and the sum of
- * each token's rows.
+ * scale per 128 neighbours, for experts that are neither int4 nor 16-bit: half the weight bytes of
+ * bf16, on matrix instructions of twice its rate (exmoe_grouped_mm takes 1.5 to 1.6 times as long for
+ * prompts). An expert layer of them is exmoe_rms_norm (16 bits for the router, 8 for the experts),
+ * exmoe_route_topk, exmoe_group_tokens, exmoe_grouped_mm_fp8 on gate and up, exmoe_swiglu_fp8 with the
+ * routing weights, exmoe_grouped_mm_fp8 on down, and the sum of each token's rows.
  *   scale = max(largest |v| of the 128 / 448, 2^-126), q = e4m3(v / scale) to nearest even (the
  *   quotient as v * (1 / scale) in fp32). A NaN among the 128 makes the scale NaN, an infinity
  *   makes it infinite; the group's values are then NaN by IEEE arithmetic.
@@ -478,10 +478,13 @@ int exmoe_lora_linear(const void* x, size_t ldx, const void* w, size_t ldw, cons
  * NULL with E = 1 (one matrix for all rows). K is a multiple of 16; rows of x and w are 16-byte
  * aligned (base, ld and w_stride), ld <= 2^22 (of scales: 2^20); y any alignment, out_dtype bf16, fp16 or fp32. What
  * x and w hold between K and ld is not read. Each block of 128 positions is
- * summed by the matrix unit and scaled into an fp32 sum. Its 8-bit adders drop what lies below
- * 2^-13 of the largest of 8 neighbouring products: for 16-bit outputs that is a tenth of their
- * rounding or less; 32-bit outputs take products and sums that lose nothing but fp32 roundings, at
- * half the rate. Products of two scales under 2^-126 lose bits. No workspace.
+ * summed by the matrix unit and scaled into an fp32 sum. Its 8-bit adders drop from each product what
+ * lies below 2^-13 of the largest of 8 neighbouring ones: a 16-bit output may be off by 7 2^-13 of the
+ * largest product of every 8 beside its rounding, which is more than the result itself where large
+ * products cancel. (On normal values it is 1.6e-5 of the outputs' norm, beside 1.7e-3 of bf16's
+ * rounding and 2.1e-4 of fp16's.) 32-bit outputs take products and sums that lose nothing but fp32
+ * roundings, at half the rate. Products of two scales under 2^-126 lose bits, and over 2^128 they are
+ * infinite. No workspace.
  * ---------------------------------------------------------------------------------- */
 typedef struct exmoe_norm {
   const void* x;

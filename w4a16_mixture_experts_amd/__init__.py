@@ -807,7 +807,8 @@ def grouped_mm_fp8(x, x_scale, w, w_scale, offsets=None, row_index=None, row_div
     x_scale fp32 [x_rows, ceil(K / 128)], w_scale fp32 [E, ceil(N / 128), ceil(K / 128)]; offsets,
     row_index and row_div as in grouped_mm, offsets None for one expert with every row. Returns y
     [rows, N] in out_dtype (bf16, the default, fp16 or fp32); rows outside every segment are left
-    as they are."""
+    as they are. 16-bit outputs may lose small products beside large ones of the same 8 positions
+    (7 x 2^-13 of the largest one of them), 32-bit outputs lose none."""
     if (x.requires_grad or w.requires_grad or x_scale.requires_grad or w_scale.requires_grad
             or y is not None and y.requires_grad):
         _no_gradient()
