@@ -551,7 +551,9 @@ int exmoe_grouped_mm_fp8(const exmoe_grouped_fp8* call, hipStream_t stream);
  * place; NULL: no residual), norm of it by w_norm, exmoe_route_topk of the 16-bit norm (whose rules hold
  * for w_router, logit_bias, k and renormalize), exmoe_group_tokens, gate and up of the 8-bit norm, exmoe_swiglu_fp8
  * with the routing weights, down, and y[t] = the sum of token t's k rows in slot order (bf16 rows, fp32
- * sums). Every result is that of the separate calls, bit for bit.
+ * sums). Every result is that of the separate calls, bit for bit. Gate and up and the rows pass between them as bf16:
+ * the rows' roundings are 0.17% of y's norm, as y's own are, beside 4.3% of the 8-bit activations; with
+ * exmoe_grouped_mm_fp8 called for fp32 rows they are none.
  * x, y, residual bf16 [T, H]; w_norm bf16 [H]; w_router bf16 [E, H]; gate_up e4m3 [E, 2 I, H], gate's rows
  * first, its scales [E, 2 I / 128, H / 128]; down e4m3 [E, H, I], its scales [E, H / 128, I / 128]; logits bf16
  * [T, E]; the routing and grouping outputs of the calls named. All contiguous and 16-byte aligned; no output

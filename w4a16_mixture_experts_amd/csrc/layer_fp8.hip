@@ -2,6 +2,12 @@
 // norm (16 bits for the router, 8 for the experts), routing, grouping, gate and up, silu(gate) * up with the
 // routing weights in its scales, down, and the sum of each token's rows, gfx950. Of 252 us of 2048 tokens (2048
 // wide, 1024 inside, 64 experts, top-8) the two products take about 195 (traced), of 100 us of 16 tokens 70.
+//
+// Gate and up and the down rows pass between the calls as bf16, half the bytes of fp32 and 8-bit products at full rate
+// (fp32 outputs take half); the int4 layers keep both in fp32. Of the result's norm (64 tokens at these sizes,
+// against 64 bits): 4.299% with bf16 rows, 4.297% with fp32 rows, 4.305% with fp32 gate and up too: the 8-bit
+// activations decide. The bf16 rows alone are 0.17%, as much as the rounding of y itself. A caller who needs fp32 rows
+// makes the calls one by one.
 #include "checks.h"
 #include "exmoe.h"
 #include "fp8.h"
