@@ -10,7 +10,7 @@ from test_layer_fp8 import BF16, by_its_calls, operands, same  # noqa: E402
 
 gpu = pytest.mark.gpu
 # T, H, I, E, k and the forms of gate and up and of down
-PROMPTS = [(400, 512, 1280, 16, 4, (128, 128), (16, 64, 2)), (4096, 1024, 512, 4, 4, (192, 256), (192, 256)), (2048, 256, 3200, 1, 1, (256, 256), (16, 64, 4))]
+PROMPTS = [(400, 512, 1280, 16, 4, (128, 128), (16, 64, 2)), (4096, 1024, 512, 4, 4, (192, 256), (192, 256)), (2048, 256, 3200, 1, 1, (256, 256), (16, 64, 2))]
 
 
 def test_the_listed_sizes_reach_their_forms():
