@@ -440,7 +440,7 @@ int exmoe_lora_linear(const void* x, size_t ldx, const void* w, size_t ldw, cons
  * The experts in 8 bits (device, asynchronous): activations and weights as e4m3 (OCP 8-bit
  * floating point: 4 exponent bits, 3 of the fraction, largest 448, no infinities) with an fp32
  * scale per 128 neighbours, for experts that are neither int4 nor 16-bit: half the weight bytes of
- * bf16, on matrix instructions of twice its rate (exmoe_grouped_mm takes 1.5 to 1.6 times as long for
+ * bf16, on matrix instructions of twice its rate (exmoe_grouped_mm takes 1.6 times as long for
  * prompts). An expert layer of them is exmoe_rms_norm (16 bits for the router, 8 for the experts),
  * exmoe_route_topk, exmoe_group_tokens, exmoe_grouped_mm_fp8 on gate and up, exmoe_swiglu_fp8 with the
  * routing weights, exmoe_grouped_mm_fp8 on down, and the sum of each token's rows.

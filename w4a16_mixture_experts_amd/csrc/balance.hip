@@ -327,9 +327,10 @@ static int lanes_of(int E) {
 }
 // Workgroups of the forward pass: a row per LANES lanes, at most one per compute unit (what is left of the rows
 // they take in turn). Large workgroups leave few sums to join (8192 tokens of 64 experts, both launches 7.5 us,
-// with workgroups of 256 threads 9.4; 65536 tokens of 256 experts 25 / 40). Up to four runs of rows are one
-// workgroup's, which needs no second launch (one / several and the join: 128 tokens of 256 experts 5.6 / 6.9 us,
-// 512 of 64 5.2 / 6.7; 1024 of 64, eight runs, 8.2 / 6.9).
+// with workgroups of 256 threads 9.4; 65536 tokens of 256 experts 25 / 40: 15 in this kernel, 10 in the join). Up to four
+// runs of rows are one workgroup's, which needs no second launch (one / several and the join, replayed: 256 tokens of
+// 64 experts, two runs, 5.2 / 6.7 us, 512 of 64, four, 7.0 / 6.7, 128 of 256, four, 7.6 / 7.1, 1024 of 64, eight, 10.9 /
+// 6.9; a call of its own, whose second launch takes the host 3 us: 6.9 / 10.2, 7.2 / 10.2, 7.5 / 10.0).
 constexpr int kLoneRuns = 4;
 static int balance_blocks(int T, int E) {
   const long long n = ((long long)T * lanes_of(E) + kFwdThreads - 1) / kFwdThreads;

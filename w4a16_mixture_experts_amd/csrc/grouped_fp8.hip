@@ -151,12 +151,16 @@ struct FarRows {
 // first fragments of the next are read between those products.
 // Row blocks are dealt to the WP wave rows in turn, and blocks past the tile's rows are skipped.
 //
-// What bounds it. 256 x 256 tiles, 8192 x 8192 x 8192: 487 us, 2.26 PFLOP/s (the installed BLAS, without block
+// What bounds it. 256 x 256 tiles, 8192 x 8192 x 8192: 486 us, 2.26 PFLOP/s (the installed BLAS, without block
 // scales, 403); the matrix unit is busy 44% of the cycles of the compute units. Per slice
 // and compute unit the LDS moves 256 KB (192 KB read as fragments, 64 KB written by the copies), 2048 cycles
-// at 128 bytes each, as many as the products take, so both together set the pace. With parts left out, an
+// at 128 bytes each, as many as the products take. Either alone would allow twice the rate: they take turns instead
+// of running side by side, since the waves of a SIMD leave the barrier together. That is this schedule, not a floor.
+// With parts left out, an
 // earlier state of 519 us took 487 without the scaling, 477 with copies that always hit the L2, 372-400 without
 // copies, 312 without copies and scaling, 323 without copies and barrier; the products alone are 250 at 2.1 GHz.
+// Few tiles of few slices (512 x 4096 x 4096: one 64 x 128 tile of 32 slices a compute unit, 33 us) wait for memory
+// once per slice, 1 us: only one slice is ahead.
 // Measured and dropped, against 488: 32 x 32 x 64 instructions (589), one wave per SIMD with 256 x 192 outputs
 // (703: the sums do not fit beside what vector instructions can address, and move to and fro), the next columns'
 // fragments read ahead (spills), 128 x 128 tiles of eight waves (746) or four (649), raised priority around the
@@ -515,33 +519,35 @@ static bool few_rows(int rows, int E) { return rows <= 12 * (long long)E; }   //
 // Tiles of bp rows into which the experts' rows fall, on average over their remainders.
 static double mean_tiles(int rows, int E, int bp) { return E > 1 ? (double)rows / bp + 0.5 * (E < rows ? E : rows) : ceil_div(rows, bp); }
 
-// Form of the call. Measured, us (bf16 out; forms: 16 x 32 blocks / 16 x 64 blocks / 64 x 128 tiles / 128 x 128 /
-// 192 x 256 / 256 x 256), N x K and E experts of R rows on average:
-//   2048 x 2048, E = 64, R = 2       44 /  45 /  55 /  55 /   - /   -
-//                        R = 8       55 /  55 /   - /  59 /   - /   -
-//                        R = 16      63 /  60 /  57 /  57 /  62 /  64
-//                        R = 32      88 /  79 /  58 /  60 /  64 /  66
-//                        R = 64     134 / 116 /  69 /  64 /  67 /  68
-//                        R = 256 (skewed)  - / 350 / 155 / 142 / 125 / 133
-//   1024 x 2048, E = 4,  R = 125     11 /  10 /  14 /  18 /  23 /  24
-//   4096 x 4096, E = 1,  R = 128      - /  13 /  25 /  30 /  38 /  41
-//                        R = 512     47 /  38 /  27 /  31 /  43 /  48
-//   2048 x 2048, E = 1,  R = 2048    51 /  43 /  17 /  19 /  25 /  28
-//   4096 x 4096, E = 8,  R = 1024     - / 530 / 225 / 210 / 174 / 187
-//   4096 x 4096, E = 1,  R = 4096     - /   - /  73 /  79 /  89 /  61
-//   14336 x 4096, E = 8, R = 1024     - /   - /   - / 681 / 597 / 544
-// and of the blocks, two waves / four (replayed, weights in turn):
-//   16 x 32: 4096 x 4096, E = 1, R = 1 (128 blocks)     8.9 /  7.6
-//            2048 x 2048, E = 8, 2 rows (128)           6.3 /  5.5
-//            2048 x 1024, E = 8, 8 rows (512)           6.3 /  6.6
-//            2048 x 2048, E = 64, R = 2 (4608)         44.6 / 48.2
-//            2048 x 4096, E = 64, R = 2 (4608)         90.4 / 83.1
-//            4096 x 14336, E = 8, R = 1 (1024)         64.3 / 65.6
-//   16 x 64: 4096 x 4096, E = 1, R = 64 (320)          11.1 /  9.8
-//            2048 x 8192, E = 1, R = 128 (288)         17.1 / 13.4
-//            1024 x 1024, E = 1, R = 256 (272)          5.3 /  5.4
-//            1024 x 4096, E = 4, R = 125 (560)         16.6 / 19.2
-//            4096 x 8192, E = 1, R = 128 (576)         20.3 / 20.7
+// Form of the call. Measured, us (bf16 out, replayed, 512 MB of weights in turn; forms: 16 x 32 blocks / 16 x 64
+// blocks / 64 x 128 tiles / 128 x 128 / 192 x 256 / 256 x 256), N x K and E experts of R rows on average:
+//   2048 x 2048, E = 64, R = 2       45 /  46 /  53 /  53 /   - /   -
+//                        R = 8       56 /  56 /  56 /  58 /   - /   -
+//                        R = 16      64 /  60 /  58 /  58 /  63 /  65
+//                        R = 32      88 /  80 /  59 /  61 /  65 /  67
+//                        R = 64     135 / 116 /  69 /  64 /  67 /  68
+//                        R = 256 (skewed)  - / 351 / 151 / 138 / 122 / 132
+//   1024 x 2048, E = 4,  R = 125     11 /  11 /  19 /  22 /  28 /  29
+//   4096 x 4096, E = 1,  R = 128      - /  16 /  33 /  39 /  53 /  56
+//                        R = 512     51 /  44 /  33 /  38 /  56 /  66
+//   2048 x 2048, E = 1,  R = 2048    51 /  44 /  19 /  21 /  29 /  29
+//   4096 x 4096, E = 8,  R = 1024     - / 530 / 222 / 205 / 173 / 188
+//   4096 x 4096, E = 1,  R = 4096     - /   - / 106 /  89 /  97 /  69
+//   14336 x 4096, E = 8, R = 1024     - /   - /   - / 675 / 600 / 539
+//   8192 x 8192, E = 1,  R = 8192     - /   - /   - / 643 / 554 / 486
+// (fp32 out, 14336 x 4096, E = 8, R = 1024: 64 x 128 1262, 128 x 128 964) and of the blocks, two waves / four:
+//   16 x 32: 4096 x 4096, E = 1, R = 1 (128 blocks)    10.9 /  8.8
+//            2048 x 2048, E = 8, 2 rows (128)           6.7 /  6.1
+//            2048 x 1024, E = 8, 8 rows (512)           6.6 /  6.6
+//            2048 x 2048, E = 64, R = 2 (4608)         44.7 / 48.4
+//            2048 x 4096, E = 64, R = 2 (4608)         90.3 / 82.9
+//            4096 x 14336, E = 8, R = 1 (1024)         59.1 / 60.3
+//   16 x 64: 4096 x 4096, E = 1, R = 64 (320)          13.7 / 11.6
+//            2048 x 8192, E = 1, R = 128 (288)         21.6 / 16.5
+//            1024 x 1024, E = 1, R = 256 (272)          5.8 /  5.8
+//            1024 x 4096, E = 4, R = 125 (560)         16.5 / 16.7
+//            4096 x 8192, E = 1, R = 128 (576)         27.1 / 26.6
+// (K >= 4096 with few rows takes four waves throughout, 2% the worse for 4096 x 14336.)
 // Few rows per expert are bound by reading W; then the number of tiles decides how many compute units work, and
 // then how often the tiles fill them: 192 x 256 tiles take 0.8 of the time of 256 x 256 ones, and the last round
 // of tiles is half full on average (with one expert their number is known).

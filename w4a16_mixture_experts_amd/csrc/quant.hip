@@ -6,7 +6,8 @@
 //             product is linear, so a weight in the scale of its input weights its output
 //   matrices  scales per 128 x 128 block
 // Both are bound by memory: each element is read and written once (gate and up of 16384 rows, 84 MB, in 15 us,
-// 5.5 TB/s; 128 rows in 2.6 us, the latency of one load and one store).
+// 5.5 TB/s; 128 rows in 2.6 us, the latency of one load and one store; weights of 64 experts of 2048 x 2048 in bf16,
+// 805 MB, in 161 us, 5.0 TB/s, 8 of 14336 x 4096 255, 5.5 TB/s, from fp32 418, 5.6 TB/s).
 #include "checks.h"
 #include "exmoe.h"
 #include "fp8.h"
