@@ -459,8 +459,9 @@ int exmoe_lora_linear(const void* x, size_t ldx, const void* w, size_t ldw, cons
  * exmoe_rms_norm, rows t < T of H <= 16384 columns:
  *   h = x + residual in fp32, rounded to the residual's type into residual_out (it may be the
  *       residual itself, same stride), or h = x without a residual (both NULL)
- *   y = h / sqrt(mean(h^2) + eps) * w in fp32, rounded once into y (x's type; NULL: not
- *       written), and q, scale of the fp32 value (both NULL: not written)
+ *   y = h / sqrt(mean(h^2) + eps) * w in fp32 (also where h^2 leaves its range: such rows are
+ *       scaled by a power of two first), rounded once into y (x's type; NULL: not written),
+ *       and q, scale of the fp32 value (both NULL: not written)
  * w is x's type or fp32 (w_dtype), so is the residual (res_dtype; what is stored is what is
  * normed). T < 2^22.
  *

@@ -3,7 +3,8 @@
 //
 //   h = x + residual rounded to the residual's type (what is stored is what is normed), or x
 //   y[i] = h[i] / sqrt(mean(h^2) + eps) * w[i]
-// in fp32; y is rounded once to x's type, and q is made of the fp32 value, not of the rounded y.
+// in fp32; y is rounded once to x's type, and q is made of the fp32 value, not of the rounded y. Rows whose squares
+// leave the range of 32 bits are scaled by a power of two first.
 // Bound by memory: a row is read once, held in registers between the sum of its squares and its
 // outputs, and written once (4096 x 4096, 152 MB, 25 us where the inputs are in the memory-side cache, 30 us where
 // not: 5.1 TB/s, the rate of a copy).
@@ -70,24 +71,51 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) void rms_norm_kernel
     if (a.res_f32) add(std::integral_constant<int, EXMOE_DTYPE_FP32>{});
     else add(std::integral_constant<int, DT>{});
   }
-  float sum = 0.f;
+  __shared__ float s_sum[2][WAVES];
+  auto squares = [&](int pass) __attribute__((always_inline)) {   // their sum over the row, in all of its lanes
+    float sum = 0.f;
 #pragma unroll
-  for (int j = 0; j < CH; j++) {
-    float s = 0.f;
+    for (int j = 0; j < CH; j++) {
+      float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; i++) s += h[j][i] * h[j][i];
-    sum += s;
+      for (int i = 0; i < 8; i++) s += h[j][i] * h[j][i];
+      sum += s;
+    }
+    sum = wave_sum_f32(sum);
+    if constexpr (WAVES > 1) {
+      if ((t & 63) == 0) s_sum[pass][t / 64] = sum;
+      __syncthreads();
+      sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < WAVES; w++) sum += s_sum[pass][w];
+    }
+    return sum;
+  };
+  float mean = squares(0) / (float)a.H + a.eps;
+  if (!(mean >= 0x1p-80f && mean <= 0x1p100f)) {   // (uniform over the row)
+    // Squares may have left the range of 32 bits: again with the row scaled by a power of two that brings the larger
+    // of its largest |h| and sqrt(eps) to 2^31 (or as near as a normal power does), eps by its square. An
+    // infinity or NaN stays as it is.
+    uint32_t top = 0;
+#pragma unroll
+    for (int j = 0; j < CH; j++) top = max(top, abs_bits8(h[j]));
+    top = wave_max_u32(top);
+    if constexpr (WAVES > 1) {
+      __shared__ uint32_t s_top[WAVES];
+      if ((t & 63) == 0) s_top[t / 64] = top;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < WAVES; w++) top = max(top, s_top[w]);
+    }
+    top = max(top, __float_as_uint(sqrtf(a.eps)));
+    if (top < 0x7F800000u) {
+      const float scale = __uint_as_float((uint32_t)min(253, 254 + 31 - (int)(top >> 23)) << 23);
+#pragma unroll
+      for (int j = 0; j < CH; j++) h[j] *= scale;
+      mean = squares(1) / (float)a.H + a.eps * scale * scale;
+    }
   }
-  sum = wave_sum_f32(sum);
-  if constexpr (WAVES > 1) {
-    __shared__ float s_sum[WAVES];
-    if ((t & 63) == 0) s_sum[t / 64] = sum;
-    __syncthreads();
-    sum = 0.f;
-#pragma unroll
-    for (int w = 0; w < WAVES; w++) sum += s_sum[w];
-  }
-  const float r = 1.f / sqrtf(sum / (float)a.H + a.eps);
+  const float r = 1.f / sqrtf(mean);
   auto finish = [&](auto wt) __attribute__((always_inline)) {
 #pragma unroll
     for (int j = 0; j < CH; j++) {
