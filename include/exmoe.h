@@ -468,7 +468,8 @@ int exmoe_lora_linear(const void* x, size_t ldx, const void* w, size_t ldw, cons
  * exmoe_quantize_fp8: q, scale of rows as they are. exmoe_swiglu_fp8: of silu(g) * u in fp32, g the
  * first and u the next n columns of x; with weights (either call), row r's scales are multiplied by
  * weights[row_index[r]] (0 for an index outside [0, n_weights)), or by weights[r] without
- * row_index: a routing weight that the down product then carries to its output.
+ * row_index: a routing weight that the down product then carries to its output. (silu by the
+ * hardware's 2^x and reciprocal: zero from g = -87.4 down, where it is under 2^-119.)
  * exmoe_quantize_fp8_weights: w [E, N, K] with one scale per 128 x 128 block, scale [E,
  * ceil(N / 128), ceil(K / 128)].
  *

@@ -1,7 +1,8 @@
 // Rows and weight matrices as e4m3 values with fp32 scales (fp8.h), gfx950.
 //
 //   rows      v = x[r, :]                              as it is
-//             v = silu(x[r, 0..n)) * x[r, n..2n)       gate and up of an expert layer side by side
+//             v = silu(x[r, 0..n)) * x[r, n..2n)       gate and up of an expert layer side by side (silu is zero
+//                                                      from -87.4 down, as the reciprocal of more than 2^126 is)
 //             scales per row and 128 columns, times the row's routing weight on request: the down
 //             product is linear, so a weight in the scale of its input weights its output
 //   matrices  scales per 128 x 128 block
